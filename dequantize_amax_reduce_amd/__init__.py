@@ -535,3 +535,14 @@ def weight_dequant(x: torch.Tensor, s: torch.Tensor, block_size: int = 128, ret_
     y = torch.empty(x.shape, dtype=ret_type, device=x.device)
     fp8q_weight_dequant_block128(x, s, y)
     return y
+
+
+# ---------------------------------------------------------------------------
+# the feed-forward operators on fp8 operands (include/fp8q_ffn.h)
+# ---------------------------------------------------------------------------
+
+from . import _ffn  # noqa: E402
+
+_ffn._bind(lib, dict(_check=_check, _dev=_dev, _stream=_stream, _hp_dtype=_hp_dtype, _fmt=_fmt, _fp8=_fp8,
+                     _FP8_DTYPE=_FP8_DTYPE))
+globals().update({_n: getattr(_ffn, _n) for _n in _ffn.FFN_NAMES})

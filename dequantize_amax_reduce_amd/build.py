@@ -33,7 +33,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8q.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fp8q_kernels.hip", "fp8q_shift.hip", "fp8q_abi.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fp8q_kernels.hip", "fp8q_shift.hip", "fp8q_abi.cpp",
+                                           "fp8q_norm.hip", "fp8q_mm_fwd.hip", "fp8q_mm_bwd.hip", "fp8q_ffn_abi.cpp")]
 ARCH = "gfx950"
 
 

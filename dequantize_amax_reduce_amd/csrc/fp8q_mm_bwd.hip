@@ -1,0 +1,342 @@
+// fp8q_mm_bwd.hip -- the backward products of the projections.
+//
+//   dg = dp u act'(g), du = dp act(g)         (a projection: dg = dy)
+//   dx = [dg | du] [Wg ; Wu]                  contraction over the columns
+//   [dWg ; dWu] = [dg | du]^T X               contraction over the rows
+//
+// Both products run on one bf16 MFMA kernel (k_mm16) whose operands are
+// contiguous in the contraction, so the operands are laid out first: dz =
+// [dg | du] and its transpose, the transposed dequantized W, and the
+// transposed dequantized X.  These passes move 8-10 bytes per element of the
+// operands (5-8 % of the products' time on square problems); the products
+// then run without a transposing read.  Each operand is rounded to bf16 once,
+// which keeps the range of binary32, so gradients need no scaling.
+// Contractions are padded with zeros to 64 elements.
+#include "fp8q_host.h"
+#include "fp8q_mm.h"
+
+namespace fp8q {
+
+namespace {
+
+struct Mm16Args {
+    const uint16_t* a;     // [M, K] bf16 (row pitch K)
+    const uint16_t* b;     // [N, K] bf16
+    int64_t M;
+    int N, KB;             // KB = K / 64
+    uint32_t tm, tn;
+    void* c0;              // rows [0, split): c0, pitch N
+    void* c1;              // rows [gap, M): c1[row - gap]
+    int64_t split, gap;
+    int cdt, vec;
+};
+
+template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Args a) {
+    constexpr int MT = BM / 32, kStage = (BM + kMmBN) * 128;
+    __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    uint32_t im, in;
+    tile_of(blockIdx.x, a.tm, a.tn, &im, &in);
+    const int64_t m0 = (int64_t)im * BM;
+    const int n0 = (int)in * 256;
+    TileLoad<BM> ld;
+    ld.init(a.a, m0, a.M, a.b, a.b, n0, n0 + 128, a.N, a.N, (int64_t)a.KB * 128, wave, lane);
+    const uint32_t lds0 = lds_offset(smem);
+
+    v4f acc[MT][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) acc[t][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const int col = lane & 15, lr = lane >> 4;
+    const uint32_t c0 = (uint32_t)((lr ^ (col & 7)) * 16), c1 = (uint32_t)(((lr + 4) ^ (col & 7)) * 16);
+    const uint32_t ra = (uint32_t)((wm * (BM / 2) + col) * 128), rb = (uint32_t)((BM + wn * 32 + col) * 128);
+
+    if (a.KB > 0) ld.issue(lds0, 0);
+    for (int kb = 0; kb < a.KB; ++kb) {
+        const int st = kb & 1;
+        dma_wait();
+        wg_barrier();
+        if (kb + 1 < a.KB) ld.issue(lds0 + (st ^ 1) * kStage, kb + 1);
+        const char* s = smem + st * kStage;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t c = h ? c1 : c0;
+            v4i b[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                b[n] = *(const v4i*)(s + rb + (n >> 1) * (128 * 128) + (n & 1) * (16 * 128) + c);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const v4i x = *(const v4i*)(s + ra + t * (16 * 128) + c);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) acc[t][n] = mfma_bf16(b[n], x, acc[t][n]);
+            }
+        }
+    }
+    const int nc = n0 + wn * 32 + lr * 8;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int64_t row = m0 + wm * (BM / 2) + t * 16 + col;
+        void* c;
+        int64_t r;
+        if (row < a.split) { c = a.c0; r = row; }
+        else if (row >= a.gap && row < a.M) { c = a.c1; r = row - a.gap; }
+        else continue;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = acc[t][2 * half + (k >> 2)][k & 3];
+            put8(c, a.cdt, r, a.N, nc + half * 128, a.N, a.vec, v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// operand layout
+// ---------------------------------------------------------------------------
+
+// A 64 (rows) x 64 (columns) tile transposed through LDS as pairs of rows:
+// word [c][i] holds column c of rows 2i and 2i + 1.  The pitch of 33 words
+// spreads both the column-wise writes and the row-wise reads over the banks.
+struct TileT {
+    uint32_t w[64][33];
+};
+
+typedef unsigned int v4u_a2 __attribute__((ext_vector_type(4), aligned(2)));
+
+// 8 elements from column c of a row (zero from column `cols` on)
+template <int DT> __device__ __forceinline__ void ld8(const uint16_t* row, int c, int cols, float* v) {
+    HpVec<DT> t;
+    if (c + 8 <= cols) {
+        const v4u_a2 r = *(const v4u_a2*)(row + c);
+        t.r = v4u{r.x, r.y, r.z, r.w};
+    } else {
+        union { v4u q; uint16_t e[8]; } u;
+        u.q = v4u{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k < cols) u.e[k] = row[c + k];
+        t.r = u.q;
+    }
+    t.widen(v);
+}
+
+// this workgroup's 64 columns of t as rows of dst (pitch `pitch` elements),
+// 64 elements each from element `at`
+__device__ __forceinline__ void store_t(const TileT& t, uint16_t* dst, int64_t pitch, int64_t at) {
+    const int c = (int)threadIdx.x >> 2, q = (int)threadIdx.x & 3;
+    uint16_t* d = dst + c * pitch + at + q * 16;
+    const uint32_t* s = &t.w[c][q * 8];
+    *(v4u*)d = v4u{s[0], s[1], s[2], s[3]};
+    *(v4u*)(d + 8) = v4u{s[4], s[5], s[6], s[7]};
+}
+
+struct DzArgs {
+    const uint16_t* dy;
+    const uint16_t* z;
+    int64_t M, Mp;         // Mp: M padded to 64
+    int N, Np;             // Np: N padded to 64
+    int act;
+    uint16_t* dz;          // [M, gated ? 2 Np : Np], or nullptr
+    uint16_t* dzt;         // [gated ? 2 Np : Np, Mp], or nullptr
+};
+
+// dz and its transpose; 256 threads, one 64 x 64 tile a workgroup; thread
+// (i, v) takes 8 columns of the rows 2i and 2i + 1
+template <int DT, bool GATED> __global__ void __launch_bounds__(256) k_dz(DzArgs a) {
+    __shared__ TileT tg, tu;
+    const int v = (int)threadIdx.x & 7, i = (int)threadIdx.x >> 3;
+    const int64_t m = (int64_t)blockIdx.y * 64 + 2 * i;
+    const int c = (int)blockIdx.x * 64 + v * 8;
+    const int64_t zp = 2 * (int64_t)a.N, dp = GATED ? 2 * (int64_t)a.Np : a.Np;
+    float g[2][8], u[2][8];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[r][k] = u[r][k] = 0.0f;
+        if (m + r < a.M) {
+            ld8<DT>(a.dy + (m + r) * a.N, c, a.N, g[r]);
+            if constexpr (GATED) {
+                float zg[8], zu[8];
+                ld8<DT>(a.z + (m + r) * zp, c, a.N, zg);
+                ld8<DT>(a.z + (m + r) * zp + a.N, c, a.N, zu);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float f, d;
+                    act_both(a.act, zg[k], &f, &d);
+                    u[r][k] = c + k < a.N ? g[r][k] * f : 0.0f;
+                    g[r][k] = c + k < a.N ? g[r][k] * zu[k] * d : 0.0f;
+                }
+            }
+            if (a.dz) {
+                *(v4u*)(a.dz + (m + r) * dp + c) = pack_out16<kBF16>(g[r]);
+                if constexpr (GATED) *(v4u*)(a.dz + (m + r) * dp + a.Np + c) = pack_out16<kBF16>(u[r]);
+            }
+        }
+    }
+    if (!a.dzt) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        tg.w[v * 8 + k][i] = pack_bf16x2(g[0][k], g[1][k]);
+        if constexpr (GATED) tu.w[v * 8 + k][i] = pack_bf16x2(u[0][k], u[1][k]);
+    }
+    __syncthreads();
+    uint16_t* d = a.dzt + (int64_t)blockIdx.x * 64 * a.Mp;
+    store_t(tg, d, a.Mp, (int64_t)blockIdx.y * 64);
+    if constexpr (GATED) store_t(tu, d + (int64_t)a.Np * a.Mp, a.Mp, (int64_t)blockIdx.y * 64);
+}
+
+struct DeqTArgs {
+    const uint8_t* q;
+    const float* s;        // s[(row >> sh) * KB + k / 128]
+    int64_t R;             // rows
+    int KB, sh;
+    uint16_t* t;           // [K, pitch], this matrix from element `at` of a row
+    int64_t pitch, at;
+};
+
+// The transposed dequantized matrix: 64 rows x 128 codes a workgroup; thread
+// (i, v) takes 16 codes of the rows 2i and 2i + 1.  Rows past R are zero.
+template <int FMT> __global__ void __launch_bounds__(256) k_deq_t(DeqTArgs a) {
+    __shared__ TileT t[2];
+    const int v = (int)threadIdx.x & 7, i = (int)threadIdx.x >> 3;
+    const int64_t r0 = (int64_t)blockIdx.y * 64 + 2 * i;
+    const int64_t K = (int64_t)a.KB * 128;
+    float f[2][16];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        if (r0 + r < a.R) {
+            const v4u c = *(const v4u*)(a.q + (r0 + r) * K + (int64_t)blockIdx.x * 128 + v * 16);
+            const float s = a.s[((r0 + r) >> a.sh) * a.KB + blockIdx.x];
+            dec4<FMT>(c.x, f[r]);
+            dec4<FMT>(c.y, f[r] + 4);
+            dec4<FMT>(c.z, f[r] + 8);
+            dec4<FMT>(c.w, f[r] + 12);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) f[r][k] *= s;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) f[r][k] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) t[v >> 2].w[(v & 3) * 16 + k][i] = pack_bf16x2(f[0][k], f[1][k]);
+    __syncthreads();
+    uint16_t* d = a.t + (int64_t)blockIdx.x * 128 * a.pitch;
+    store_t(t[0], d, a.pitch, a.at + (int64_t)blockIdx.y * 64);
+    store_t(t[1], d + 64 * a.pitch, a.pitch, a.at + (int64_t)blockIdx.y * 64);
+}
+
+__global__ void __launch_bounds__(256) k_zero16(uint16_t* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+void zero(void* p, int64_t n, int dt, hipStream_t st) {
+    if (p && n > 0) launch_zero16(p, n * (dt == kF32 ? 2 : 1), st);
+}
+
+int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// c[m, n] = sum_k a[m, k] b[n, k]; rows [0, split) to c0, rows from gap to c1
+void mm16(const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K, void* c0, void* c1, int64_t split,
+          int64_t gap, int cdt, hipStream_t st) {
+    Mm16Args a{A, B, M, (int)N, (int)(K / 64), 0, 0, c0, c1, split, gap, cdt, 0};
+    a.vec = N % 8 == 0 && al(c0, 16) && (!c1 || al(c1, 16));
+    a.tn = (uint32_t)((N + 255) / 256);
+    // the tallest tile that still gives most CUs one
+    int bm = 256;
+    while (bm > 64 && (M + bm - 1) / bm * a.tn < 200) bm /= 2;
+    a.tm = (uint32_t)((M + bm - 1) / bm);
+    const unsigned g = a.tm * a.tn;
+    if (bm == 256) k_mm16<256><<<g, kMmThreads, 0, st>>>(a);
+    else if (bm == 128) k_mm16<128><<<g, kMmThreads, 0, st>>>(a);
+    else k_mm16<64><<<g, kMmThreads, 0, st>>>(a);
+}
+
+template <typename F> void with_fmt(int f, F&& go) {
+    if (f == kE4M3) go(KC<kE4M3>{});
+    else go(KC<kE5M2>{});
+}
+
+void deq_t(const uint8_t* q, int fmt, const float* s, int64_t R, int64_t Rp, int KB, int sh, uint16_t* t, int64_t pitch,
+           int64_t at, hipStream_t st) {
+    const DeqTArgs a{q, s, R, KB, sh, t, pitch, at};
+    const dim3 g((unsigned)KB, (unsigned)(Rp / 64));
+    with_fmt(fmt, [&](auto F) { k_deq_t<decltype(F)::value><<<g, 256, 0, st>>>(a); });
+}
+
+struct BwdLayout {
+    int64_t Mp, Np, C;     // padded rows and columns; C: columns of dz
+    int64_t dz, dzt, wt, xt, bytes;
+};
+BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated) {
+    BwdLayout l;
+    l.Mp = up64(M);
+    l.Np = up64(N);
+    l.C = gated ? 2 * l.Np : l.Np;
+    int64_t at = 0;
+    auto take = [&](int64_t elems) { const int64_t p = at; at += up256(2 * elems); return p; };
+    l.dz = take(M * l.C);
+    l.dzt = take(l.C * l.Mp);
+    l.wt = take(K * l.C);
+    l.xt = take(K * l.Mp);
+    l.bytes = at;
+    return l;
+}
+
+}  // namespace
+
+void launch_zero16(void* p, int64_t n, hipStream_t st) {
+    k_zero16<<<(unsigned)std::min<int64_t>((n + 255) / 256, 65536), 256, 0, st>>>((uint16_t*)p, n);
+}
+
+int64_t mm_bwd_workspace(int64_t M, int64_t N, int64_t K, bool gated) {
+    if (M == 0 || N == 0 || K == 0) return 0;
+    return layout(M, N, K, gated).bytes;
+}
+
+void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
+    const bool gated = f.gated;
+    if (f.M == 0 || f.N == 0 || f.K == 0) {
+        zero(f.dx, f.M * f.K, f.dt, st);
+        zero(f.dw0, (int64_t)f.N * f.K, f.dwdt, st);
+        zero(f.dw1, (int64_t)f.N * f.K, f.dwdt, st);
+        return;
+    }
+    const BwdLayout l = layout(f.M, f.N, f.K, gated);
+    char* ws = (char*)f.ws;
+    uint16_t *dz = (uint16_t*)(ws + l.dz), *dzt = (uint16_t*)(ws + l.dzt), *wt = (uint16_t*)(ws + l.wt),
+             *xt = (uint16_t*)(ws + l.xt);
+    const int KB = f.K / 128;
+    const bool wdx = f.dx != nullptr, wdw = f.dw0 != nullptr;
+    // a bf16 gradient whose rows are whole 128-byte steps is dz already
+    const bool direct = !gated && f.dt == kBF16 && f.N % 64 == 0 && al(f.dy, 16);
+    const DzArgs d{(const uint16_t*)f.dy, (const uint16_t*)f.z, f.M, l.Mp, f.N, (int)l.Np, f.act,
+                   wdx && !direct ? dz : nullptr, wdw ? dzt : nullptr};
+    if (d.dz || d.dzt) {
+        const dim3 g((unsigned)(l.Np / 64), (unsigned)(l.Mp / 64));
+        if (f.dt == kBF16) {
+            if (gated) k_dz<kBF16, true><<<g, 256, 0, st>>>(d);
+            else k_dz<kBF16, false><<<g, 256, 0, st>>>(d);
+        } else {
+            if (gated) k_dz<kF16, true><<<g, 256, 0, st>>>(d);
+            else k_dz<kF16, false><<<g, 256, 0, st>>>(d);
+        }
+    }
+    if (wdx) {
+        deq_t(f.w0, f.wfmt, f.ws0, f.N, l.Np, KB, 7, wt, l.C, 0, st);
+        if (gated) deq_t(f.w1, f.wfmt, f.ws1, f.N, l.Np, KB, 7, wt, l.C, l.Np, st);
+        mm16(direct ? (const uint16_t*)f.dy : dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, st);
+    }
+    if (wdw) {
+        deq_t(f.x, f.xfmt, f.xs, f.M, l.Mp, KB, 0, xt, l.Mp, 0, st);
+        if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, st);
+        else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, st);
+    }
+}
+
+}  // namespace fp8q
