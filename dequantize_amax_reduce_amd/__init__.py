@@ -543,6 +543,5 @@ def weight_dequant(x: torch.Tensor, s: torch.Tensor, block_size: int = 128, ret_
 
 from . import _ffn  # noqa: E402
 
-_ffn._bind(lib, dict(_check=_check, _dev=_dev, _stream=_stream, _hp_dtype=_hp_dtype, _fmt=_fmt, _fp8=_fp8,
-                     _FP8_DTYPE=_FP8_DTYPE))
+_ffn._bind(lib, dict(_check=_check, _dev=_dev, _fmt=_fmt, _fp8=_fp8, _FP8_DTYPE=_FP8_DTYPE, _DT=_DT))
 globals().update({_n: getattr(_ffn, _n) for _n in _ffn.FFN_NAMES})

@@ -62,13 +62,43 @@ def ffn_header_functions() -> list:
 
 
 # set by the package once its own marshalling helpers exist
-lib = _check = _dev = _stream = _hp_dtype = _fmt = _fp8 = _FP8_DTYPE = None
+lib = _check = _dev = _fmt = _fp8 = _FP8_DTYPE = _DT = None
 
 
 def _bind(package_lib, helpers):
     global lib
     lib = load_ffn(package_lib)
     globals().update(helpers)
+
+
+# A call on one token is bound by its host time, so the marshalling asks each
+# tensor as little as it can (about 0.25 us a tensor against 0.7 us for _dev).
+
+def _ptr(t, name) -> int:
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dev(t, name)                                # raises, or 0 for an empty tensor
+
+
+# the raw handle of a device's current stream; torch.cuda.current_stream costs 2 us more
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _stream(t, stream):
+    if stream is None:
+        return _raw_stream(t.get_device()) if t.is_cuda else None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _hp_dtype(t, name) -> int:
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name}: only float32, bfloat16 and float16 are supported (got {t.dtype})")
+    return dt
 
 
 def _act(name) -> int:
@@ -78,13 +108,13 @@ def _act(name) -> int:
 
 
 def _opt(t, name):
-    return 0 if t is None else _dev(t, name)
+    return 0 if t is None else _ptr(t, name)
 
 
 def _f32(t, numel, name):
     if t.dtype != torch.float32 or t.numel() != numel:
         raise ValueError(f"{name} must be float32 with {numel} elements")
-    return _dev(t, name)
+    return _ptr(t, name)
 
 
 def _flat(t, name):
@@ -106,25 +136,26 @@ def _same(t, shape, dtype, name):
     return t
 
 
-def _ws(t, need, name):
+_AUTO = object()                                        # the helpers' workspaces: allocated within the call
+
+
+def _ws(t, need, like, name):
+    """The workspace tensor of a call (the caller keeps it until the call has
+    been enqueued), or None where none is needed."""
     if need == 0:
-        return 0
+        return None
+    if t is _AUTO:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
     if t is None or t.numel() * t.element_size() < need:
         raise ValueError(f"{name}: the workspace needs {need} bytes")
-    return _dev(t, "workspace")
-
-
-def _new_ws(need, device):
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    return t
 
 
 def _x_codes(x, xs, name):
     """(pointer, format, scale pointer), rows, K of an activation"""
     f = _fp8(x, None, "x")
     M, K = _flat(x, "x")
-    if K % 128 == 0:
-        _f32(xs, M * (K // 128), "x_scale_inv")
-    return (_dev(x, "x"), f, _dev(xs, "x_scale_inv")), M, K
+    return (_ptr(x, "x"), f, _f32(xs, M * (K // 128), "x_scale_inv")), M, K
 
 
 def _w_codes(w, ws, K, name):
@@ -133,9 +164,7 @@ def _w_codes(w, ws, K, name):
     if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"{name} must be 2-D with {K} columns")
     N = w.shape[0]
-    if K % 128 == 0:
-        _f32(ws, ((N + 127) // 128) * (K // 128), name + "_scale_inv")
-    return _dev(w, name), f, _dev(ws, name + "_scale_inv"), N
+    return _ptr(w, name), f, _f32(ws, ((N + 127) // 128) * (K // 128), "the weight's scale_inv"), N
 
 
 def _pair(w_gate, gs, w_up, us, K):
@@ -156,17 +185,17 @@ def _norm(name, x, weight, q, scale_inv, residual, h, rstd, eps, fmt, stream):
     dt = _hp_dtype(x, "x")
     if q.numel() != x.numel() or weight.numel() != cols:
         raise ValueError(f"{name}: q must match x and weight must have x's last dimension")
-    for t, n in ((residual, "residual"), (h, "h")):
-        _same(t, (rows, cols), x.dtype, n)
-    if rstd is not None:
-        _f32(rstd, rows, "rstd")
-    if name.endswith("per_channel"):
-        _f32(scale_inv, rows, "scale_inv")
-    elif cols % 128 == 0:
-        _f32(scale_inv, rows * (cols // 128), "scale_inv")
-    _check(getattr(lib, name)(_dev(x, "x"), dt, _opt(residual, "residual"), _dev(weight, "weight"),
-                              _hp_dtype(weight, "weight"), rows, cols, eps, f, _dev(q, "q"),
-                              _dev(scale_inv, "scale_inv"), _opt(h, "h"), _opt(rstd, "rstd"), _stream(x, stream)), name)
+    if residual is not None:
+        _same(residual, (rows, cols), x.dtype, "residual")
+    if h is not None:
+        _same(h, (rows, cols), x.dtype, "h")
+    scales = rows if name == "fp8q_rmsnorm_cast_per_channel" else rows * (cols // 128)
+    st = getattr(lib, name)(_ptr(x, "x"), dt, 0 if residual is None else _ptr(residual, "residual"),
+                            _ptr(weight, "weight"), _hp_dtype(weight, "weight"), rows, cols, eps, f, _ptr(q, "q"),
+                            _f32(scale_inv, scales, "scale_inv"), 0 if h is None else _ptr(h, "h"),
+                            0 if rstd is None else _f32(rstd, rows, "rstd"), _stream(x, stream))
+    if st:
+        _check(st, name)
 
 
 def fp8q_rmsnorm_cast_group128(x, weight, q, scale_inv, residual=None, h=None, rstd=None, eps=1e-6, fmt="e4m3fn",
@@ -193,10 +222,11 @@ def fp8q_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, worksp
     if dweight is not None and (dweight.numel() != cols or dweight.dtype != weight.dtype):
         raise ValueError("fp8q_rmsnorm_backward: dweight must match weight")
     need = lib.fp8q_rmsnorm_backward_workspace_bytes(rows, cols) if dweight is not None else 0
-    _check(lib.fp8q_rmsnorm_backward(_dev(dy, "dy"), _dev(h, "h"), dt, _dev(weight, "weight"),
+    ws = _ws(workspace, need, h, "fp8q_rmsnorm_backward")
+    _check(lib.fp8q_rmsnorm_backward(_ptr(dy, "dy"), _ptr(h, "h"), dt, _ptr(weight, "weight"),
                                      _hp_dtype(weight, "weight"), _f32(rstd, rows, "rstd"), _opt(dh, "dh"), rows, cols,
-                                     _dev(dx, "dx"), _opt(dweight, "dweight"),
-                                     _ws(workspace, need, "fp8q_rmsnorm_backward"), _stream(h, stream)),
+                                     _ptr(dx, "dx"), _opt(dweight, "dweight"),
+                                     _opt(ws, "workspace"), _stream(h, stream)),
            "fp8q_rmsnorm_backward")
 
 
@@ -208,8 +238,8 @@ def fp8q_linear(x, x_scale_inv, w, w_scale_inv, y, workspace=None, stream=None) 
     xa, M, K = _x_codes(x, x_scale_inv, "x")
     wp, wf, wsp, N = _w_codes(w, w_scale_inv, K, "w")
     _same(y, (M, N), y.dtype, "y")
-    _check(lib.fp8q_linear(*xa, wp, wf, wsp, M, N, K, _dev(y, "y"), _hp_dtype(y, "y"),
-                           _ws(workspace, lib.fp8q_linear_workspace_bytes(M, N, K), "fp8q_linear"),
+    scratch = _ws(workspace, lib.fp8q_linear_workspace_bytes(M, N, K), x, "fp8q_linear")
+    _check(lib.fp8q_linear(*xa, wp, wf, wsp, M, N, K, _ptr(y, "y"), _hp_dtype(y, "y"), _opt(scratch, "workspace"),
                            _stream(x, stream)), "fp8q_linear")
 
 
@@ -234,8 +264,9 @@ def fp8q_linear_backward(dy, x, x_scale_inv, w, w_scale_inv, dx=None, dw=None, w
         _same(dw, (N, K), dw.dtype, "dw")
     gdt = dt if dw is None else _hp_dtype(dw, "dw")
     need = lib.fp8q_linear_backward_workspace_bytes(M, N, K)
-    _check(lib.fp8q_linear_backward(_dev(dy, "dy"), dt, *xa, wp, wf, wsp, M, N, K, _opt(dx, "dx"), _opt(dw, "dw"), gdt,
-                                    _ws(workspace, need, "fp8q_linear_backward"), _stream(x, stream)),
+    scratch = _ws(workspace, need, x, "fp8q_linear_backward")
+    _check(lib.fp8q_linear_backward(_ptr(dy, "dy"), dt, *xa, wp, wf, wsp, M, N, K, _opt(dx, "dx"), _opt(dw, "dw"), gdt,
+                                    _opt(scratch, "workspace"), _stream(x, stream)),
            "fp8q_linear_backward")
 
 
@@ -247,7 +278,7 @@ def _z_arg(z, M, F):
     if z is None:
         return 0, 0
     _same(z, (M, 2 * F), z.dtype, "z")
-    return _dev(z, "z"), _hp_dtype(z, "z")
+    return _ptr(z, "z"), _hp_dtype(z, "z")
 
 
 def fp8q_gated_linear(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, h, z=None, activation="silu",
@@ -256,8 +287,9 @@ def fp8q_gated_linear(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale
     pair, F = _pair(w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, K)
     _same(h, (M, F), h.dtype, "h")
     need = lib.fp8q_gated_linear_workspace_bytes(M, F, K, 0)
-    _check(lib.fp8q_gated_linear(*xa, *pair, M, F, K, _act(activation), _dev(h, "h"), _hp_dtype(h, "h"),
-                                 *_z_arg(z, M, F), _ws(workspace, need, "fp8q_gated_linear"), _stream(x, stream)),
+    scratch = _ws(workspace, need, x, "fp8q_gated_linear")
+    _check(lib.fp8q_gated_linear(*xa, *pair, M, F, K, _act(activation), _ptr(h, "h"), _hp_dtype(h, "h"),
+                                 *_z_arg(z, M, F), _opt(scratch, "workspace"), _stream(x, stream)),
            "fp8q_gated_linear")
 
 
@@ -271,9 +303,10 @@ def fp8q_gated_linear_cast(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_
     if F % 128 == 0:
         _f32(scale_inv, M * (F // 128), "scale_inv")
     need = lib.fp8q_gated_linear_workspace_bytes(M, F, K, 1)
-    _check(lib.fp8q_gated_linear_cast(*xa, *pair, M, F, K, _act(activation), f, _dev(q, "q"),
-                                      _dev(scale_inv, "scale_inv"), *_z_arg(z, M, F),
-                                      _ws(workspace, need, "fp8q_gated_linear_cast"), _stream(x, stream)),
+    scratch = _ws(workspace, need, x, "fp8q_gated_linear_cast")
+    _check(lib.fp8q_gated_linear_cast(*xa, *pair, M, F, K, _act(activation), f, _ptr(q, "q"),
+                                      _ptr(scale_inv, "scale_inv"), *_z_arg(z, M, F),
+                                      _opt(scratch, "workspace"), _stream(x, stream)),
            "fp8q_gated_linear_cast")
 
 
@@ -295,9 +328,10 @@ def fp8q_gated_linear_backward(dp, z, x, x_scale_inv, w_gate, w_gate_scale_inv, 
     g = _grad_dtype((dw_gate, dw_up))
     gdt = dt if g is None else _hp_dtype(dw_gate if dw_gate is not None else dw_up, "dw")
     need = lib.fp8q_gated_linear_backward_workspace_bytes(M, F, K)
-    _check(lib.fp8q_gated_linear_backward(_dev(dp, "dp"), _dev(z, "z"), dt, *xa, *pair, M, F, K, _act(activation),
+    scratch = _ws(workspace, need, x, "fp8q_gated_linear_backward")
+    _check(lib.fp8q_gated_linear_backward(_ptr(dp, "dp"), _ptr(z, "z"), dt, *xa, *pair, M, F, K, _act(activation),
                                           _opt(dx, "dx"), _opt(dw_gate, "dw_gate"), _opt(dw_up, "dw_up"), gdt,
-                                          _ws(workspace, need, "fp8q_gated_linear_backward"), _stream(x, stream)),
+                                          _opt(scratch, "workspace"), _stream(x, stream)),
            "fp8q_gated_linear_backward")
 
 
@@ -328,34 +362,28 @@ def rmsnorm_cast(x, weight, residual=None, eps=1e-6, fp8_format="e4m3fn", per_ch
 def rmsnorm_cast_backward(dy, h, weight, rstd, dh=None, out=None):
     """(dx, dweight) of rmsnorm_cast; dx is the gradient of x and of the
     residual.  dh: the gradient that reaches h along the residual path."""
-    rows, cols = _flat(h, "h")
     dx, dw = out if out is not None else (torch.empty_like(h), torch.empty_like(weight))
-    ws = _new_ws(lib.fp8q_rmsnorm_backward_workspace_bytes(rows, cols), h.device)
-    fp8q_rmsnorm_backward(dy, h, weight, rstd, dx, dw, dh, ws)
+    fp8q_rmsnorm_backward(dy, h, weight, rstd, dx, dw, dh, _AUTO)
     return dx, dw
 
 
 def linear_fp8(x, x_scale_inv, w, w_scale_inv, ret_type=torch.bfloat16, out=None):
     """y = X W^T for codes x [..., K] with scales per 128-group and w [N, K]
     with scales per 128x128 block."""
-    M, K = _flat(x, "x")
-    N = w.shape[0]
-    y = out if out is not None else torch.empty((*x.shape[:-1], N), dtype=ret_type, device=x.device)
-    fp8q_linear(x, x_scale_inv, w, w_scale_inv, y, _new_ws(lib.fp8q_linear_workspace_bytes(M, N, K), x.device))
+    y = out if out is not None else torch.empty((*x.shape[:-1], w.shape[0]), dtype=ret_type, device=x.device)
+    fp8q_linear(x, x_scale_inv, w, w_scale_inv, y, _AUTO)
     return y
 
 
 def linear_fp8_backward(dy, x, x_scale_inv, w, w_scale_inv, grad_type=None, out=None):
     """(dx, dw) of linear_fp8, dx in dy's dtype (bf16 or f16), dw in grad_type
     (dy's dtype by default, or float32)."""
-    M, K = _flat(x, "x")
     if out is not None:
         dx, dw = out
     else:
         dx = torch.empty(x.shape, dtype=dy.dtype, device=x.device)
         dw = torch.empty(w.shape, dtype=grad_type or dy.dtype, device=x.device)
-    ws = _new_ws(lib.fp8q_linear_backward_workspace_bytes(M, w.shape[0], K), x.device)
-    fp8q_linear_backward(dy, x, x_scale_inv, w, w_scale_inv, dx, dw, ws)
+    fp8q_linear_backward(dy, x, x_scale_inv, w, w_scale_inv, dx, dw, _AUTO)
     return dx, dw
 
 
@@ -363,15 +391,13 @@ def gated_linear_fp8(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_
                      ret_type=torch.bfloat16, keep=None, out=None):
     """(h, z): h = act(X Wg^T) * (X Wu^T) in ret_type; z [..., 2F] holds both
     products in `keep`'s dtype for the backward pass, or is None."""
-    M, K = _flat(x, "x")
     F = w_gate.shape[0]
     if out is not None:
         h, z = out
     else:
         h = torch.empty((*x.shape[:-1], F), dtype=ret_type, device=x.device)
         z = None if keep is None else torch.empty((*x.shape[:-1], 2 * F), dtype=keep, device=x.device)
-    ws = _new_ws(lib.fp8q_gated_linear_workspace_bytes(M, F, K, 0), x.device)
-    fp8q_gated_linear(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, h, z, activation, ws)
+    fp8q_gated_linear(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, h, z, activation, _AUTO)
     return h, z
 
 
@@ -379,17 +405,15 @@ def gated_linear_fp8_cast(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_s
                           fp8_format="e4m3fn", keep=None, out=None):
     """(q, scale_inv, z): gated_linear_fp8's product cast to fp8 per 128-group
     (F % 128 == 0) without a 16-bit copy in between, and z as there."""
-    M, K = _flat(x, "x")
     F = w_gate.shape[0]
     if out is not None:
         q, s, z = out
     else:
         q = torch.empty((*x.shape[:-1], F), dtype=_FP8_DTYPE[_fmt(fp8_format)], device=x.device)
-        s = torch.empty((M, F // 128), dtype=torch.float32, device=x.device)
+        s = torch.empty((_flat(x, "x")[0], F // 128), dtype=torch.float32, device=x.device)
         z = None if keep is None else torch.empty((*x.shape[:-1], 2 * F), dtype=keep, device=x.device)
-    ws = _new_ws(lib.fp8q_gated_linear_workspace_bytes(M, F, K, 1), x.device)
     fp8q_gated_linear_cast(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, q, s, z, activation,
-                           fp8_format, ws)
+                           fp8_format, _AUTO)
     return q, s, z
 
 
@@ -397,17 +421,14 @@ def gated_linear_fp8_backward(dp, z, x, x_scale_inv, w_gate, w_gate_scale_inv, w
                               activation="silu", grad_type=None, out=None):
     """(dx, dw_gate, dw_up) from dp, the gradient of the product, and the
     forward's z; dtypes as in linear_fp8_backward."""
-    M, K = _flat(x, "x")
-    F = w_gate.shape[0]
     if out is not None:
         dx, dg, du = out
     else:
         dx = torch.empty(x.shape, dtype=dp.dtype, device=x.device)
         dg = torch.empty(w_gate.shape, dtype=grad_type or dp.dtype, device=x.device)
         du = torch.empty(w_up.shape, dtype=grad_type or dp.dtype, device=x.device)
-    ws = _new_ws(lib.fp8q_gated_linear_backward_workspace_bytes(M, F, K), x.device)
     fp8q_gated_linear_backward(dp, z, x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, dx, dg, du,
-                               activation, ws)
+                               activation, _AUTO)
     return dx, dg, du
 
 

@@ -53,8 +53,13 @@ __device__ __forceinline__ void lds_dma4(uint32_t lds, uint32_t voff, const void
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base)
                  : "memory");
 }
-// this wave's LDS loads have landed and its LDS reads have returned
-__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void lds_dma4_at(uint32_t lds, const void* addr) {   // a lane's own address
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(addr) : "memory");
+}
+// all but this wave's N newest LDS loads have landed, and its LDS reads have returned
+template <int N = 0> __device__ __forceinline__ void dma_wait() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void wg_barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -145,6 +150,12 @@ template <int BM> struct TileLoad {
 // two 16-byte chunks of LDS as one fragment
 __device__ __forceinline__ v8i frag(const char* p0, const char* p1) {
     const v4i a = *(const v4i*)p0, b = *(const v4i*)p1;
+    return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
+// the same from memory, for data read once
+__device__ __forceinline__ v8i frag_nt(const char* p0, const char* p1) {
+    const v4i a = __builtin_nontemporal_load((const v4i*)p0), b = __builtin_nontemporal_load((const v4i*)p1);
     return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 

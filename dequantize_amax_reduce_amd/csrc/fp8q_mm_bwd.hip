@@ -54,27 +54,49 @@ template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Ar
     const uint32_t c0 = (uint32_t)((lr ^ (col & 7)) * 16), c1 = (uint32_t)(((lr + 4) ^ (col & 7)) * 16);
     const uint32_t ra = (uint32_t)((wm * (BM / 2) + col) * 128), rb = (uint32_t)((BM + wn * 32 + col) * 128);
 
-    if (a.KB > 0) ld.issue(lds0, 0);
-    for (int kb = 0; kb < a.KB; ++kb) {
-        const int st = kb & 1;
-        dma_wait();
+    // Two halves of 32 elements a step, each half's fragments read while the
+    // other half's MFMAs run.  The barrier sits between the halves: by then a
+    // step's fragments are all in registers, so its buffer takes the tiles of
+    // the step after next, which have a whole step to arrive.
+    struct Half {
+        v4i b[4], x[MT];
+    } f0, f1;
+    auto read = [&](Half& f, const char* s, uint32_t c) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) f.b[n] = *(const v4i*)(s + rb + (n >> 1) * (128 * 128) + (n & 1) * (16 * 128) + c);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) f.x[t] = *(const v4i*)(s + ra + t * (16 * 128) + c);
+    };
+    auto mul = [&](const Half& f) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) acc[t][n] = mfma_bf16(f.b[n], f.x[t], acc[t][n]);
+    };
+    auto step = [&](int kb, auto NEXT, auto LOAD) {
+        const char* s = smem + (kb & 1) * kStage;
+        read(f1, s, c1);
+        __builtin_amdgcn_sched_barrier(0);
+        mul(f0);
+        __builtin_amdgcn_sched_barrier(0);
+        dma_wait<0>();
         wg_barrier();
-        if (kb + 1 < a.KB) ld.issue(lds0 + (st ^ 1) * kStage, kb + 1);
-        const char* s = smem + st * kStage;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t c = h ? c1 : c0;
-            v4i b[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-                b[n] = *(const v4i*)(s + rb + (n >> 1) * (128 * 128) + (n & 1) * (16 * 128) + c);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const v4i x = *(const v4i*)(s + ra + t * (16 * 128) + c);
-#pragma unroll
-                for (int n = 0; n < 4; ++n) acc[t][n] = mfma_bf16(b[n], x, acc[t][n]);
-            }
-        }
+        if constexpr (decltype(LOAD)::value) ld.issue(lds0 + (kb & 1) * kStage, kb + 2);
+        if constexpr (decltype(NEXT)::value) read(f0, smem + ((kb & 1) ^ 1) * kStage, c0);
+        __builtin_amdgcn_sched_barrier(0);
+        mul(f1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (a.KB > 0) {
+        ld.issue(lds0, 0);
+        dma_wait<0>();
+        wg_barrier();
+        if (a.KB > 1) ld.issue(lds0 + kStage, 1);
+        read(f0, smem, c0);
+        int kb = 0;
+        for (; kb < a.KB - 2; ++kb) step(kb, std::true_type{}, std::true_type{});
+        if (kb < a.KB - 1) step(kb++, std::true_type{}, std::false_type{});
+        step(kb, std::false_type{}, std::false_type{});
     }
     const int nc = n0 + wn * 32 + lr * 8;
 #pragma unroll

@@ -37,9 +37,13 @@ struct FwdArgs {
     float* part;           // [splits][M][gated ? 2 N : N]
 };
 
+// LDS of one step: the tiles, then 64 floats a wave: the scales of BM / 8
+// rows of A and, in the last two, of the halves of B
 template <int BM> struct FwdLds {
-    static constexpr int kStage = (BM + kMmBN) * 128 + BM * 4;
-    static constexpr int kStages = 2;
+    static constexpr int kS = (BM + kMmBN) * 128;
+    static constexpr int kStage = kS + 8 * 256;
+    static constexpr int kStages = BM == 256 ? 2 : 3;
+    static constexpr int kPer = BM / 64 + 4 + 1;            // loads a wave issues for a step
 };
 
 // group-cast epilogue: the amax of a token's 128 columns is over a lane's 8
@@ -102,21 +106,22 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
     TileLoad<BM> ld;
     ld.init(a.x, m0, a.M, a.w0, gated ? a.w1 : a.w0, n0, n1, a.N, a.N, (int64_t)a.KB * 128, wave, lane);
     const uint32_t lds0 = lds_offset(smem);
-    // scales of A: lane l of wave w < BM / 64 brings row 64 w + l
-    uint32_t vs = 0;
-    {
-        int64_t r = wave * 64 + lane;
+    // Scales through LDS like the tiles (a load into a register inside the
+    // loop would wait for every tile load issued before it): lanes below BM / 8
+    // bring the wave's rows of A, the last two the halves of B.
+    const float* sp;
+    if (lane < 62) {
+        int64_t r = wave * (BM / 8) + (lane < BM / 8 ? lane : 0);
         if (r > a.M - 1 - m0) r = a.M - 1 - m0;
-        vs = (uint32_t)(r * a.KB * 4);
+        sp = a.xs + (m0 + r) * a.KB;
+    } else {
+        sp = lane == 62 ? a.ws0 + (int64_t)(n0 >> 7) * a.KB
+                        : (gated ? a.ws1 : a.ws0) + (int64_t)(min(n1, a.N - 1) >> 7) * a.KB;
     }
-    const char* xs = (const char*)(a.xs + m0 * a.KB);
-    const float* sw0 = a.ws0 + (int64_t)(n0 >> 7) * a.KB;
-    const float* sw1 = (gated ? a.ws1 : a.ws0) + (int64_t)(min(n1, ((a.N - 1) >> 7) << 7) >> 7) * a.KB;
-
-    auto issue = [&](int kb, int stage) {
-        const uint32_t s = lds0 + stage * L::kStage;
+    auto issue = [&](int kb, int buf) {
+        const uint32_t s = lds0 + buf * L::kStage;
         ld.issue(s, kb);
-        if (wave < BM / 64) lds_dma4(s + (BM + kMmBN) * 128 + wave * 256, vs, xs + (int64_t)kb * 4);
+        lds_dma4_at(s + L::kS + wave * 256, sp + kb);
     };
 
     v4f acc[MT][4];
@@ -128,34 +133,56 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
     const int col = lane & 15, lr = lane >> 4;
     const uint32_t c0 = (uint32_t)((lr ^ (col & 7)) * 16), c1 = (uint32_t)(((lr + 4) ^ (col & 7)) * 16);
     const uint32_t ra = (uint32_t)((wm * (BM / 2) + col) * 128), rb = (uint32_t)((BM + wn * 32 + col) * 128);
+    // row r of A: scale r % (BM / 8) of wave r / (BM / 8)
+    const uint32_t rs = (uint32_t)(L::kS + wm * 1024 + (BM == 64 ? (col >> 3) * 256 + (col & 7) * 4 : col * 4));
+    auto scale_at = [&](int t) { return rs + (BM == 256 ? (t >> 1) * 256 + (t & 1) * 64 : t * (BM == 128 ? 256 : 512)); };
 
-    if (kb0 < kb1) issue(kb0, 0);
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const int st = (kb - kb0) & 1;
-        dma_wait();
-        wg_barrier();
-        if (kb + 1 < kb1) issue(kb + 1, st ^ 1);
-        const char* s = smem + st * L::kStage;
-        v8i b[4];
-        v4i bw[4][4];
+    // A step reads its fragments PF row tiles ahead of their MFMAs.  Its
+    // barrier comes when the last of them are in registers: the step's buffer
+    // is free then and takes the tiles of the step ST later, and the first
+    // fragments of the next step are read behind the step's last MFMAs.
+    // The tallest tile has no registers for the next B beside its own, and reads
+    // it after the step's last MFMA.
+    constexpr int ST = L::kStages, PF = MT >= 4 ? 2 : 1;
+    constexpr bool BLATE = BM == 256;
+    v8i b[4], bn[4], x[MT + PF];                            // x[MT ..): the next step's first
+    auto read_b = [&](v8i (&d)[4], const char* s) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const char* p = s + rb + (n >> 1) * (128 * 128) + (n & 1) * (16 * 128);
-            b[n] = frag(p + c0, p + c1);
-            if constexpr (EX) widen_codes<WF>(b[n], bw[n]);
+            d[n] = frag(p + c0, p + c1);
         }
-        const float s0 = sw0[kb], s1 = sw1[kb];
-        const float* sx = (const float*)(s + (BM + kMmBN) * 128) + wm * (BM / 2) + col;
+    };
+    auto read_x = [&](const char* s, int t) { return frag(s + ra + t * (16 * 128) + c0, s + ra + t * (16 * 128) + c1); };
+    int buf = 0;
+    auto step = [&](int kb, auto NEXT, auto LOAD) {
+        const char* s = smem + buf * L::kStage;
+        const int nbuf = buf + 1 == ST ? 0 : buf + 1;
+        float sx[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) sx[t] = *(const float*)(s + scale_at(t));
+        const float s0 = *(const float*)(s + L::kS + 62 * 4), s1 = *(const float*)(s + L::kS + 63 * 4);
+        v4i bw[4][4];
+        if constexpr (EX)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) widen_codes<WF>(b[n], bw[n]);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const char* p = s + ra + t * (16 * 128);
-            const v8i x = frag(p + c0, p + c1);
-            const float sc = sx[t * 16];
-            const float f0 = sc * s0, f1 = sc * s1;
+            if (t + PF < MT) x[t + PF] = read_x(s, t + PF);
+            if (t == MT - PF) {
+                if constexpr (decltype(LOAD)::value) dma_wait<(ST - 2) * L::kPer>();
+                else dma_wait<0>();
+                wg_barrier();
+                if constexpr (decltype(LOAD)::value) issue(kb + ST, buf);
+                if constexpr (decltype(NEXT)::value && !BLATE) read_b(bn, smem + nbuf * L::kStage);
+            }
+            if constexpr (decltype(NEXT)::value)
+                if (t >= MT - PF) x[t + PF] = read_x(smem + nbuf * L::kStage, t + PF - MT);
+            const float f0 = sx[t] * s0, f1 = sx[t] * s1;
             v4f r[4];
             if constexpr (EX) {
                 v4i xw[4];
-                widen_codes<XF>(x, xw);
+                widen_codes<XF>(x[t], xw);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) r[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -164,8 +191,10 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
                     for (int n = 0; n < 4; ++n) r[n] = mfma_bf16(bw[n][k], xw[k], r[n]);
             } else {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) r[n] = mfma_fp8<WF, XF>(b[n], x);
+                for (int n = 0; n < 4; ++n) r[n] = mfma_fp8<WF, XF>(b[n], x[t]);
             }
+            if constexpr (decltype(NEXT)::value && BLATE)
+                if (t == MT - 1) read_b(b, smem + nbuf * L::kStage);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float f = n < 2 ? f0 : f1;
@@ -173,6 +202,28 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
                 for (int i = 0; i < 4; ++i) acc[t][n][i] = __builtin_fmaf(r[n][i], f, acc[t][n][i]);
             }
         }
+        if constexpr (decltype(NEXT)::value) {
+            if constexpr (!BLATE)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) b[n] = bn[n];
+#pragma unroll
+            for (int t = 0; t < PF; ++t) x[t] = x[MT + t];
+        }
+        buf = nbuf;
+    };
+    if (kb0 < kb1) {
+        const int first = min(ST, kb1 - kb0);
+        for (int i = 0; i < first; ++i) issue(kb0 + i, i);
+        if (first == ST) dma_wait<(ST - 1) * L::kPer>();
+        else dma_wait<0>();
+        wg_barrier();
+        read_b(b, smem);
+#pragma unroll
+        for (int t = 0; t < PF; ++t) x[t] = read_x(smem, t);
+        int kb = kb0;
+        for (; kb < kb1 - ST; ++kb) step(kb, std::true_type{}, std::true_type{});
+        for (; kb < kb1 - 1; ++kb) step(kb, std::true_type{}, std::false_type{});
+        step(kb, std::false_type{}, std::false_type{});
     }
 
     const int nc = n0 + wn * 32 + lr * 8;                  // this lane's 8 columns of the first half
@@ -276,9 +327,10 @@ __global__ void __launch_bounds__(256) k_mm_join(JoinArgs a) {
 // every 8th block of K each, straight from memory to registers: nothing is
 // read twice by a workgroup, and the eight waves' loads cover 1 KB runs of
 // each weight row.  The waves' sums meet in LDS in a fixed order.
-template <int XF, int WF, int MT, int NT, bool GATED> __global__ void __launch_bounds__(512) k_mm_rows(FwdArgs a, float* pbuf) {
+template <int XF, int WF, int MT, int NT, bool GATED, int NW>
+__global__ void __launch_bounds__(64 * NW) k_mm_rows(FwdArgs a, float* pbuf) {
     constexpr int H = GATED ? 2 : 1, BT = NT * H;           // MFMA tiles of weights a wave holds
-    __shared__ __attribute__((aligned(16))) float red[8][BT][MT][64][4];
+    __shared__ __attribute__((aligned(16))) float red[NW][BT][MT][64][4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, lr = lane >> 4;
@@ -308,34 +360,47 @@ template <int XF, int WF, int MT, int NT, bool GATED> __global__ void __launch_b
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[j][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int kb = wave; kb < a.KB; kb += 8) {
+    struct Block {
         v8i w[BT], x[MT];
         float sx[MT];
+    };
+    auto load = [&](Block& b, int kb) {
 #pragma unroll
-        for (int j = 0; j < BT; ++j) w[j] = frag((const char*)wp[j] + kb * 128, (const char*)wp[j] + kb * 128 + 64);
+        for (int j = 0; j < BT; ++j) b.w[j] = frag_nt((const char*)wp[j] + kb * 128, (const char*)wp[j] + kb * 128 + 64);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            x[t] = frag((const char*)xp[t] + kb * 128, (const char*)xp[t] + kb * 128 + 64);
-            sx[t] = sp[t][kb];
+            b.x[t] = frag((const char*)xp[t] + kb * 128, (const char*)xp[t] + kb * 128 + 64);
+            b.sx[t] = sp[t][kb];
         }
+    };
+    auto mul = [&](const Block& b, int kb) {
         const float f0 = s0[kb], f1 = s1[kb];
-        v4i xw[MT][4];
+        v4i ww[BT][4];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) widen_codes<XF>(x[t], xw[t]);
+        for (int j = 0; j < BT; ++j) widen_codes<WF>(b.w[j], ww[j]);
 #pragma unroll
-        for (int j = 0; j < BT; ++j) {
-            v4i ww[4];
-            widen_codes<WF>(w[j], ww);
+        for (int t = 0; t < MT; ++t) {
+            v4i xw[4];
+            widen_codes<XF>(b.x[t], xw);
+            v4f r[BT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                v4f r = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < BT; ++j) r[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) r = mfma_bf16(ww[k], xw[t][k], r);
-                const float f = sx[t] * (j < NT ? f0 : f1);
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[j][t][i] = __builtin_fmaf(r[i], f, acc[j][t][i]);
+                for (int j = 0; j < BT; ++j) r[j] = mfma_bf16(ww[j][k], xw[k], r[j]);
+#pragma unroll
+            for (int j = 0; j < BT; ++j) {
+                const float f = b.sx[t] * (j < NT ? f0 : f1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][t][i] = __builtin_fmaf(r[j][i], f, acc[j][t][i]);
             }
         }
+    };
+    for (int kb = wave; kb < a.KB; kb += NW) {
+        Block b;
+        load(b, kb);
+        mul(b, kb);
     }
 #pragma unroll
     for (int j = 0; j < BT; ++j)
@@ -343,14 +408,14 @@ template <int XF, int WF, int MT, int NT, bool GATED> __global__ void __launch_b
         for (int t = 0; t < MT; ++t) *(v4f*)red[wave][j][t][lane] = acc[j][t];
     __syncthreads();
     // outputs: NT x MT tiles of 16 x 16; n fastest
-    for (int i = threadIdx.x; i < NT * MT * 256; i += 512) {
+    for (int i = threadIdx.x; i < NT * MT * 256; i += 64 * NW) {
         const int nl = i % (NT * 16), m = i / (NT * 16);
         const int j = nl >> 4, n = n0 + nl;
         if (m >= a.M || n >= a.N) continue;
         const int l = (m & 15) + ((nl & 15) >> 2) * 16, e = nl & 3, t = m >> 4;
         float g = 0.0f, u = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) {
+        for (int w = 0; w < NW; ++w) {
             g += red[w][j][t][l][e];
             if constexpr (GATED) u += red[w][NT * (H - 1) + j][t][l][e];
         }
@@ -374,6 +439,7 @@ template <int XF, int WF, int MT, int NT, bool GATED> __global__ void __launch_b
 // ---------------------------------------------------------------------------
 
 constexpr int64_t kRowsMax = 64;       // rows that k_mm_rows takes
+constexpr int NTV = 2, NWV = 16;
 
 // How a product is tiled: rows a tile, and workgroups over K (splits)
 struct Plan {
@@ -412,14 +478,15 @@ int64_t part_bytes(const Plan& p, int64_t M, int64_t N, bool gated) {
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 template <int XF, int WF> void run_rows(const FwdArgs& a, float* pbuf, bool gated, hipStream_t st) {
-    auto go = [&](auto MTc) {
-        constexpr int MT = decltype(MTc)::value, NT = MT >= 4 ? 2 : 1;
-        if (gated) k_mm_rows<XF, WF, MT, NT, true><<<(a.N + 16 * NT - 1) / (16 * NT), 512, 0, st>>>(a, pbuf);
-        else k_mm_rows<XF, WF, MT, 2, false><<<(a.N + 31) / 32, 512, 0, st>>>(a, pbuf);
+    auto go = [&](auto MTc, auto NTc, auto NWc) {
+        constexpr int MT = decltype(MTc)::value, NT = decltype(NTc)::value, NW = decltype(NWc)::value;
+        const unsigned g = (unsigned)((a.N + 16 * NT - 1) / (16 * NT));
+        if (gated) k_mm_rows<XF, WF, MT, NT, true, NW><<<g, 64 * NW, 0, st>>>(a, pbuf);
+        else k_mm_rows<XF, WF, MT, 2 * NT, false, NW><<<(g + 1) / 2, 64 * NW, 0, st>>>(a, pbuf);
     };
-    if (a.M <= 16) go(KC<1>{});
-    else if (a.M <= 32) go(KC<2>{});
-    else go(KC<4>{});
+    if (a.M <= 16) go(KC<1>{}, KC<NTV>{}, KC<NWV>{});
+    else if (a.M <= 32) go(KC<2>{}, KC<1>{}, KC<8>{});
+    else go(KC<4>{}, KC<1>{}, KC<8>{});
 }
 
 template <int XF, int WF> void run_tiles(const FwdArgs& a, const Plan& p, bool gated, bool ex, hipStream_t st) {
