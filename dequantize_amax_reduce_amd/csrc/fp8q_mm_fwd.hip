@@ -276,8 +276,8 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
 }
 
 // The end of a split product: the partial sums of every output, in order,
-// then the epilogue.  With cast, p goes to pbuf in binary32 and the group cast
-// follows as its own launch.
+// then the epilogue.  A thread takes V columns of a row (4 where the rows are
+// whole vectors); with CAST, the 32 threads of a 128-group find its amax.
 struct JoinArgs {
     const float* part;
     int splits;
@@ -285,9 +285,11 @@ struct JoinArgs {
     int N, gated, act;
     void* y;
     int ydt;
-    float* pbuf;
     void* z;
     int zdt;
+    uint8_t* q;
+    int qfmt;
+    float* sinv;
 };
 
 __device__ __forceinline__ void put1(void* y, int dt, int64_t e, float v) {
@@ -296,150 +298,199 @@ __device__ __forceinline__ void put1(void* y, int dt, int64_t e, float v) {
     else store1<kF16>(y, e, v);
 }
 
-__global__ void __launch_bounds__(256) k_mm_join(JoinArgs a) {
-    const int64_t total = a.M * a.N, W = a.gated ? 2 * (int64_t)a.N : a.N, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        const int64_t m = i / a.N, n = i - m * a.N;
+template <int V, bool CAST> __global__ void __launch_bounds__(256) k_mm_join(JoinArgs a) {
+    const int64_t W = a.gated ? 2 * (int64_t)a.N : a.N, per = a.N / V, total = a.M * per;
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
+        const int64_t m = i / per, n = (i - m * per) * V;
         const float* p = a.part + m * W + n;
-        float g = 0.0f, u = 0.0f;
-        for (int s = 0; s < a.splits; ++s) {
-            g += p[(int64_t)s * a.M * W];
-            if (a.gated) u += p[(int64_t)s * a.M * W + a.N];
-        }
-        float v = g;
-        if (a.gated) {
-            if (a.z) {
-                put1(a.z, a.zdt, m * W + n, g);
-                put1(a.z, a.zdt, m * W + a.N + n, u);
+        float g[V], u[V], v[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) g[k] = u[k] = 0.0f;
+        for (int s = 0; s < a.splits; ++s, p += a.M * W) {
+            if constexpr (V == 4) {
+                const v4f x = *(const v4f*)p;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) g[k] += x[k];
+                if (a.gated) {
+                    const v4f y = *(const v4f*)(p + a.N);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) u[k] += y[k];
+                }
+            } else {
+                g[0] += p[0];
+                if (a.gated) u[0] += p[a.N];
             }
-            v = act_value(a.act, g) * u;
         }
-        if (a.pbuf) a.pbuf[i] = v;
-        else put1(a.y, a.ydt, i, v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            v[k] = a.gated ? act_value(a.act, g[k]) * u[k] : g[k];
+            if (a.z) {
+                put1(a.z, a.zdt, m * W + n + k, g[k]);
+                put1(a.z, a.zdt, m * W + a.N + n + k, u[k]);
+            }
+            if (!CAST) put1(a.y, a.ydt, m * a.N + n + k, v[k]);
+        }
+        if constexpr (CAST) {                              // N % 128 == 0: whole groups of 32 threads
+            uint32_t mx = 0;
+#pragma unroll
+            for (int k = 0; k < V; ++k) mx = umax(mx, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+            mx = umax(max_lanes<32>(mx), 0x38D1B717u);      // the group cast's 1e-4 clamp
+            const float top = a.qfmt == kE4M3 ? Fp8Fmt<kE4M3>::max : Fp8Fmt<kE5M2>::max;
+            const float sc = top / __uint_as_float(mx);
+            if ((threadIdx.x & 31) == 0) a.sinv[i >> 5] = __uint_as_float(mx) / top;
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] *= sc;
+            const uint32_t w = a.qfmt == kE4M3 ? enc4<kE4M3>(v[0], v[1 % V], v[2 % V], v[3 % V])
+                                               : enc4<kE5M2>(v[0], v[1 % V], v[2 % V], v[3 % V]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) a.q[m * a.N + n + k] = (uint8_t)(w >> (8 * k));
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------
-// A workgroup of 8 waves owns 16 NT rows of the weights (of each of the two
-// for a gated pair) and all of the rows of X (16 MT of them); its waves take
-// every 8th block of K each, straight from memory to registers: nothing is
-// read twice by a workgroup, and the eight waves' loads cover 1 KB runs of
-// each weight row.  The waves' sums meet in LDS in a fixed order.
-template <int XF, int WF, int MT, int NT, bool GATED, int NW>
-__global__ void __launch_bounds__(64 * NW) k_mm_rows(FwdArgs a, float* pbuf) {
-    constexpr int H = GATED ? 2 : 1, BT = NT * H;           // MFMA tiles of weights a wave holds
-    __shared__ __attribute__((aligned(16))) float red[NW][BT][MT][64][4];
+// Up to 16 rows of X: bound by the weights' bytes.  A workgroup takes tiles of
+// 16 BT weight rows (8 BT columns of each projection of a gated pair: the gate
+// in the first 8 rows of an MFMA tile, the up projection in the other 8), and
+// its 8 waves every 8th block of K.  Each wave streams its blocks through a
+// ring of D stages in LDS that is its own: whole 128-byte lines of each row,
+// D - 1 stages in flight, no registers held and no barrier.  The ring runs on
+// across tiles, so that the loads of the next tile are in flight while the
+// waves' sums of this one meet in LDS, in a fixed order.
+template <int MP, int BT> struct RowsLds {
+    static constexpr int kX = BT * 2048, kS = kX + MP * 1024, kStage = kS + 256;
+    static constexpr int kRed = 8 * BT * 1024;
+    static constexpr int kStages = (160 * 1024 - kRed) / (8 * kStage) < 6 ? (160 * 1024 - kRed) / (8 * kStage) : 6;
+    static constexpr int kPer = 2 * BT + MP + 1;
+};
+
+// MP: 8-row pieces of X (1 or 2)
+template <int XF, int WF, int MP, int BT, bool GATED> __global__ void __launch_bounds__(512) k_mm_rows(FwdArgs a, float* pbuf) {
+    using L = RowsLds<MP, BT>;
+    constexpr int D = L::kStages, C = GATED ? 8 * BT : 16 * BT;   // columns a tile
+    __shared__ __attribute__((aligned(1024))) char smem[8 * D * L::kStage + L::kRed];
+    float* red = (float*)(smem + 8 * D * L::kStage);              // [wave][tile][lane][4]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, lr = lane >> 4;
-    const int n0 = (int)blockIdx.x * 16 * NT;
+    const int col = lane & 15, lr = lane >> 4, sub = lane >> 3;
     const int64_t pitch = (int64_t)a.KB * 128;
+    const int tiles = (a.N + C - 1) / C, nb = (a.KB + 7) / 8;
+    char* ring = smem + wave * D * L::kStage;
+    const uint32_t ring_lds = lds_offset(ring), off = (uint32_t)(((lane & 7) ^ sub) * 16);
 
-    const uint8_t* wp[BT];
+    uint32_t vx[MP];
 #pragma unroll
-    for (int j = 0; j < BT; ++j) {
-        const int n = min(n0 + (j % NT) * 16 + col, a.N - 1);
-        wp[j] = (j < NT ? a.w0 : a.w1) + n * pitch + lr * 16;
-    }
-    const uint8_t* xp[MT];
-    const float* sp[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int64_t m = min((int64_t)(t * 16 + col), a.M - 1);
-        xp[t] = a.x + m * pitch + lr * 16;
-        sp[t] = a.xs + m * a.KB;
-    }
-    const float* s0 = a.ws0 + (int64_t)(n0 >> 7) * a.KB;    // 16 NT divides 128: one block row a workgroup
-    const float* s1 = GATED ? a.ws1 + (int64_t)(n0 >> 7) * a.KB : s0;
+    for (int p = 0; p < MP; ++p) vx[p] = (uint32_t)(min((int64_t)(p * 8 + sub), a.M - 1) * pitch) + off;
+    const float* sx = a.xs + min((int64_t)col, a.M - 1) * a.KB;
 
-    v4f acc[BT][MT];
+    // the next block to load: block `li` of tile `lt`.  A wave's blocks past
+    // the end of K (and of the last tile) are loads of the last one again, so
+    // that the count in flight is the same for all; they are not multiplied.
+    int lt = blockIdx.x, li = 0;
+    auto issue = [&](int stage) {
+        const int n0 = lt * C, kb = min(wave + 8 * li, a.KB - 1);
+        const uint32_t s = ring_lds + stage * L::kStage;
 #pragma unroll
-    for (int j = 0; j < BT; ++j)
+        for (int j = 0; j < BT; ++j)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[j][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-    struct Block {
-        v8i w[BT], x[MT];
-        float sx[MT];
-    };
-    auto load = [&](Block& b, int kb) {
+            for (int p = 0; p < 2; ++p) {
+                const int r = GATED ? 8 * j + sub : 16 * j + 8 * p + sub;
+                const uint32_t v = (uint32_t)(min(r, a.N - 1 - n0) * pitch) + off;
+                lds_dma16(s + j * 2048 + p * 1024, v, (GATED && p ? a.w1 : a.w0) + n0 * pitch + kb * 128);
+            }
 #pragma unroll
-        for (int j = 0; j < BT; ++j) b.w[j] = frag_nt((const char*)wp[j] + kb * 128, (const char*)wp[j] + kb * 128 + 64);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            b.x[t] = frag((const char*)xp[t] + kb * 128, (const char*)xp[t] + kb * 128 + 64);
-            b.sx[t] = sp[t][kb];
+        for (int p = 0; p < MP; ++p) lds_dma16(s + L::kX + p * 1024, vx[p], a.x + kb * 128);
+        const float* sp = lane < 62 ? sx : (GATED && lane == 63 ? a.ws1 : a.ws0) + (int64_t)(n0 >> 7) * a.KB;
+        lds_dma4_at(s + L::kS, sp + kb);
+        if (++li == nb) {
+            li = 0;
+            if (lt + (int)gridDim.x < tiles) lt += gridDim.x;
         }
     };
-    auto mul = [&](const Block& b, int kb) {
-        const float f0 = s0[kb], f1 = s1[kb];
-        v4i ww[BT][4];
+    if (a.KB > 0)
+        for (int i = 0; i < D - 1; ++i) issue(i);
+    int stage = 0;
+    const uint32_t c0 = (uint32_t)((lr ^ (col & 7)) * 16), c1 = (uint32_t)(((lr + 4) ^ (col & 7)) * 16);
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        v4f acc[BT];
 #pragma unroll
-        for (int j = 0; j < BT; ++j) widen_codes<WF>(b.w[j], ww[j]);
+        for (int j = 0; j < BT; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < nb; ++i) {
+            issue(stage == 0 ? D - 1 : stage - 1);
+            dma_wait<(D - 1) * L::kPer>();
+            const char* s = ring + stage * L::kStage;
+            v8i w[BT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
+            for (int j = 0; j < BT; ++j) w[j] = frag(s + j * 2048 + col * 128 + c0, s + j * 2048 + col * 128 + c1);
+            const char* px = s + L::kX + (MP == 1 ? col & 7 : col) * 128;
+            const v8i x = frag(px + c0, px + c1);
+            const float f = *(const float*)(s + L::kS + col * 4);
+            const float f0 = f * *(const float*)(s + L::kS + 62 * 4), f1 = f * *(const float*)(s + L::kS + 63 * 4);
             v4i xw[4];
-            widen_codes<XF>(b.x[t], xw);
+            widen_codes<XF>(x, xw);
             v4f r[BT];
 #pragma unroll
-            for (int j = 0; j < BT; ++j) r[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int j = 0; j < BT; ++j) r[j] = mfma_bf16(ww[j][k], xw[k], r[j]);
-#pragma unroll
             for (int j = 0; j < BT; ++j) {
-                const float f = b.sx[t] * (j < NT ? f0 : f1);
+                v4i ww[4];
+                widen_codes<WF>(w[j], ww);
+                r[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[j][t][i] = __builtin_fmaf(r[j][i], f, acc[j][t][i]);
+                for (int k = 0; k < 4; ++k) r[j] = mfma_bf16(ww[k], xw[k], r[j]);
             }
+            // rows 8 to 15 of a gated tile, the up projection's, are in the lanes from 32 on
+            const float fl = GATED && lr >= 2 ? f1 : f0;
+            if (wave + 8 * i < a.KB)
+#pragma unroll
+                for (int j = 0; j < BT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][e] = __builtin_fmaf(r[j][e], fl, acc[j][e]);
+            // this stage's reads are done before its next loads are issued
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            stage = stage + 1 == D ? 0 : stage + 1;
         }
-    };
-    for (int kb = wave; kb < a.KB; kb += NW) {
-        Block b;
-        load(b, kb);
-        mul(b, kb);
-    }
 #pragma unroll
-    for (int j = 0; j < BT; ++j)
+        for (int j = 0; j < BT; ++j) *(v4f*)(red + ((wave * BT + j) * 64 + lane) * 4) = acc[j];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wg_barrier();
+        for (int i = threadIdx.x; i < C * 16; i += 512) {
+            const int nl = i % C, m = i / C, n = tile * C + nl;
+            if (m >= a.M || n >= a.N) continue;
+            const int j = GATED ? nl >> 3 : nl >> 4, row = GATED ? nl & 7 : nl & 15;
+            const float* p = red + (j * 64 + m + (row >> 2) * 16) * 4 + (row & 3);
+            float g = 0.0f, u = 0.0f;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) *(v4f*)red[wave][j][t][lane] = acc[j][t];
-    __syncthreads();
-    // outputs: NT x MT tiles of 16 x 16; n fastest
-    for (int i = threadIdx.x; i < NT * MT * 256; i += 64 * NW) {
-        const int nl = i % (NT * 16), m = i / (NT * 16);
-        const int j = nl >> 4, n = n0 + nl;
-        if (m >= a.M || n >= a.N) continue;
-        const int l = (m & 15) + ((nl & 15) >> 2) * 16, e = nl & 3, t = m >> 4;
-        float g = 0.0f, u = 0.0f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            g += red[w][j][t][l][e];
-            if constexpr (GATED) u += red[w][NT * (H - 1) + j][t][l][e];
-        }
-        float v = g;
-        if constexpr (GATED) {
-            if (a.z) {
-                const int64_t at = m * 2 * (int64_t)a.N + n;
-                put1(a.z, a.zdt, at, g);
-                put1(a.z, a.zdt, at + a.N, u);
+            for (int w = 0; w < 8; ++w) {
+                g += p[w * BT * 256];
+                if constexpr (GATED) u += p[w * BT * 256 + 32 * 4];
             }
-            v = act_value(a.act, g) * u;
+            float v = g;
+            if constexpr (GATED) {
+                if (a.z) {
+                    const int64_t at = m * 2 * (int64_t)a.N + n;
+                    put1(a.z, a.zdt, at, g);
+                    put1(a.z, a.zdt, at + a.N, u);
+                }
+                v = act_value(a.act, g) * u;
+            }
+            const int64_t at = m * (int64_t)a.N + n;
+            if (pbuf) pbuf[at] = v;
+            else put1(a.y, a.ydt, at, v);
         }
-        const int64_t at = m * (int64_t)a.N + n;
-        if (pbuf) pbuf[at] = v;
-        else put1(a.y, a.ydt, at, v);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wg_barrier();                                      // red is free for the next tile
     }
+    dma_wait<0>();                                         // no load may land in LDS that is no longer ours
 }
 
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
 
-constexpr int64_t kRowsMax = 64;       // rows that k_mm_rows takes
-constexpr int NTV = 2, NWV = 16;
+constexpr int64_t kRowsMax = 16;       // rows that k_mm_rows takes
+constexpr int64_t kExactMax = 64;      // rows up to which sums are binary32 whatever the outputs
 
 // How a product is tiled: rows a tile, and workgroups over K (splits)
 struct Plan {
@@ -448,8 +499,14 @@ struct Plan {
     int64_t tm, tn;
 };
 
-// ex: binary32 sums (k_mm's EX), whose tiles are at most 128 rows tall: the
-// widened fragments leave registers for no more
+// The tile height and the split of K with the least estimated time.  A round
+// of 256 workgroups takes the measured microseconds below per block of K (8192
+// columns, K = 7168, every round full: fp8 sums 257, 282 and 350 us for 4096
+// rows at heights 256, 128 and 64; binary32 sums 413 and 492 at 128 and 64)
+// and about 4 to fill and drain; a split writes its partial sums and the join
+// reads them, at about 5 TB/s and a launch.  ex: binary32 sums (k_mm's EX),
+// whose tiles are at most 128 rows tall: the widened fragments leave registers
+// for no more.
 Plan plan(int64_t M, int64_t N, int64_t K, bool gated, bool ex) {
     Plan p{};
     const int64_t KB = K / 128;
@@ -459,16 +516,22 @@ Plan plan(int64_t M, int64_t N, int64_t K, bool gated, bool ex) {
         return p;
     }
     p.tn = (N + (gated ? 127 : 255)) / (gated ? 128 : 256);
-    // the tallest tile that still gives most CUs one; below that, K is split
-    p.bm = ex ? 128 : 256;
-    while (p.bm > 64 && (M + p.bm - 1) / p.bm * p.tn < 200) p.bm /= 2;
-    p.tm = (M + p.bm - 1) / p.bm;
-    const int64_t tiles = p.tm * p.tn;
-    int64_t s = 1;
-    while (tiles * s * 2 <= 256 && KB / (s * 2) >= 8) s *= 2;
-    p.kper = (int)((KB + s - 1) / s);
-    if (p.kper < 1) p.kper = 1;
-    p.splits = (int)std::max<int64_t>(1, (KB + p.kper - 1) / p.kper);
+    double best = 0.0;
+    for (int bm = ex ? 128 : 256; bm >= 64; bm /= 2) {
+        const double block = ex ? (bm == 128 ? 1.84 : 1.10) : (bm == 256 ? 2.30 : bm == 128 ? 1.26 : 0.78);
+        const int64_t tm = (M + bm - 1) / bm, tiles = tm * p.tn;
+        for (int64_t s = 1; s == 1 || (s <= 16 && tiles * s <= 512 && KB / s >= 2); s *= 2) {
+            const int64_t kper = std::max<int64_t>(1, (KB + s - 1) / s);
+            const double t = (double)((tiles * s + 255) / 256) * ((double)kper * block + 4.0) +
+                             (s > 1 ? 3.0 + (double)(s * M * N * (gated ? 16 : 8)) / 5e6 : 0.0);
+            if (best > 0.0 && t >= best) continue;
+            best = t;
+            p.bm = bm;
+            p.tm = tm;
+            p.kper = (int)kper;
+            p.splits = (int)std::max<int64_t>(1, (KB + kper - 1) / kper);
+        }
+    }
     return p;
 }
 
@@ -478,15 +541,25 @@ int64_t part_bytes(const Plan& p, int64_t M, int64_t N, bool gated) {
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 template <int XF, int WF> void run_rows(const FwdArgs& a, float* pbuf, bool gated, hipStream_t st) {
-    auto go = [&](auto MTc, auto NTc, auto NWc) {
-        constexpr int MT = decltype(MTc)::value, NT = decltype(NTc)::value, NW = decltype(NWc)::value;
-        const unsigned g = (unsigned)((a.N + 16 * NT - 1) / (16 * NT));
-        if (gated) k_mm_rows<XF, WF, MT, NT, true, NW><<<g, 64 * NW, 0, st>>>(a, pbuf);
-        else k_mm_rows<XF, WF, MT, 2 * NT, false, NW><<<(g + 1) / 2, 64 * NW, 0, st>>>(a, pbuf);
+    // One or two MFMA tiles a workgroup tile: whichever spreads the weights
+    // more evenly over 256 workgroups, and two where they are level (the rows
+    // of X are read half as often).  One token through 18432 gated columns:
+    // 45.1 us with one (9 rounds of 8 columns), 46.6 with two (5 of 16, the
+    // last half empty); 16 rows through 7168 columns: 34.8 and 27.9.
+    const int per = gated ? 8 : 16;
+    auto rounds = [&](int bt) { return (((a.N + per * bt - 1) / (per * bt) + 255) / 256) * bt; };
+    auto go = [&](auto MPc, auto BTc) {
+        constexpr int MP = decltype(MPc)::value, BT = decltype(BTc)::value;
+        const unsigned g = (unsigned)std::min((a.N + per * BT - 1) / (per * BT), 256);
+        if (gated) k_mm_rows<XF, WF, MP, BT, true><<<g, 512, 0, st>>>(a, pbuf);
+        else k_mm_rows<XF, WF, MP, BT, false><<<g, 512, 0, st>>>(a, pbuf);
     };
-    if (a.M <= 16) go(KC<1>{}, KC<NTV>{}, KC<NWV>{});
-    else if (a.M <= 32) go(KC<2>{}, KC<1>{}, KC<8>{});
-    else go(KC<4>{}, KC<1>{}, KC<8>{});
+    auto rows = [&](auto MPc) {
+        if (rounds(1) < rounds(2)) go(MPc, KC<1>{});
+        else go(MPc, KC<2>{});
+    };
+    if (a.M <= 8) rows(KC<1>{});
+    else rows(KC<2>{});
 }
 
 template <int XF, int WF> void run_tiles(const FwdArgs& a, const Plan& p, bool gated, bool ex, hipStream_t st) {
@@ -515,7 +588,7 @@ int64_t mm_fwd_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool cast)
     int64_t most = 0;
     for (int ex = cast ? 1 : 0; ex < 2; ++ex) {
         const Plan p = plan(M, N, K, gated, ex);
-        const int64_t pb = cast && (p.rows || p.splits > 1) ? M * N * 4 : 0;
+        const int64_t pb = cast && p.rows ? M * N * 4 : 0;
         most = std::max(most, up256(part_bytes(p, M, N, gated)) + pb);
     }
     return most;
@@ -523,7 +596,7 @@ int64_t mm_fwd_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool cast)
 
 void launch_mm_fwd(const MmFwd& f, hipStream_t st) {
     const bool gated = f.gated;
-    const bool ex = f.q || (f.y && f.ydt == kF32) || (f.z && f.zdt == kF32);
+    const bool ex = f.M <= kExactMax || f.q || (f.y && f.ydt == kF32) || (f.z && f.zdt == kF32);
     const Plan p = plan(f.M, f.N, f.K, gated, ex);
     FwdArgs a{f.x, f.xs, f.w0, f.ws0, f.w1, f.ws1, f.M, f.N, f.K / 128, (uint32_t)p.tm, (uint32_t)p.tn, f.act,
               f.y, f.ydt, f.q, f.qfmt, f.sinv, f.z, f.zdt, 0, 0, gated, p.kper, nullptr};
@@ -532,7 +605,7 @@ void launch_mm_fwd(const MmFwd& f, hipStream_t st) {
     char* ws = (char*)f.ws;
     float* pbuf = nullptr;
     if (p.splits > 1) a.part = (float*)ws;
-    if (f.q && (p.rows || p.splits > 1)) pbuf = (float*)(ws + up256(part_bytes(p, f.M, f.N, gated)));
+    if (f.q && p.rows) pbuf = (float*)ws;
     auto run = [&](auto X, auto W) {
         constexpr int XF = decltype(X)::value, WF = decltype(W)::value;
         if (p.rows) run_rows<XF, WF>(a, pbuf, gated, st);
@@ -541,9 +614,12 @@ void launch_mm_fwd(const MmFwd& f, hipStream_t st) {
     if (f.xfmt == kE4M3) { if (f.wfmt == kE4M3) run(KC<0>{}, KC<0>{}); else run(KC<0>{}, KC<1>{}); }
     else { if (f.wfmt == kE4M3) run(KC<1>{}, KC<0>{}); else run(KC<1>{}, KC<1>{}); }
     if (p.splits > 1) {
-        const JoinArgs j{a.part, p.splits, f.M, f.N, gated, f.act, f.y, f.ydt, pbuf, f.z, f.zdt};
-        const int64_t n = (f.M * f.N + 255) / 256;
-        k_mm_join<<<(unsigned)std::min<int64_t>(n, 4096), 256, 0, st>>>(j);
+        const JoinArgs j{a.part, p.splits, f.M, f.N, gated, f.act, f.y, f.ydt, f.z, f.zdt, f.q, f.qfmt, f.sinv};
+        const int V = f.N % 4 == 0 ? 4 : 1;
+        const unsigned g = (unsigned)std::min<int64_t>((f.M * (f.N / V) + 255) / 256, 4096);
+        if (f.q) k_mm_join<4, true><<<g, 256, 0, st>>>(j);
+        else if (V == 4) k_mm_join<4, false><<<g, 256, 0, st>>>(j);
+        else k_mm_join<1, false><<<g, 256, 0, st>>>(j);
     }
     if (pbuf) launch_group128_cast(pbuf, kF32, f.M * (f.N / 128), f.qfmt, f.q, f.sinv, st);
 }
