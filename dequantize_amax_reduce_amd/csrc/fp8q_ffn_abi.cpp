@@ -13,7 +13,7 @@
 namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 21;    // K, N, F
-constexpr int64_t kMaxRows = 65535 * 64;         // M of a backward pass: a grid's second dimension
+constexpr int64_t kMaxRows = 65535 * 64;         // M of a backward pass
 constexpr int64_t kMaxNormRows = INT32_MAX, kMaxNormCols = int64_t(1) << 30;
 constexpr int64_t kMaxTiles = (int64_t(1) << 23) - 1;   // workgroups of 512 threads: 2^32 threads a grid
 
@@ -267,6 +267,9 @@ static fp8q_status_t backward(fp8q::MmBwd& f, int64_t M, int64_t N, int64_t K, b
     fp8q_status_t st = check_sizes(M, N, K, kMaxRows);
     if (st != FP8Q_OK) return st;
     if (!grid_ok(M, K) || !grid_ok(2 * N + 64, K)) return FP8Q_EINVAL;
+    // the layout pass: 64 x 64 tiles of dy, 64 x 128 of the codes, 256 threads each
+    const int64_t mt = M / 64 + 1, nt = N / 64 + 1;
+    if (mt * nt + (K / 128) * (mt + 2 * nt) >= int64_t(1) << 24) return FP8Q_EINVAL;
     if (gated && (f.dw0 == nullptr) != (f.dw1 == nullptr) && N > 0 && K > 0) return FP8Q_EINVAL;
     const int64_t n = M * N;
     if (n > 0 && K > 0) {

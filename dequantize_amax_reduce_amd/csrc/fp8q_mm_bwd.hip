@@ -169,11 +169,11 @@ struct DzArgs {
 
 // dz and its transpose; 256 threads, one 64 x 64 tile a workgroup; thread
 // (i, v) takes 8 columns of the rows 2i and 2i + 1
-template <int DT, bool GATED> __global__ void __launch_bounds__(256) k_dz(DzArgs a) {
-    __shared__ TileT tg, tu;
+template <int DT, bool GATED> __device__ __forceinline__ void dz_tile(const DzArgs& a, uint32_t bx, uint32_t by, TileT* lds) {
+    TileT &tg = lds[0], &tu = lds[1];
     const int v = (int)threadIdx.x & 7, i = (int)threadIdx.x >> 3;
-    const int64_t m = (int64_t)blockIdx.y * 64 + 2 * i;
-    const int c = (int)blockIdx.x * 64 + v * 8;
+    const int64_t m = (int64_t)by * 64 + 2 * i;
+    const int c = (int)bx * 64 + v * 8;
     const int64_t zp = 2 * (int64_t)a.N, dp = GATED ? 2 * (int64_t)a.Np : a.Np;
     float g[2][8], u[2][8];
 #pragma unroll
@@ -207,9 +207,9 @@ template <int DT, bool GATED> __global__ void __launch_bounds__(256) k_dz(DzArgs
         if constexpr (GATED) tu.w[v * 8 + k][i] = pack_bf16x2(u[0][k], u[1][k]);
     }
     __syncthreads();
-    uint16_t* d = a.dzt + (int64_t)blockIdx.x * 64 * a.Mp;
-    store_t(tg, d, a.Mp, (int64_t)blockIdx.y * 64);
-    if constexpr (GATED) store_t(tu, d + (int64_t)a.Np * a.Mp, a.Mp, (int64_t)blockIdx.y * 64);
+    uint16_t* d = a.dzt + (int64_t)bx * 64 * a.Mp;
+    store_t(tg, d, a.Mp, (int64_t)by * 64);
+    if constexpr (GATED) store_t(tu, d + (int64_t)a.Np * a.Mp, a.Mp, (int64_t)by * 64);
 }
 
 struct DeqTArgs {
@@ -223,17 +223,16 @@ struct DeqTArgs {
 
 // The transposed dequantized matrix: 64 rows x 128 codes a workgroup; thread
 // (i, v) takes 16 codes of the rows 2i and 2i + 1.  Rows past R are zero.
-template <int FMT> __global__ void __launch_bounds__(256) k_deq_t(DeqTArgs a) {
-    __shared__ TileT t[2];
+template <int FMT> __device__ __forceinline__ void deq_tile(const DeqTArgs& a, uint32_t bx, uint32_t by, TileT* t) {
     const int v = (int)threadIdx.x & 7, i = (int)threadIdx.x >> 3;
-    const int64_t r0 = (int64_t)blockIdx.y * 64 + 2 * i;
+    const int64_t r0 = (int64_t)by * 64 + 2 * i;
     const int64_t K = (int64_t)a.KB * 128;
     float f[2][16];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         if (r0 + r < a.R) {
-            const v4u c = *(const v4u*)(a.q + (r0 + r) * K + (int64_t)blockIdx.x * 128 + v * 16);
-            const float s = a.s[((r0 + r) >> a.sh) * a.KB + blockIdx.x];
+            const v4u c = *(const v4u*)(a.q + (r0 + r) * K + (int64_t)bx * 128 + v * 16);
+            const float s = a.s[((r0 + r) >> a.sh) * a.KB + bx];
             dec4<FMT>(c.x, f[r]);
             dec4<FMT>(c.y, f[r] + 4);
             dec4<FMT>(c.z, f[r] + 8);
@@ -248,9 +247,34 @@ template <int FMT> __global__ void __launch_bounds__(256) k_deq_t(DeqTArgs a) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) t[v >> 2].w[(v & 3) * 16 + k][i] = pack_bf16x2(f[0][k], f[1][k]);
     __syncthreads();
-    uint16_t* d = a.t + (int64_t)blockIdx.x * 128 * a.pitch;
-    store_t(t[0], d, a.pitch, a.at + (int64_t)blockIdx.y * 64);
-    store_t(t[1], d + 64 * a.pitch, a.pitch, a.at + (int64_t)blockIdx.y * 64);
+    uint16_t* d = a.t + (int64_t)bx * 128 * a.pitch;
+    store_t(t[0], d, a.pitch, a.at + (int64_t)by * 64);
+    store_t(t[1], d + 64 * a.pitch, a.pitch, a.at + (int64_t)by * 64);
+}
+
+// All of a call's layout passes in one launch: workgroups [0, e0) take tiles
+// of dz, [e0, e1) of X, [e1, e2) of W (or the gate), the rest of the up
+// projection.
+struct PrepArgs {
+    DzArgs dz;
+    DeqTArgs x, w0, w1;
+    uint32_t e0, e1, e2, dzx;
+};
+template <int DT, bool GATED, int XF, int WF> __global__ void __launch_bounds__(256) k_prep(PrepArgs a) {
+    __shared__ TileT lds[2];
+    const uint32_t b = blockIdx.x;
+    if (b < a.e0) {
+        dz_tile<DT, GATED>(a.dz, b % a.dzx, b / a.dzx, lds);
+    } else if (b < a.e1) {
+        const uint32_t i = b - a.e0;
+        deq_tile<XF>(a.x, i % (uint32_t)a.x.KB, i / (uint32_t)a.x.KB, lds);
+    } else if (b < a.e2) {
+        const uint32_t i = b - a.e1;
+        deq_tile<WF>(a.w0, i % (uint32_t)a.w0.KB, i / (uint32_t)a.w0.KB, lds);
+    } else {
+        const uint32_t i = b - a.e2;
+        deq_tile<WF>(a.w1, i % (uint32_t)a.w1.KB, i / (uint32_t)a.w1.KB, lds);
+    }
 }
 
 __global__ void __launch_bounds__(256) k_zero16(uint16_t* p, int64_t n) {
@@ -291,13 +315,6 @@ void mm16(const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K,
 template <typename F> void with_fmt(int f, F&& go) {
     if (f == kE4M3) go(KC<kE4M3>{});
     else go(KC<kE5M2>{});
-}
-
-void deq_t(const uint8_t* q, int fmt, const float* s, int64_t R, int64_t Rp, int KB, int sh, uint16_t* t, int64_t pitch,
-           int64_t at, hipStream_t st) {
-    const DeqTArgs a{q, s, R, KB, sh, t, pitch, at};
-    const dim3 g((unsigned)KB, (unsigned)(Rp / 64));
-    with_fmt(fmt, [&](auto F) { k_deq_t<decltype(F)::value><<<g, 256, 0, st>>>(a); });
 }
 
 struct BwdLayout {
@@ -346,25 +363,32 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
     const bool wdx = f.dx != nullptr, wdw = f.dw0 != nullptr;
     // a bf16 gradient whose rows are whole 128-byte steps is dz already
     const bool direct = !gated && f.dt == kBF16 && f.N % 64 == 0 && al(f.dy, 16);
-    const DzArgs d{(const uint16_t*)f.dy, (const uint16_t*)f.z, f.M, l.Mp, f.N, (int)l.Np, f.act,
-                   wdx && !direct ? dz : nullptr, wdw ? dzt : nullptr};
-    if (d.dz || d.dzt) {
-        const dim3 g((unsigned)(l.Np / 64), (unsigned)(l.Mp / 64));
-        if (f.dt == kBF16) {
-            if (gated) k_dz<kBF16, true><<<g, 256, 0, st>>>(d);
-            else k_dz<kBF16, false><<<g, 256, 0, st>>>(d);
-        } else {
-            if (gated) k_dz<kF16, true><<<g, 256, 0, st>>>(d);
-            else k_dz<kF16, false><<<g, 256, 0, st>>>(d);
-        }
-    }
-    if (wdx) {
-        deq_t(f.w0, f.wfmt, f.ws0, f.N, l.Np, KB, 7, wt, l.C, 0, st);
-        if (gated) deq_t(f.w1, f.wfmt, f.ws1, f.N, l.Np, KB, 7, wt, l.C, l.Np, st);
-        mm16(direct ? (const uint16_t*)f.dy : dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, st);
-    }
+    PrepArgs p{};
+    p.dz = DzArgs{(const uint16_t*)f.dy, (const uint16_t*)f.z, f.M, l.Mp, f.N, (int)l.Np, f.act,
+                  wdx && !direct ? dz : nullptr, wdw ? dzt : nullptr};
+    p.x = DeqTArgs{f.x, f.xs, f.M, KB, 0, xt, l.Mp, 0};
+    p.w0 = DeqTArgs{f.w0, f.ws0, f.N, KB, 7, wt, l.C, 0};
+    p.w1 = DeqTArgs{f.w1, f.ws1, f.N, KB, 7, wt, l.C, l.Np};
+    p.dzx = (uint32_t)(l.Np / 64);
+    const uint32_t row_tiles = (uint32_t)(l.Mp / 64), w_tiles = wdx ? (uint32_t)KB * p.dzx : 0;
+    p.e0 = p.dz.dz || p.dz.dzt ? p.dzx * row_tiles : 0;
+    p.e1 = p.e0 + (wdw ? (uint32_t)KB * row_tiles : 0);
+    p.e2 = p.e1 + w_tiles;
+    const unsigned g = p.e2 + (gated ? w_tiles : 0);
+    with_fmt(f.xfmt, [&](auto X) {
+        with_fmt(f.wfmt, [&](auto W) {
+            constexpr int XF = decltype(X)::value, WF = decltype(W)::value;
+            if (f.dt == kBF16) {
+                if (gated) k_prep<kBF16, true, XF, WF><<<g, 256, 0, st>>>(p);
+                else k_prep<kBF16, false, XF, WF><<<g, 256, 0, st>>>(p);
+            } else {
+                if (gated) k_prep<kF16, true, XF, WF><<<g, 256, 0, st>>>(p);
+                else k_prep<kF16, false, XF, WF><<<g, 256, 0, st>>>(p);
+            }
+        });
+    });
+    if (wdx) mm16(direct ? (const uint16_t*)f.dy : dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, st);
     if (wdw) {
-        deq_t(f.x, f.xfmt, f.xs, f.M, l.Mp, KB, 0, xt, l.Mp, 0, st);
         if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, st);
         else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, st);
     }

@@ -23,11 +23,16 @@ typedef unsigned int v2u_a1 __attribute__((ext_vector_type(2), aligned(1)));
 typedef unsigned int u32_a1 __attribute__((aligned(1)));
 
 // the lane vector of VE elements of row `row` that starts at column c; the
-// last vector of a row may hold fewer than VE (the rest read as zero)
-template <int DT> __device__ __forceinline__ v4u ld_row(const void* row, int c, int cols) {
+// last vector of a row may hold fewer than VE (the rest read as zero).  NT: a
+// stream read once.  Rows of whole 128-element groups are streamed past the
+// caches (16384 x 7168 bf16: 158.6 us against 166.6); rows that may end inside
+// a line are not, because the line's other half is the next row's (1999 x 5001
+// f32: 21.4 us streamed, 19.1 cached).
+template <int DT, bool NT = true> __device__ __forceinline__ v4u ld_row(const void* row, int c, int cols) {
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
     if (c + VE <= cols) {
-        const v4u_a2 t = *(const v4u_a2*)((const char*)row + (int64_t)c * ES);
+        const v4u_a2* p = (const v4u_a2*)((const char*)row + (int64_t)c * ES);
+        const v4u_a2 t = NT ? __builtin_nontemporal_load(p) : *p;
         return v4u{t.x, t.y, t.z, t.w};
     }
     union { v4u v; uint32_t w[4]; uint16_t e[8]; } t;
@@ -41,11 +46,13 @@ template <int DT> __device__ __forceinline__ v4u ld_row(const void* row, int c, 
     return t.v;
 }
 
-template <int DT> __device__ __forceinline__ void st_row(void* row, int c, int cols, const float* p) {
+template <int DT, bool NT = true> __device__ __forceinline__ void st_row(void* row, int c, int cols, const float* p) {
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
     const v4u t = pack_out16<DT>(p);
     if (c + VE <= cols) {
-        *(v4u_a2*)((char*)row + (int64_t)c * ES) = v4u_a2{t.x, t.y, t.z, t.w};
+        v4u_a2* d = (v4u_a2*)((char*)row + (int64_t)c * ES);
+        if constexpr (NT) __builtin_nontemporal_store(v4u_a2{t.x, t.y, t.z, t.w}, d);
+        else *d = v4u_a2{t.x, t.y, t.z, t.w};
         return;
     }
 #pragma unroll
@@ -53,12 +60,14 @@ template <int DT> __device__ __forceinline__ void st_row(void* row, int c, int c
         if (c + k < cols) store1<DT>(row, c + k, p[k]);
 }
 
-template <int FMT, int VE> __device__ __forceinline__ void st_codes(uint8_t* row, int c, int cols, const float* p) {
+template <int FMT, int VE, bool NT> __device__ __forceinline__ void st_codes(uint8_t* row, int c, int cols, const float* p) {
     uint32_t w[VE / 4];
 #pragma unroll
     for (int k = 0; k < VE / 4; ++k) w[k] = enc4<FMT>(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
     if (c + VE <= cols) {
-        if constexpr (VE == 8) *(v2u_a1*)(row + c) = v2u_a1{w[0], w[1]};
+        if constexpr (VE == 8 && NT) __builtin_nontemporal_store(v2u_a1{w[0], w[1]}, (v2u_a1*)(row + c));
+        else if constexpr (VE == 8) *(v2u_a1*)(row + c) = v2u_a1{w[0], w[1]};
+        else if constexpr (NT) __builtin_nontemporal_store((u32_a1)w[0], (u32_a1*)(row + c));
         else *(u32_a1*)(row + c) = w[0];
         return;
     }
@@ -73,16 +82,36 @@ template <int DT> __device__ __forceinline__ void widen16(v4u r, float* v) {
     t.widen(v);
 }
 
-// VE weights from column c (zero past the row's end), as binary32; WF32: the
+// VE weights from column c (zero past the row's end), kept as loaded; WF32: the
 // weight is binary32 whatever the activations are
-template <int DT, bool WF32> __device__ __forceinline__ void ld_weight(const void* w, int c, int cols, float* v) {
-    constexpr int VE = LaneVE<DT>::value;
-    if constexpr (!WF32 || DT == kF32) {
-        widen16<DT>(ld_row<DT>(w, c, cols), v);
-    } else {
-        widen16<kF32>(ld_row<kF32>(w, c, cols), v);
-        if constexpr (VE == 8) widen16<kF32>(ld_row<kF32>(w, c + 4, cols), v + 4);
+template <int DT, bool WF32> struct Weights {
+    static constexpr bool kWide = WF32 && DT != kF32;
+    v4u r[kWide ? 2 : 1];
+    __device__ __forceinline__ void load(const void* w, int c, int cols) {
+        if constexpr (!kWide) {
+            r[0] = ld_row<DT, false>(w, c, cols);
+        } else {
+            r[0] = ld_row<kF32, false>(w, c, cols);
+            r[1] = ld_row<kF32, false>(w, c + 4, cols);
+        }
     }
+    // the asm keeps the compiler from widening once for all rows: that holds
+    // twice the registers, and spills beside the next row's loads
+    __device__ __forceinline__ void widen(float* v) {
+        asm volatile("" : "+v"(r[0]));
+        if constexpr (kWide) asm volatile("" : "+v"(r[1]));
+        if constexpr (!kWide) {
+            widen16<DT>(r[0], v);
+        } else {
+            widen16<kF32>(r[0], v);
+            widen16<kF32>(r[1], v + 4);
+        }
+    }
+};
+template <int DT, bool WF32> __device__ __forceinline__ void ld_weight(const void* w, int c, int cols, float* v) {
+    Weights<DT, WF32> t;
+    t.load(w, c, cols);
+    t.widen(v);
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -91,14 +120,23 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
+// LDS writes of every wave are visible after it; loads in flight stay in
+// flight (the next row's are)
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // sum and max over the lanes of a row: one wave (WAVE), or the whole
-// workgroup through lds, whose 16 words are free again only after a barrier
+// workgroup through lds, whose 16 words may be written again after the
+// workgroup's next barrier
 template <bool WAVE> __device__ __forceinline__ float row_sum(float v, float* lds) {
     v = wave_sum(v);
     if constexpr (WAVE) return v;
     const int nw = (int)blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
+    lds_barrier();
     float s = lds[0];
     for (int i = 1; i < nw; ++i) s += lds[i];
     return s;
@@ -109,7 +147,7 @@ template <bool WAVE> __device__ __forceinline__ uint32_t row_max(uint32_t v, uin
     if constexpr (WAVE) return v;
     const int nw = (int)blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
+    lds_barrier();
     uint32_t m = lds[0];
     for (int i = 1; i < nw; ++i) m = umax(m, lds[i]);
     return m;
@@ -132,16 +170,19 @@ __device__ __forceinline__ float rstd_of(float ss, int cols, float eps) {
     return 1.0f / sqrtf(ss / (float)cols + eps);
 }
 
-// h of one lane vector, in binary32
-template <int DT> __device__ __forceinline__ void load_h(const void* xr, const void* rr, int c, int cols, float* h) {
+// h of one lane vector, in binary32, from the loaded vectors
+template <int DT> __device__ __forceinline__ void sum_h(v4u x, v4u r, bool res, float* h) {
     constexpr int VE = LaneVE<DT>::value;
-    widen16<DT>(ld_row<DT>(xr, c, cols), h);
-    if (rr) {
+    widen16<DT>(x, h);
+    if (res) {
         float t[VE];
-        widen16<DT>(ld_row<DT>(rr, c, cols), t);
+        widen16<DT>(r, t);
 #pragma unroll
         for (int k = 0; k < VE; ++k) h[k] += t[k];
     }
+}
+template <int DT> __device__ __forceinline__ void load_h(const void* xr, const void* rr, int c, int cols, float* h) {
+    sum_h<DT>(ld_row<DT>(xr, c, cols), rr ? ld_row<DT>(rr, c, cols) : v4u{0, 0, 0, 0}, rr != nullptr, h);
 }
 
 // scale and encode one lane vector of y; group: every 128 / VE lanes hold one
@@ -165,7 +206,7 @@ __device__ __forceinline__ void cast_vec(const float* y, int c, int cols, uint8_
 #pragma unroll
         for (int k = 0; k < VE; ++k) p[k] = satur ? sat<FMT>(y[k] * scale) : y[k] * scale;
     }
-    if (c < cols) st_codes<FMT, VE>(qr, c, cols, p);
+    if (c < cols) st_codes<FMT, VE, GROUP>(qr, c, cols, p);
 }
 
 // the per-row scale from the row's amax bits (the per-channel cast's guard)
@@ -178,61 +219,80 @@ template <int FMT> __device__ __forceinline__ float row_scale(uint32_t m, float*
     return scale;
 }
 
-// One row per workgroup (or, WAVE, per wave), V lane vectors a thread.
-template <int DT, bool WF32, int FMT, bool GROUP, bool WAVE, int V>
-__global__ void __launch_bounds__(1024) k_norm_rows(NormArgs a) {
+// One row per workgroup (or, WAVE, per wave) at a time, V lane vectors a
+// thread.  A workgroup takes several rows, so that the weight is read once and
+// the next row's loads are in flight through the reductions and stores of this
+// one: 16384 x 7168 bf16 with residual 158.6 us with one row a workgroup.
+// TB: the most threads; up to 512 leave the registers for the next row's loads.
+template <int DT, bool WF32, int FMT, bool GROUP, bool WAVE, int V, int TB>
+__global__ void __launch_bounds__(TB) k_norm_rows(NormArgs a) {
+    constexpr bool PF = TB <= 512;
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
-    __shared__ float lds_s[16];
-    __shared__ uint32_t lds_m[16];
+    __shared__ float lds_s[2][16];
+    __shared__ uint32_t lds_m[2][16];
     const int lanes = WAVE ? 64 : (int)blockDim.x;
     const int t = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
     const int per = WAVE ? (int)blockDim.x >> 6 : 1;        // rows a workgroup takes at once
-    for (int64_t row = (int64_t)blockIdx.x * per + (WAVE ? threadIdx.x >> 6 : 0); row < a.rows;
-         row += (int64_t)gridDim.x * per) {
+    const int64_t first = (int64_t)blockIdx.x * per + (WAVE ? threadIdx.x >> 6 : 0), next = (int64_t)gridDim.x * per;
+    if (first >= a.rows) return;                            // whole waves; whole workgroups unless WAVE
+    v4u xv[V], rv[V];
+    auto load = [&](int64_t row) {
         const int64_t off = row * (int64_t)a.cols * ES;
-        const void* xr = (const char*)a.x + off;
-        const void* rr = a.res ? (const char*)a.res + off : nullptr;
-
-        float h[V][VE], w[V][VE];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * lanes + t) * VE;
+            xv[v] = ld_row<DT, GROUP>((const char*)a.x + off, c, a.cols);
+            if (a.res) rv[v] = ld_row<DT, GROUP>((const char*)a.res + off, c, a.cols);
+        }
+    };
+    load(first);
+    Weights<DT, WF32> w[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v].load(a.w, (v * lanes + t) * VE, a.cols);
+    int flip = 0;
+    for (int64_t row = first; row < a.rows; row += next, flip ^= 1) {
+        float h[V][VE];
         float ss = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) load_h<DT>(xr, rr, (v * lanes + t) * VE, a.cols, h[v]);
-#pragma unroll
-        for (int v = 0; v < V; ++v) ld_weight<DT, WF32>(a.w, (v * lanes + t) * VE, a.cols, w[v]);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            sum_h<DT>(xv[v], rv[v], a.res != nullptr, h[v]);
 #pragma unroll
             for (int k = 0; k < VE; ++k) ss = __builtin_fmaf(h[v][k], h[v][k], ss);
-        const float rs = rstd_of(row_sum<WAVE>(ss, lds_s), a.cols, a.eps);
+        }
+        if (PF && row + next < a.rows) load(row + next);
+        const float rs = rstd_of(row_sum<WAVE>(ss, lds_s[flip]), a.cols, a.eps);
         if (t == 0 && a.rstd) a.rstd[row] = rs;
         if (a.h) {
-            void* hr = (char*)a.h + off;
+            void* hr = (char*)a.h + row * (int64_t)a.cols * ES;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = (v * lanes + t) * VE;
-                if (c < a.cols) st_row<DT>(hr, c, a.cols, h[v]);
+                if (c < a.cols) st_row<DT, GROUP>(hr, c, a.cols, h[v]);
             }
         }
         uint32_t m = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            float wv[VE];
+            w[v].widen(wv);
 #pragma unroll
             for (int k = 0; k < VE; ++k) {
-                h[v][k] = (h[v][k] * rs) * w[v][k];
+                h[v][k] = (h[v][k] * rs) * wv[k];
                 if constexpr (!GROUP) {
                     const int c = (v * lanes + t) * VE + k;     // columns past the row's end do not count
                     m = umax(m, c < a.cols ? __float_as_uint(h[v][k]) & 0x7FFFFFFFu : 0u);
                 }
             }
+        }
         float scale = 0.0f;
         bool satur = false;
-        if constexpr (!GROUP) scale = row_scale<FMT>(row_max<WAVE>(m, lds_m), a.sinv + row, t == 0, &satur);
+        if constexpr (!GROUP) scale = row_scale<FMT>(row_max<WAVE>(m, lds_m[flip]), a.sinv + row, t == 0, &satur);
         uint8_t* qr = a.q + row * (int64_t)a.cols;
         float* sr = GROUP ? a.sinv + row * (int64_t)(a.cols >> 7) : nullptr;
 #pragma unroll
         for (int v = 0; v < V; ++v)
             cast_vec<DT, FMT, GROUP>(h[v], (v * lanes + t) * VE, a.cols, qr, sr, scale, satur);
-        if constexpr (!WAVE) __syncthreads();                   // the reductions' LDS is used again
+        if (!PF && row + next < a.rows) load(row + next);
     }
 }
 
@@ -308,43 +368,58 @@ struct NormBwdArgs {
     float* part;   // [gridDim.x][cols], or nullptr
 };
 
-template <int DT, bool WF32, int V> __global__ void __launch_bounds__(1024) k_norm_bwd(NormBwdArgs a) {
+// Waves of up to 512 threads hold the next row's dy and h meanwhile (8192 x
+// 7168 bf16: 91.8 us against 95.5 without; dh too spilled registers, 101 us).
+template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB, 4) k_norm_bwd(NormBwdArgs a) {
+    constexpr bool PF = TB <= 512 && !Weights<DT, WF32>::kWide;
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
     __shared__ float lds[2][16];
     const int T = (int)blockDim.x, t = (int)threadIdx.x;
-    float w[V][VE], acc[V][VE];
+    Weights<DT, WF32> w[V];
+    float acc[V][VE];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        ld_weight<DT, WF32>(a.w, (v * T + t) * VE, a.cols, w[v]);
+        w[v].load(a.w, (v * T + t) * VE, a.cols);
 #pragma unroll
         for (int k = 0; k < VE; ++k) acc[v][k] = 0.0f;
     }
     int flip = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+    v4u dyr[V], hr[V], dhr[V];
+    float rsn;
+    auto load = [&](int64_t row) {
         const int64_t off = row * (int64_t)a.cols * ES;
-        v4u dyr[V], hr[V], dhr[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * T + t) * VE;
             dyr[v] = ld_row<DT>((const char*)a.dy + off, c, a.cols);
             hr[v] = ld_row<DT>((const char*)a.h + off, c, a.cols);
-            if (a.dh) dhr[v] = ld_row<DT>((const char*)a.dh + off, c, a.cols);
         }
-        const float rs = a.rstd[row];
+        rsn = a.rstd[row];
+    };
+    if ((int64_t)blockIdx.x < a.rows) load(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+        const int64_t off = row * (int64_t)a.cols * ES;
+        const float rs = rsn;
         float s = 0.0f;
         float n[V][VE], dn[V][VE];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            float wv[VE];
+            w[v].widen(wv);
             widen16<DT>(dyr[v], dn[v]);
             widen16<DT>(hr[v], n[v]);
 #pragma unroll
             for (int k = 0; k < VE; ++k) {
                 n[v][k] *= rs;
                 acc[v][k] = __builtin_fmaf(dn[v][k], n[v][k], acc[v][k]);
-                dn[v][k] *= w[v][k];
+                dn[v][k] *= wv[k];
                 s = __builtin_fmaf(dn[v][k], n[v][k], s);
             }
         }
+        if (a.dh)
+#pragma unroll
+            for (int v = 0; v < V; ++v) dhr[v] = ld_row<DT>((const char*)a.dh + off, (v * T + t) * VE, a.cols);
+        if (PF && row + gridDim.x < a.rows) load(row + gridDim.x);   // in flight through the reduction and the stores
         const float mean = row_sum<false>(s, lds[flip]) / (float)a.cols;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -360,6 +435,7 @@ template <int DT, bool WF32, int V> __global__ void __launch_bounds__(1024) k_no
             }
             if (c < a.cols) st_row<DT>((char*)a.dx + off, c, a.cols, o);
         }
+        if (!PF && row + gridDim.x < a.rows) load(row + gridDim.x);
     }
     if (a.part) {
         float* p = a.part + (int64_t)blockIdx.x * a.cols;
@@ -440,6 +516,7 @@ template <int WDT> __global__ void __launch_bounds__(1024) k_norm_dw(const float
     if (rl == 0 && c < cols) store1<WDT>(dw, c, lds[0][cl]);
 }
 
+constexpr int kNormWaves = 8192;  // waves a launch of the forward pass asks for: what the chip holds at once
 constexpr int kBwdParts = 512;   // workgroups (and partial dweight rows) of the backward pass
 
 // f(bool_constant) over a runtime flag
@@ -465,15 +542,16 @@ template <int DT, int FMT> struct NormCast {
             with_bool(wf32 && DT != kF32, [&](auto W) {
                 constexpr bool GR = decltype(G)::value, WF = decltype(W)::value;
                 if (nv <= 128 && a.rows > 256) {           // short rows: a wave each, no barrier
-                    const unsigned g = grid((a.rows + 3) / 4);
-                    if (nv <= 64) k_norm_rows<DT, WF, FMT, GR, true, 1><<<g, 256, 0, st>>>(a);
-                    else k_norm_rows<DT, WF, FMT, GR, true, 2><<<g, 256, 0, st>>>(a);
+                    const unsigned g = (unsigned)std::min<int64_t>((a.rows + 3) / 4, kNormWaves / 4);
+                    if (nv <= 64) k_norm_rows<DT, WF, FMT, GR, true, 1, 256><<<g, 256, 0, st>>>(a);
+                    else k_norm_rows<DT, WF, FMT, GR, true, 2, 256><<<g, 256, 0, st>>>(a);
                 } else if (nv <= 4096) {
                     const int V = pick_v(nv), T = threads_for(nv, V);
-                    const unsigned g = grid(a.rows);
-                    if (V == 1) k_norm_rows<DT, WF, FMT, GR, false, 1><<<g, T, 0, st>>>(a);
-                    else if (V == 2) k_norm_rows<DT, WF, FMT, GR, false, 2><<<g, T, 0, st>>>(a);
-                    else k_norm_rows<DT, WF, FMT, GR, false, 4><<<g, T, 0, st>>>(a);
+                    const unsigned g = (unsigned)std::min<int64_t>(a.rows, std::max(256, kNormWaves / (T / 64) / 256 * 256));
+                    if (V == 1) k_norm_rows<DT, WF, FMT, GR, false, 1, 256><<<g, T, 0, st>>>(a);
+                    else if (V == 2 && T <= 512) k_norm_rows<DT, WF, FMT, GR, false, 2, 512><<<g, T, 0, st>>>(a);
+                    else if (V == 2) k_norm_rows<DT, WF, FMT, GR, false, 2, 1024><<<g, T, 0, st>>>(a);
+                    else k_norm_rows<DT, WF, FMT, GR, false, 4, 1024><<<g, T, 0, st>>>(a);
                 } else {
                     k_norm_long<DT, WF, FMT, GR><<<grid(a.rows), 1024, 0, st>>>(a);
                 }
@@ -489,8 +567,9 @@ template <int DT> void norm_bwd(bool wf32, const NormBwdArgs& a, unsigned g, hip
         constexpr bool WF = decltype(W)::value;
         if (nv <= 2048) {
             const int V = nv <= 256 ? 1 : 2, T = threads_for(nv, V);
-            if (V == 1) k_norm_bwd<DT, WF, 1><<<g, T, 0, st>>>(a);
-            else k_norm_bwd<DT, WF, 2><<<g, T, 0, st>>>(a);
+            if (V == 1) k_norm_bwd<DT, WF, 1, 256><<<g, T, 0, st>>>(a);
+            else if (T <= 512) k_norm_bwd<DT, WF, 2, 512><<<g, T, 0, st>>>(a);
+            else k_norm_bwd<DT, WF, 2, 1024><<<g, T, 0, st>>>(a);
         } else {
             k_norm_bwd_long<DT, WF><<<g, 1024, 0, st>>>(a);
         }

@@ -16,7 +16,8 @@
  *    whole multiples of 128 bytes).  Other pointers need only their element's
  *    alignment; 16-byte aligned ones are faster.
  *  - K, N and F are at most 2^21, M at most 2^31 (4194240 in the backward
- *    passes), and a product has fewer than 2^23 tiles of 64 x 128 outputs
+ *    passes), a product has fewer than 2^23 tiles of 64 x 128 outputs, and a
+ *    backward pass fewer than 2^24 tiles of 64 x 64 operand elements
  *    (FP8Q_EINVAL beyond).  Norms take up to 2^31 - 1 rows of up to 2^30.
  *  - A workspace is scratch for one call: its contents need no initialisation
  *    and hold nothing the caller reads.  It is 256-byte aligned, owned by the
