@@ -163,9 +163,6 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
         for (int t = 0; t < MT; ++t) sx[t] = *(const float*)(s + scale_at(t));
         const float s0 = *(const float*)(s + L::kS + 62 * 4), s1 = *(const float*)(s + L::kS + 63 * 4);
         v4i bw[4][4];
-        if constexpr (EX)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) widen_codes<WF>(b[n], bw[n]);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             if (t + PF < MT) x[t + PF] = read_x(s, t + PF);
@@ -180,15 +177,32 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
                 if (t >= MT - PF) x[t + PF] = read_x(smem + nbuf * L::kStage, t + PF - MT);
             const float f0 = sx[t] * s0, f1 = sx[t] * s1;
             v4f r[4];
+            auto add = [&](int n) {
+                const float f = n < 2 ? f0 : f1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[t][n][i] = __builtin_fmaf(r[n][i], f, acc[t][n][i]);
+            };
             if constexpr (EX) {
                 v4i xw[4];
                 widen_codes<XF>(x[t], xw);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) r[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                if (t == 0) {
+                    // each column tile is widened when its MFMAs come, so that
+                    // they start before all four are
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                    for (int n = 0; n < 4; ++n) {
+                        widen_codes<WF>(b[n], bw[n]);
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) r[n] = mfma_bf16(bw[n][k], xw[k], r[n]);
+                        for (int k = 0; k < 4; ++k) r[n] = mfma_bf16(bw[n][k], xw[k], r[n]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) r[n] = mfma_bf16(bw[n][k], xw[k], r[n]);
+                }
             } else {
 #pragma unroll
                 for (int n = 0; n < 4; ++n) r[n] = mfma_fp8<WF, XF>(b[n], x[t]);
@@ -196,11 +210,7 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
             if constexpr (decltype(NEXT)::value && BLATE)
                 if (t == MT - 1) read_b(b, smem + nbuf * L::kStage);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const float f = n < 2 ? f0 : f1;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][n][i] = __builtin_fmaf(r[n][i], f, acc[t][n][i]);
-            }
+            for (int n = 0; n < 4; ++n) add(n);
         }
         if constexpr (decltype(NEXT)::value) {
             if constexpr (!BLATE)
