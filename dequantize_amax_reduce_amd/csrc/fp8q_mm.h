@@ -169,6 +169,11 @@ __device__ __forceinline__ v4f mfma_bf16(v4i a, v4i b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ v4f mfma_f16(v4i a, v4i b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
 // 16 fp8 codes of each chunk as bf16, 8 at a time: exact for every code
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 template <int FMT> __device__ __forceinline__ void widen_codes(v8i c, v4i (&o)[4]) {

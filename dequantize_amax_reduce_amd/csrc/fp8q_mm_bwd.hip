@@ -4,14 +4,22 @@
 //   dx = [dg | du] [Wg ; Wu]                  contraction over the columns
 //   [dWg ; dWu] = [dg | du]^T X               contraction over the rows
 //
-// Both products run on one bf16 MFMA kernel (k_mm16) whose operands are
-// contiguous in the contraction, so the operands are laid out first: dz =
-// [dg | du] and its transpose, the transposed dequantized W, and the
-// transposed dequantized X.  These passes move 8-10 bytes per element of the
-// operands (5-8 % of the products' time on square problems); the products
-// then run without a transposing read.  Each operand is rounded to bf16 once,
-// which keeps the range of binary32, so gradients need no scaling.
-// Contractions are padded with zeros to 64 elements.
+// Both products run on one 16-bit MFMA kernel (k_mm16) whose operands are
+// contiguous in the contraction, so the operands are laid out first, in one
+// launch (k_prep): dz = [dg | du] and its transpose, the transposed dequantized
+// W, and the transposed dequantized X.  That pass moves 8-10 bytes per element
+// of the operands (8 % of the time of 4096 x 7168 -> 18432); the products then
+// run without a transposing read.  Contractions are padded with zeros to 64
+// elements.
+//
+// Operands are rounded to f16 (11 bits), each once, after a power of two has
+// brought their largest value just under 2^15: one exponent for dz, from the
+// largest magnitudes of dp and z, and one per 128 columns of K for W and for
+// X, from their scales (k_exps).  The exponents are taken off the sums in the
+// epilogue.  So no gradient needs scaling, and every value down to 2^-29 of
+// the largest keeps 11 bits (8 bits at 2^-32); bf16 operands, the simpler
+// choice at the same MFMA rate, gave 2.4e-3 where f16 results allow 2.1e-4,
+// and 2.9e-3 where bf16 results allow 1.7e-3.
 #include "fp8q_host.h"
 #include "fp8q_mm.h"
 
@@ -20,8 +28,8 @@ namespace fp8q {
 namespace {
 
 struct Mm16Args {
-    const uint16_t* a;     // [M, K] bf16 (row pitch K)
-    const uint16_t* b;     // [N, K] bf16
+    const uint16_t* a;     // [M, K] f16 (row pitch K)
+    const uint16_t* b;     // [N, K] f16
     int64_t M;
     int N, KB;             // KB = K / 64
     uint32_t tm, tn;
@@ -29,6 +37,8 @@ struct Mm16Args {
     void* c1;              // rows [gap, M): c1[row - gap]
     int64_t split, gap;
     int cdt, vec;
+    const int* ea;         // the exponent of a
+    const int* eb;         // of 128 rows of b (columns of c) each
 };
 
 template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Args a) {
@@ -71,7 +81,7 @@ template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Ar
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) acc[t][n] = mfma_bf16(f.b[n], f.x[t], acc[t][n]);
+            for (int n = 0; n < 4; ++n) acc[t][n] = mfma_f16(f.b[n], f.x[t], acc[t][n]);
     };
     auto step = [&](int kb, auto NEXT, auto LOAD) {
         const char* s = smem + (kb & 1) * kStage;
@@ -99,6 +109,8 @@ template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Ar
         step(kb, std::false_type{}, std::false_type{});
     }
     const int nc = n0 + wn * 32 + lr * 8;
+    const int last = (a.N - 1) >> 7;
+    const int e[2] = {-(*a.ea + a.eb[min(n0 >> 7, last)]), -(*a.ea + a.eb[min((n0 >> 7) + 1, last)])};
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int64_t row = m0 + wm * (BM / 2) + t * 16 + col;
@@ -111,7 +123,7 @@ template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Ar
         for (int half = 0; half < 2; ++half) {
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = acc[t][2 * half + (k >> 2)][k & 3];
+            for (int k = 0; k < 8; ++k) v[k] = ldexpf(acc[t][2 * half + (k >> 2)][k & 3], e[half]);
             put8(c, a.cdt, r, a.N, nc + half * 128, a.N, a.vec, v);
         }
     }
@@ -121,14 +133,14 @@ template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Ar
 // operand layout
 // ---------------------------------------------------------------------------
 
+typedef unsigned int v4u_a2 __attribute__((ext_vector_type(4), aligned(2)));
+
 // A 64 (rows) x 64 (columns) tile transposed through LDS as pairs of rows:
 // word [c][i] holds column c of rows 2i and 2i + 1.  The pitch of 33 words
 // spreads both the column-wise writes and the row-wise reads over the banks.
 struct TileT {
     uint32_t w[64][33];
 };
-
-typedef unsigned int v4u_a2 __attribute__((ext_vector_type(4), aligned(2)));
 
 // 8 elements from column c of a row (zero from column `cols` on)
 template <int DT> __device__ __forceinline__ void ld8(const uint16_t* row, int c, int cols, float* v) {
@@ -157,6 +169,85 @@ __device__ __forceinline__ void store_t(const TileT& t, uint16_t* dst, int64_t p
     *(v4u*)(d + 8) = v4u{s[4], s[5], s[6], s[7]};
 }
 
+// ---------------------------------------------------------------------------
+// exponents
+// ---------------------------------------------------------------------------
+
+// the largest finite |v| of 16-bit values, as binary32 bits
+template <int DT> __device__ __forceinline__ uint32_t finite_bits(uint32_t b) {
+    b &= 0x7FFFu;
+    return b < (DT == kBF16 ? 0x7F80u : 0x7C00u) ? abs16_to_f32bits<DT>(b) : 0u;
+}
+// floor(log2) of a positive finite binary32 (0 for 0)
+__device__ __forceinline__ int log2_of(uint32_t bits) { return bits ? ilogbf(__uint_as_float(bits)) : 0; }
+
+// dz = dz' 2^-e with |dz'| < 2^15: |dy| < 2^(p + 1); |dg|, |du| <= 1.13 |dp| |z|
+// < 2^(p + z + 3), the activations' slopes being at most 1.13
+__device__ __forceinline__ int dz_exponent(uint32_t p, uint32_t z, bool gated) {
+    if (p == 0 || (gated && z == 0)) return 0;
+    return gated ? 12 - log2_of(p) - log2_of(z) : 14 - log2_of(p);
+}
+
+struct ExpArgs {
+    const uint16_t* dy;
+    const uint16_t* z;     // or nullptr
+    int64_t ndy, nz;       // their elements; 0: the exponent stays 0
+    uint32_t* top;         // [3]: the largest finite |dy| and |z|, zeroed before, and dz's exponent
+    uint32_t gdy;          // workgroups of that part
+    const float* xs;       // [M, KB]
+    int64_t M;
+    const float* ws0;      // [nb, KB] each
+    const float* ws1;      // or nullptr
+    int nb, KB;
+    int* ex;               // [KB] exponents of X
+    int* ew;               // [KB] of W
+    int qx, qw;            // bits above 1 of the formats' largest values
+};
+
+template <int DT> __global__ void __launch_bounds__(256) k_exps(ExpArgs a) {
+    __shared__ uint32_t lds4[4];
+    if (blockIdx.x < a.gdy) {
+        for (int which = 0; which < 2; ++which) {
+            const uint16_t* p = which ? a.z : a.dy;
+            const int64_t n = which ? a.nz : a.ndy, step = (int64_t)a.gdy * 256 * 8;
+            uint32_t m = 0;
+            for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += step) {
+                union { v4u q; uint16_t e[8]; } u;
+                if (i + 8 <= n) {
+                    const v4u_a2 r = *(const v4u_a2*)(p + i);
+                    u.q = v4u{r.x, r.y, r.z, r.w};
+                } else {
+                    u.q = v4u{0, 0, 0, 0};
+                    for (int k = 0; k < 8; ++k)
+                        if (i + k < n) u.e[k] = p[i + k];
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m = umax(m, finite_bits<DT>(u.e[k]));
+            }
+            m = block_max256(m, lds4);
+            if (threadIdx.x == 0 && m) atomicMax(a.top + which, m);   // order-independent
+        }
+        return;
+    }
+    const int kb = (int)(blockIdx.x - a.gdy);
+    auto top = [&](const float* s, int64_t rows) {
+        uint32_t m = 0;
+        for (int64_t r = threadIdx.x; r < rows; r += 256) {
+            const uint32_t b = __float_as_uint(s[r * a.KB + kb]) & 0x7FFFFFFFu;
+            m = umax(m, b < 0x7F800000u ? b : 0u);
+        }
+        return block_max256(m, lds4);
+    };
+    const uint32_t mx = top(a.xs, a.M);
+    uint32_t mw = top(a.ws0, a.nb);
+    if (a.ws1) mw = umax(mw, top(a.ws1, a.nb));
+    if (threadIdx.x == 0) {
+        if (a.gdy == 0 && kb == 0) a.top[0] = a.top[1] = a.top[2] = 0;
+        a.ex[kb] = 14 - a.qx - log2_of(mx);
+        a.ew[kb] = 14 - a.qw - log2_of(mw);
+    }
+}
+
 struct DzArgs {
     const uint16_t* dy;
     const uint16_t* z;
@@ -165,6 +256,8 @@ struct DzArgs {
     int act;
     uint16_t* dz;          // [M, gated ? 2 Np : Np], or nullptr
     uint16_t* dzt;         // [gated ? 2 Np : Np, Mp], or nullptr
+    const uint32_t* top;   // largest |dy|, |z|
+    int* ez;               // the exponent, for the products
 };
 
 // dz and its transpose; 256 threads, one 64 x 64 tile a workgroup; thread
@@ -174,6 +267,8 @@ template <int DT, bool GATED> __device__ __forceinline__ void dz_tile(const DzAr
     const int v = (int)threadIdx.x & 7, i = (int)threadIdx.x >> 3;
     const int64_t m = (int64_t)by * 64 + 2 * i;
     const int c = (int)bx * 64 + v * 8;
+    const int ez = dz_exponent(a.top[0], a.top[1], GATED);
+    if (bx == 0 && by == 0 && threadIdx.x == 0) *a.ez = ez;
     const int64_t zp = 2 * (int64_t)a.N, dp = GATED ? 2 * (int64_t)a.Np : a.Np;
     float g[2][8], u[2][8];
 #pragma unroll
@@ -190,21 +285,23 @@ template <int DT, bool GATED> __device__ __forceinline__ void dz_tile(const DzAr
                 for (int k = 0; k < 8; ++k) {
                     float f, d;
                     act_both(a.act, zg[k], &f, &d);
-                    u[r][k] = c + k < a.N ? g[r][k] * f : 0.0f;
+                    u[r][k] = c + k < a.N ? ldexpf(g[r][k] * f, ez) : 0.0f;
                     g[r][k] = c + k < a.N ? g[r][k] * zu[k] * d : 0.0f;
                 }
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) g[r][k] = ldexpf(g[r][k], ez);
             if (a.dz) {
-                *(v4u*)(a.dz + (m + r) * dp + c) = pack_out16<kBF16>(g[r]);
-                if constexpr (GATED) *(v4u*)(a.dz + (m + r) * dp + a.Np + c) = pack_out16<kBF16>(u[r]);
+                *(v4u*)(a.dz + (m + r) * dp + c) = pack_out16<kF16>(g[r]);
+                if constexpr (GATED) *(v4u*)(a.dz + (m + r) * dp + a.Np + c) = pack_out16<kF16>(u[r]);
             }
         }
     }
     if (!a.dzt) return;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        tg.w[v * 8 + k][i] = pack_bf16x2(g[0][k], g[1][k]);
-        if constexpr (GATED) tu.w[v * 8 + k][i] = pack_bf16x2(u[0][k], u[1][k]);
+        tg.w[v * 8 + k][i] = pack_f16x2(g[0][k], g[1][k]);
+        if constexpr (GATED) tu.w[v * 8 + k][i] = pack_f16x2(u[0][k], u[1][k]);
     }
     __syncthreads();
     uint16_t* d = a.dzt + (int64_t)bx * 64 * a.Mp;
@@ -219,6 +316,7 @@ struct DeqTArgs {
     int KB, sh;
     uint16_t* t;           // [K, pitch], this matrix from element `at` of a row
     int64_t pitch, at;
+    const int* e;          // [KB] exponents
 };
 
 // The transposed dequantized matrix: 64 rows x 128 codes a workgroup; thread
@@ -232,7 +330,7 @@ template <int FMT> __device__ __forceinline__ void deq_tile(const DeqTArgs& a, u
     for (int r = 0; r < 2; ++r) {
         if (r0 + r < a.R) {
             const v4u c = *(const v4u*)(a.q + (r0 + r) * K + (int64_t)bx * 128 + v * 16);
-            const float s = a.s[((r0 + r) >> a.sh) * a.KB + bx];
+            const float s = ldexpf(a.s[((r0 + r) >> a.sh) * a.KB + bx], a.e[bx]);
             dec4<FMT>(c.x, f[r]);
             dec4<FMT>(c.y, f[r] + 4);
             dec4<FMT>(c.z, f[r] + 8);
@@ -245,7 +343,7 @@ template <int FMT> __device__ __forceinline__ void deq_tile(const DeqTArgs& a, u
         }
     }
 #pragma unroll
-    for (int k = 0; k < 16; ++k) t[v >> 2].w[(v & 3) * 16 + k][i] = pack_bf16x2(f[0][k], f[1][k]);
+    for (int k = 0; k < 16; ++k) t[v >> 2].w[(v & 3) * 16 + k][i] = pack_f16x2(f[0][k], f[1][k]);
     __syncthreads();
     uint16_t* d = a.t + (int64_t)bx * 128 * a.pitch;
     store_t(t[0], d, a.pitch, a.at + (int64_t)by * 64);
@@ -289,8 +387,8 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // c[m, n] = sum_k a[m, k] b[n, k]; rows [0, split) to c0, rows from gap to c1
 void mm16(const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K, void* c0, void* c1, int64_t split,
-          int64_t gap, int cdt, hipStream_t st) {
-    Mm16Args a{A, B, M, (int)N, (int)(K / 64), 0, 0, c0, c1, split, gap, cdt, 0};
+          int64_t gap, int cdt, const int* ea, const int* eb, hipStream_t st) {
+    Mm16Args a{A, B, M, (int)N, (int)(K / 64), 0, 0, c0, c1, split, gap, cdt, 0, ea, eb};
     a.vec = N % 8 == 0 && al(c0, 16) && (!c1 || al(c1, 16));
     a.tn = (uint32_t)((N + 255) / 256);
     // The tile height with the fewest rounds of 256 workgroups, each weighted
@@ -319,7 +417,7 @@ template <typename F> void with_fmt(int f, F&& go) {
 
 struct BwdLayout {
     int64_t Mp, Np, C;     // padded rows and columns; C: columns of dz
-    int64_t dz, dzt, wt, xt, bytes;
+    int64_t dz, dzt, wt, xt, exps, bytes;   // exps: [2] largest magnitudes, the exponent of dz, then [K/128] of X and of W
 };
 BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated) {
     BwdLayout l;
@@ -332,6 +430,7 @@ BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated) {
     l.dzt = take(l.C * l.Mp);
     l.wt = take(K * l.C);
     l.xt = take(K * l.Mp);
+    l.exps = take(2 * (4 + K / 64));
     l.bytes = at;
     return l;
 }
@@ -361,14 +460,25 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
              *xt = (uint16_t*)(ws + l.xt);
     const int KB = f.K / 128;
     const bool wdx = f.dx != nullptr, wdw = f.dw0 != nullptr;
-    // a bf16 gradient whose rows are whole 128-byte steps is dz already
-    const bool direct = !gated && f.dt == kBF16 && f.N % 64 == 0 && al(f.dy, 16);
+    uint32_t* top = (uint32_t*)(ws + l.exps);
+    int *ez = (int*)top + 2, *ex = (int*)top + 4, *ew = ex + KB;
+    // an f16 gradient keeps its exponent (0), and one whose rows are whole
+    // 128-byte steps is dz already
+    const bool plain = !gated && f.dt == kF16, direct = plain && f.N % 64 == 0 && al(f.dy, 16);
+    if (!plain) launch_zero16(top, 6, st);                  // else k_exps clears them
+    const int64_t ndy = plain ? 0 : f.M * f.N, nz = gated ? 2 * ndy : 0;
+    const int qx = f.xfmt == kE4M3 ? 9 : 16, qw = f.wfmt == kE4M3 ? 9 : 16;   // 448 < 2^9, 57344 < 2^16
+    const ExpArgs ea{(const uint16_t*)f.dy, (const uint16_t*)f.z, ndy, nz, top,
+                     (uint32_t)std::min<int64_t>((std::max(ndy, nz) + 2047) / 2048, 1024), f.xs, f.M, f.ws0,
+                     gated ? f.ws1 : nullptr, (f.N + 127) / 128, KB, ex, ew, qx, qw};
+    if (f.dt == kBF16) k_exps<kBF16><<<ea.gdy + KB, 256, 0, st>>>(ea);
+    else k_exps<kF16><<<ea.gdy + KB, 256, 0, st>>>(ea);
     PrepArgs p{};
     p.dz = DzArgs{(const uint16_t*)f.dy, (const uint16_t*)f.z, f.M, l.Mp, f.N, (int)l.Np, f.act,
-                  wdx && !direct ? dz : nullptr, wdw ? dzt : nullptr};
-    p.x = DeqTArgs{f.x, f.xs, f.M, KB, 0, xt, l.Mp, 0};
-    p.w0 = DeqTArgs{f.w0, f.ws0, f.N, KB, 7, wt, l.C, 0};
-    p.w1 = DeqTArgs{f.w1, f.ws1, f.N, KB, 7, wt, l.C, l.Np};
+                  wdx && !direct ? dz : nullptr, wdw ? dzt : nullptr, top, ez};
+    p.x = DeqTArgs{f.x, f.xs, f.M, KB, 0, xt, l.Mp, 0, ex};
+    p.w0 = DeqTArgs{f.w0, f.ws0, f.N, KB, 7, wt, l.C, 0, ew};
+    p.w1 = DeqTArgs{f.w1, f.ws1, f.N, KB, 7, wt, l.C, l.Np, ew};
     p.dzx = (uint32_t)(l.Np / 64);
     const uint32_t row_tiles = (uint32_t)(l.Mp / 64), w_tiles = wdx ? (uint32_t)KB * p.dzx : 0;
     p.e0 = p.dz.dz || p.dz.dzt ? p.dzx * row_tiles : 0;
@@ -387,10 +497,10 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
             }
         });
     });
-    if (wdx) mm16(direct ? (const uint16_t*)f.dy : dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, st);
+    if (wdx) mm16(direct ? (const uint16_t*)f.dy : dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, ez, ew, st);
     if (wdw) {
-        if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, st);
-        else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, st);
+        if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, ez, ex, st);
+        else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, ez, ex, st);
     }
 }
 

@@ -36,9 +36,12 @@
  *    block's largest product (up to 4e-5 of the sum's rms measured).
  *  - Every sum has a fixed order: the same call gives the same bits.
  *  - NaN and infinities follow the formulas (0 * inf is NaN).
- *  - Backward products take their operands in bf16 (the gradient, and the
- *    dequantized X and W, each rounded once) and sum in binary32; see each
- *    entry point.
+ *  - Backward products take their operands in f16 (the gradient, and the
+ *    dequantized X and W, each rounded once after a power of two has brought its
+ *    largest finite value just under 2^15: one exponent for the gradient, one
+ *    per 128 columns of K for X and for W) and sum in binary32.  The exponents
+ *    are taken off the sums, so gradients of any magnitude need no scaling;
+ *    values down to 2^-29 of the largest keep 11 bits.
  *  - The gradient of a cast is the identity: gradients are those of the
  *    formulas at the values the codes stand for.
  */
@@ -109,9 +112,8 @@ fp8q_status_t fp8q_linear(const uint8_t* x, fp8q_fmt_t xfmt, const float* x_scal
 /*
  * Its backward: dx [M, K] = dy W, dw [N, K] = dy^T X.  dy is bf16 or f16
  * (FP8Q_F32 -> FP8Q_EDTYPE); dx has dy's type; dw has dwdtype: dy's type or
- * FP8Q_F32.  Either of dx and dw may be NULL (not computed).  dy, X and W are
- * rounded to bf16 (no scaling of the gradient is needed), the sums are
- * binary32.  M == 0 writes dw = 0; N == 0 writes dx = 0.
+ * FP8Q_F32.  Either of dx and dw may be NULL (not computed).
+ * M == 0 writes dw = 0; N == 0 writes dx = 0.
  * workspace: fp8q_linear_backward_workspace_bytes(M, N, K) bytes.
  */
 size_t fp8q_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
@@ -146,7 +148,7 @@ fp8q_status_t fp8q_gated_linear_cast(const uint8_t* x, fp8q_fmt_t xfmt, const fl
 
 /*
  * Its backward, from dp [M, F] (the gradient of p) and the forward's z:
- *   dg = dp * u * act'(g), du = dp * act(g)  (binary32, rounded to bf16);
+ *   dg = dp * u * act'(g), du = dp * act(g)  (binary32, then an operand);
  *   dx [M, K] = dg Wg + du Wu;  dw_gate [F, K] = dg^T X;  dw_up = du^T X.
  * dp and z have dtype, bf16 or f16; dx too; dw_gate and dw_up have dwdtype
  * (dtype or FP8Q_F32).  dx may be NULL, and dw_gate and dw_up may both be.
