@@ -39,9 +39,23 @@ struct Mm16Args {
     int cdt, vec;
     const int* ea;         // the exponent of a
     const int* eb;         // of 128 rows of b (columns of c) each
+    int kper, splits;      // steps a split takes
+    float* part;           // [splits][M][N] sums as they are, where splits > 1
 };
 
-template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Args a) {
+// row of c0 or c1 that row `row` of the product is, or none (padding)
+__device__ __forceinline__ bool out_row(const Mm16Args& a, int64_t row, void** c, int64_t* r) {
+    if (row < a.split) {
+        *c = a.c0;
+        *r = row;
+        return true;
+    }
+    *c = a.c1;
+    *r = row - a.gap;
+    return row >= a.gap && row < a.M;
+}
+
+template <int BM, bool PART> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Args a) {
     constexpr int MT = BM / 32, kStage = (BM + kMmBN) * 128;
     __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
     const int lane = threadIdx.x & 63;
@@ -83,29 +97,31 @@ template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Ar
 #pragma unroll
             for (int n = 0; n < 4; ++n) acc[t][n] = mfma_f16(f.b[n], f.x[t], acc[t][n]);
     };
+    const int kb0 = PART ? (int)blockIdx.y * a.kper : 0, kb1 = PART ? min(a.KB, kb0 + a.kper) : a.KB;
     auto step = [&](int kb, auto NEXT, auto LOAD) {
-        const char* s = smem + (kb & 1) * kStage;
+        const int cur = (kb - kb0) & 1;
+        const char* s = smem + cur * kStage;
         read(f1, s, c1);
         __builtin_amdgcn_sched_barrier(0);
         mul(f0);
         __builtin_amdgcn_sched_barrier(0);
         dma_wait<0>();
         wg_barrier();
-        if constexpr (decltype(LOAD)::value) ld.issue(lds0 + (kb & 1) * kStage, kb + 2);
-        if constexpr (decltype(NEXT)::value) read(f0, smem + ((kb & 1) ^ 1) * kStage, c0);
+        if constexpr (decltype(LOAD)::value) ld.issue(lds0 + cur * kStage, kb + 2);
+        if constexpr (decltype(NEXT)::value) read(f0, smem + (cur ^ 1) * kStage, c0);
         __builtin_amdgcn_sched_barrier(0);
         mul(f1);
         __builtin_amdgcn_sched_barrier(0);
     };
-    if (a.KB > 0) {
-        ld.issue(lds0, 0);
+    if (kb0 < kb1) {
+        ld.issue(lds0, kb0);
         dma_wait<0>();
         wg_barrier();
-        if (a.KB > 1) ld.issue(lds0 + kStage, 1);
+        if (kb1 - kb0 > 1) ld.issue(lds0 + kStage, kb0 + 1);
         read(f0, smem, c0);
-        int kb = 0;
-        for (; kb < a.KB - 2; ++kb) step(kb, std::true_type{}, std::true_type{});
-        if (kb < a.KB - 1) step(kb++, std::true_type{}, std::false_type{});
+        int kb = kb0;
+        for (; kb < kb1 - 2; ++kb) step(kb, std::true_type{}, std::true_type{});
+        if (kb < kb1 - 1) step(kb++, std::true_type{}, std::false_type{});
         step(kb, std::false_type{}, std::false_type{});
     }
     const int nc = n0 + wn * 32 + lr * 8;
@@ -114,11 +130,20 @@ template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Ar
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int64_t row = m0 + wm * (BM / 2) + t * 16 + col;
+        if constexpr (PART) {
+            if (row >= a.M) continue;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = acc[t][2 * half + (k >> 2)][k & 3];
+                put8(a.part + (int64_t)blockIdx.y * a.M * a.N, kF32, row, a.N, nc + half * 128, a.N, true, v);
+            }
+            continue;
+        }
         void* c;
         int64_t r;
-        if (row < a.split) { c = a.c0; r = row; }
-        else if (row >= a.gap && row < a.M) { c = a.c1; r = row - a.gap; }
-        else continue;
+        if (!out_row(a, row, &c, &r)) continue;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float v[8];
@@ -126,6 +151,35 @@ template <int BM> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Ar
             for (int k = 0; k < 8; ++k) v[k] = ldexpf(acc[t][2 * half + (k >> 2)][k & 3], e[half]);
             put8(c, a.cdt, r, a.N, nc + half * 128, a.N, a.vec, v);
         }
+    }
+}
+
+// the end of a split product: the partial sums in order; a thread takes 8
+// columns (the columns are a multiple of 128)
+__global__ void __launch_bounds__(256) k_mm16_join(Mm16Args a) {
+    const int64_t per = a.N / 8, total = a.M * per, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
+        const int64_t row = i / per;
+        const int n = (int)(i - row * per) * 8;
+        void* c;
+        int64_t r;
+        if (!out_row(a, row, &c, &r)) continue;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        const float* p = a.part + row * a.N + n;
+        for (int s = 0; s < a.splits; ++s, p += a.M * a.N) {
+            const v4f x = *(const v4f*)p, y = *(const v4f*)(p + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[k] += x[k];
+                v[4 + k] += y[k];
+            }
+        }
+        const int e = -(*a.ea + a.eb[n >> 7]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = ldexpf(v[k], e);
+        put8(c, a.cdt, r, a.N, n, a.N, a.vec, v);
     }
 }
 
@@ -385,29 +439,53 @@ void zero(void* p, int64_t n, int dt, hipStream_t st) {
 int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// c[m, n] = sum_k a[m, k] b[n, k]; rows [0, split) to c0, rows from gap to c1
-void mm16(const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K, void* c0, void* c1, int64_t split,
-          int64_t gap, int cdt, const int* ea, const int* eb, hipStream_t st) {
-    Mm16Args a{A, B, M, (int)N, (int)(K / 64), 0, 0, c0, c1, split, gap, cdt, 0, ea, eb};
-    a.vec = N % 8 == 0 && al(c0, 16) && (!c1 || al(c1, 16));
-    a.tn = (uint32_t)((N + 255) / 256);
-    // The tile height with the fewest rounds of 256 workgroups, each weighted
-    // with its measured time: 1, 0.58 and 0.32 at heights 256, 128 and 64
-    // (4096 x 8192 outputs of 4096-long sums: 200, 232 and 256 us).
-    int bm = 256;
+// The tile height and the split of the contraction with the least estimated
+// time: a round of 256 workgroups takes the measured microseconds below per
+// step of 64 (4096 x 8192 outputs of 4096-long sums: 200, 232 and 256 us at
+// heights 256, 128 and 64) and about 4 to fill and drain; a split writes
+// binary32 sums that the join reads, at about 5 TB/s and a launch.
+struct Plan16 {
+    int bm, splits, kper;
+    int64_t part;          // bytes of partial sums
+};
+Plan16 plan16(int64_t M, int64_t N, int64_t K) {
+    Plan16 p{};
+    const int64_t KB = K / 64, tn = (N + 255) / 256;
     double best = 0.0;
     for (int h = 256; h >= 64; h /= 2) {
-        const int64_t tiles = (M + h - 1) / h * a.tn;
-        const double t = (double)((tiles + 255) / 256) * (h == 256 ? 1.0 : h == 128 ? 0.58 : 0.32);
-        if (best > 0.0 && t >= best) continue;
-        best = t;
-        bm = h;
+        const double each = h == 256 ? 1.56 : h == 128 ? 0.90 : 0.50;
+        const int64_t tiles = (M + h - 1) / h * tn;
+        for (int64_t s = 1; s == 1 || (s <= 32 && tiles * s <= 512 && KB / s >= 4); s *= 2) {
+            const int64_t kper = (KB + s - 1) / s, n = (KB + kper - 1) / kper;
+            const double t = (double)((tiles * n + 255) / 256) * ((double)kper * each + 4.0) +
+                             (n > 1 ? 3.0 + (double)(n * M * N * 8) / 5e6 : 0.0);
+            if (best > 0.0 && t >= best) continue;
+            best = t;
+            p = Plan16{h, (int)n, (int)kper, n > 1 ? n * M * N * 4 : 0};
+        }
     }
-    a.tm = (uint32_t)((M + bm - 1) / bm);
-    const unsigned g = a.tm * a.tn;
-    if (bm == 256) k_mm16<256><<<g, kMmThreads, 0, st>>>(a);
-    else if (bm == 128) k_mm16<128><<<g, kMmThreads, 0, st>>>(a);
-    else k_mm16<64><<<g, kMmThreads, 0, st>>>(a);
+    return p;
+}
+
+// c[m, n] = sum_k a[m, k] b[n, k]; rows [0, split) to c0, rows from gap to c1;
+// N % 128 == 0
+void mm16(const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K, void* c0, void* c1, int64_t split,
+          int64_t gap, int cdt, const int* ea, const int* eb, float* part, hipStream_t st) {
+    const Plan16 p = plan16(M, N, K);
+    Mm16Args a{A, B, M, (int)N, (int)(K / 64), 0, 0, c0, c1, split, gap, cdt, 0, ea, eb, p.kper, p.splits, part};
+    a.vec = al(c0, 16) && (!c1 || al(c1, 16));
+    a.tn = (uint32_t)((N + 255) / 256);
+    a.tm = (uint32_t)((M + p.bm - 1) / p.bm);
+    const dim3 g(a.tm * a.tn, (unsigned)p.splits);
+    auto go = [&](auto BMc) {
+        constexpr int BM = decltype(BMc)::value;
+        if (p.splits > 1) k_mm16<BM, true><<<g, kMmThreads, 0, st>>>(a);
+        else k_mm16<BM, false><<<g, kMmThreads, 0, st>>>(a);
+    };
+    if (p.bm == 256) go(KC<256>{});
+    else if (p.bm == 128) go(KC<128>{});
+    else go(KC<64>{});
+    if (p.splits > 1) k_mm16_join<<<(unsigned)std::min<int64_t>((M * (N / 8) + 255) / 256, 4096), 256, 0, st>>>(a);
 }
 
 template <typename F> void with_fmt(int f, F&& go) {
@@ -417,7 +495,7 @@ template <typename F> void with_fmt(int f, F&& go) {
 
 struct BwdLayout {
     int64_t Mp, Np, C;     // padded rows and columns; C: columns of dz
-    int64_t dz, dzt, wt, xt, exps, bytes;   // exps: [2] largest magnitudes, the exponent of dz, then [K/128] of X and of W
+    int64_t dz, dzt, wt, xt, exps, part, bytes;   // part: the products' partial sums; exps: [2] largest magnitudes, the exponent of dz, then [K/128] of X and of W
 };
 BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated) {
     BwdLayout l;
@@ -431,6 +509,7 @@ BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated) {
     l.wt = take(K * l.C);
     l.xt = take(K * l.Mp);
     l.exps = take(2 * (4 + K / 64));
+    l.part = take(std::max(plan16(M, K, l.C).part, plan16(gated ? l.Np + N : N, K, l.Mp).part) / 2);
     l.bytes = at;
     return l;
 }
@@ -458,6 +537,7 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
     char* ws = (char*)f.ws;
     uint16_t *dz = (uint16_t*)(ws + l.dz), *dzt = (uint16_t*)(ws + l.dzt), *wt = (uint16_t*)(ws + l.wt),
              *xt = (uint16_t*)(ws + l.xt);
+    float* part = (float*)(ws + l.part);
     const int KB = f.K / 128;
     const bool wdx = f.dx != nullptr, wdw = f.dw0 != nullptr;
     uint32_t* top = (uint32_t*)(ws + l.exps);
@@ -497,10 +577,10 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
             }
         });
     });
-    if (wdx) mm16(direct ? (const uint16_t*)f.dy : dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, ez, ew, st);
+    if (wdx) mm16(direct ? (const uint16_t*)f.dy : dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, ez, ew, part, st);
     if (wdw) {
-        if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, ez, ex, st);
-        else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, ez, ex, st);
+        if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, ez, ex, part, st);
+        else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, ez, ex, part, st);
     }
 }
 
