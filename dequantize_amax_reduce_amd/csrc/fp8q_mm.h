@@ -1,9 +1,9 @@
 // fp8q_mm.h -- the tiled matrix products of the feed-forward operators.
 //
-// One pipeline serves the fp8 forward products and the bf16 backward ones.
+// One loader serves the fp8 forward products and the f16 backward ones.
 // Both are C[m, n] = sum_k A[m, k] B[n, k] with rows of A ("tokens") and of B
 // ("columns") contiguous in k, and both move 128 bytes of every row per step:
-// 128 fp8 codes or 64 bf16 values.
+// 128 fp8 codes or 64 f16 values.
 //
 //  - A workgroup of 8 waves owns BM rows of A by 256 rows of B.  Wave (wm, wn)
 //    of the 2 x 4 grid owns BM/2 rows of A and 64 of B: 32 from each half of
@@ -41,16 +41,13 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 constexpr int kMmThreads = 512;
 constexpr int kMmBN = 256;
 
-// 16 (or 4) bytes a lane from base + voff to LDS at lds + lane * 16 (or 4).
-// base and lds are wave-uniform.  Written as asm because the compiler would
-// otherwise wait for every load in flight before each LDS read; nothing is
-// returned in registers, and the pipeline waits with dma_wait.
+// 16 bytes a lane from base + voff to LDS at lds + lane * 16 (lds_dma4_at: 4
+// bytes from the lane's own address).  base and lds are wave-uniform.  Written
+// as asm because the compiler would otherwise wait for every load in flight
+// before each LDS read; nothing is returned in registers, and the pipeline
+// waits with dma_wait.
 __device__ __forceinline__ void lds_dma16(uint32_t lds, uint32_t voff, const void* base) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base)
-                 : "memory");
-}
-__device__ __forceinline__ void lds_dma4(uint32_t lds, uint32_t voff, const void* base) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base)
                  : "memory");
 }
 __device__ __forceinline__ void lds_dma4_at(uint32_t lds, const void* addr) {   // a lane's own address
@@ -68,13 +65,6 @@ __device__ __forceinline__ void wg_barrier() {
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
-__device__ __forceinline__ const void* uniform_ptr(const void* p) {
-    const uint64_t u = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
-    return (const void*)(((uint64_t)hi << 32) | lo);
-}
-
 // Workgroup -> tile.  Workgroup i runs on XCD i mod 8; each XCD takes one
 // contiguous run of the tile order, which walks groups of 8 row tiles column
 // by column, so the 32 workgroups an XCD runs at once share 8 A tiles and 4 B
@@ -150,12 +140,6 @@ template <int BM> struct TileLoad {
 // two 16-byte chunks of LDS as one fragment
 __device__ __forceinline__ v8i frag(const char* p0, const char* p1) {
     const v4i a = *(const v4i*)p0, b = *(const v4i*)p1;
-    return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-}
-
-// the same from memory, for data read once
-__device__ __forceinline__ v8i frag_nt(const char* p0, const char* p1) {
-    const v4i a = __builtin_nontemporal_load((const v4i*)p0), b = __builtin_nontemporal_load((const v4i*)p1);
     return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 

@@ -243,7 +243,11 @@ def test_norm_backward(rows, cols, dt, dh, wf32):
     wdt = "f32" if wf32 else dt
     wantw = (dy.to(D) * n).sum(0)
     near(dw, wantw, out_tol(wantw, wdt, (dy.to(D) * n).abs().sum(0) * (rows + 4) * e), "dweight")
-    # again, in place over dy, without dweight: the same dx
+    # again, in place over dh or dy, without dweight: the same dx
+    if dh:
+        dhd = up(dhv)
+        fq.fp8q_rmsnorm_backward(up(dy), up(h), up(w), up(rstd), dhd, None, dhd)
+        assert torch.equal(dhd, dx)
     dyd = up(dy)
     fq.fp8q_rmsnorm_backward(dyd, up(h), up(w), up(rstd), dyd, None, up(dhv) if dh else None)
     assert torch.equal(dyd, dx)
