@@ -495,7 +495,10 @@ template <typename F> void with_fmt(int f, F&& go) {
 
 struct BwdLayout {
     int64_t Mp, Np, C;     // padded rows and columns; C: columns of dz
-    int64_t dz, dzt, wt, xt, exps, part, bytes;   // part: the products' partial sums; exps: [2] largest magnitudes, the exponent of dz, then [K/128] of X and of W
+    int64_t dz, dzt, wt, xt;
+    int64_t exps;          // two largest magnitudes, the exponent of dz, then [K / 128] of X and of W
+    int64_t part;          // the products' partial sums
+    int64_t bytes;
 };
 BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated) {
     BwdLayout l;

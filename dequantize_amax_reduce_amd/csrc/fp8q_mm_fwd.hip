@@ -378,7 +378,8 @@ template <int MP, int BT> struct RowsLds {
 };
 
 // MP: 8-row pieces of X (1 or 2)
-template <int XF, int WF, int MP, int BT, bool GATED> __global__ void __launch_bounds__(512) k_mm_rows(FwdArgs a, float* pbuf) {
+template <int XF, int WF, int MP, int BT, bool GATED>
+__global__ void __launch_bounds__(512) k_mm_rows(FwdArgs a, float* pbuf) {
     using L = RowsLds<MP, BT>;
     constexpr int D = L::kStages, C = GATED ? 8 * BT : 16 * BT;   // columns a tile
     __shared__ __attribute__((aligned(1024))) char smem[8 * D * L::kStage + L::kRed];

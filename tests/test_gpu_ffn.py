@@ -144,8 +144,9 @@ def test_norm_group(rows, cols, dt, res, fmt, wf32):
 
 
 @pytest.mark.parametrize("rows,cols,dt,res", [(1, 1, "bf16", True), (4, 7, "f32", False), (300, 333, "f16", True),
-                                              (260, 129, "bf16", False), (5, 5001, "f32", True), (3, 8195, "bf16", True),
-                                              (2, 40001, "f16", True), (2, 33333, "f32", False), (1000, 64, "bf16", True)])
+                                              (260, 129, "bf16", False), (5, 5001, "f32", True),
+                                              (3, 8195, "bf16", True), (2, 40001, "f16", True),
+                                              (2, 33333, "f32", False), (1000, 64, "bf16", True)])
 @pytest.mark.parametrize("fmt,wf32", [("e4m3fn", True), ("e5m2", False)])
 def test_norm_per_channel(rows, cols, dt, res, fmt, wf32):
     _norm_case(rows, cols, dt, res, fmt, wf32, False)
@@ -283,7 +284,8 @@ def test_norm_gradient_against_differences():
 # rows that reach every tiling: one row, the few-row kernels' 16, 32 and 64,
 # the first tiled row count, split contractions, and tiles of 64, 128 and 256
 LINEAR = [(1, 128, 1), (1, 7168, 33), (15, 1152, 130), (17, 256, 16), (33, 1152, 257), (64, 2176, 100),
-          (65, 256, 129), (70, 4096, 128), (200, 4224, 300), (1000, 512, 3001), (1700, 384, 4104), (4200, 128, 4096)]
+          (65, 256, 129), (70, 4096, 128), (200, 4224, 300), (1000, 512, 3001), (1700, 384, 4104), (4200, 128, 4096),
+          (5, 384, 9001), (13, 1280, 8500)]                # more tiles of few rows than workgroups
 
 
 @pytest.mark.parametrize("M,K,N", LINEAR)
@@ -300,7 +302,7 @@ def test_linear(M, K, N, dt, xf, wf):
 
 
 GATED = [(1, 128, 1), (1, 7168, 40), (16, 1152, 130), (31, 256, 384), (50, 1152, 300), (64, 384, 256), (65, 256, 256),
-         (100, 2048, 131), (90, 4096, 128), (1000, 512, 1501), (3000, 384, 2176)]
+         (100, 2048, 131), (90, 4096, 128), (1000, 512, 1501), (3000, 384, 2176), (3, 256, 4501), (12, 1152, 4400)]
 
 
 @pytest.mark.parametrize("M,K,F", GATED)
