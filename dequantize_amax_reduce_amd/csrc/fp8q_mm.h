@@ -45,14 +45,21 @@ constexpr int kMmBN = 256;
 // bytes from the lane's own address).  base and lds are wave-uniform.  Written
 // as asm because the compiler would otherwise wait for every load in flight
 // before each LDS read; nothing is returned in registers, and the pipeline
-// waits with dma_wait.
+// waits with dma_wait.  The LDS address goes through m0, which is named as
+// clobbered: the compiler writes m0 for uses of its own, and would keep such a
+// value across the asm.  It warns that m0 is a reserved register, which is that
+// it never allocates m0 to a value.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_dma16(uint32_t lds, uint32_t voff, const void* base) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void lds_dma4_at(uint32_t lds, const void* addr) {   // a lane's own address
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(addr) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(addr)
+                 : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // all but this wave's N newest LDS loads have landed, and its LDS reads have returned
 template <int N = 0> __device__ __forceinline__ void dma_wait() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
