@@ -6,20 +6,27 @@
 //
 // Both products run on one 16-bit MFMA kernel (k_mm16) whose operands are
 // contiguous in the contraction, so the operands are laid out first, in one
-// launch (k_prep): dz = [dg | du] and its transpose, the transposed dequantized
+// launch after the exponents' two (k_scales, k_keys; k_prep): dz = [dg | du] and its transpose, the transposed dequantized
 // W, and the transposed dequantized X.  That pass moves 8-10 bytes per element
 // of the operands (8 % of the time of 4096 x 7168 -> 18432); the products then
 // run without a transposing read.  Contractions are padded with zeros to 64
 // elements.
 //
-// Operands are rounded to f16 (11 bits), each once, after a power of two has
-// brought their largest value just under 2^15: one exponent for dz, from the
-// largest magnitudes of dp and z, and one per 128 columns of K for W and for
-// X, from their scales (k_exps).  The exponents are taken off the sums in the
-// epilogue.  So no gradient needs scaling, and every value down to 2^-29 of
-// the largest keeps 11 bits (8 bits at 2^-32); bf16 operands, the simpler
-// choice at the same MFMA rate, gave 2.4e-3 where f16 results allow 2.1e-4,
-// and 2.9e-3 where bf16 results allow 1.7e-3.
+// Operands are rounded to f16 (11 bits), each once, below powers of two that
+// the epilogue takes off the sums again:
+//
+//   X[m, k] = 2^ex[m] X'[m, k],   W[n, k] = 2^ew[n/128] W'[n, k],
+//   dx = (dz 2^ew) W',            dW = (dz 2^ex)^T X',
+//
+// where 2^ex[m] is the largest scale of row m of X and 2^ew that of a block
+// row of W.  The gradient's operand then has one exponent a row for dx (a row of
+// dx depends on its own row of dz alone) and one a column for dW; X' and W'
+// have one per 128 columns of K.  So what a row or column holds does not reach
+// the others, a row of X or W that meets no gradient costs nothing whatever its
+// scale, and no gradient needs scaling: every value down to 2^-29 of the
+// largest that it is added to keeps 11 bits.  bf16 operands, the simpler choice
+// at the same MFMA rate, gave 2.4e-3 where f16 results allow 2.1e-4, and 2.9e-3
+// where bf16 results allow 1.7e-3.
 #include "fp8q_host.h"
 #include "fp8q_mm.h"
 
@@ -37,11 +44,23 @@ struct Mm16Args {
     void* c1;              // rows [gap, M): c1[row - gap]
     int64_t split, gap;
     int cdt, vec;
-    const int* ea;         // the exponent of a
-    const int* eb;         // of 128 rows of b (columns of c) each
+    const uint32_t* ka;    // the key of each row of a
+    const uint32_t* kb;    // of 128 rows of b (columns of c) each,
+    int qb;                // whose values are codes below 2^qb times what the key bounds
     int kper, splits;      // steps a split takes
     float* part;           // [splits][M][N] sums as they are, where splits > 1
 };
+
+// Keys hold exponents in a form that an unsigned max folds: a finite nonzero
+// binary32 v has a key k > 0 with |v| < 2^(k - kKeyBias - 126), 0 stands for
+// none.  `shift`: the key of v 2^shift.
+constexpr int kKeyBias = 1024;
+__device__ __forceinline__ uint32_t key_of(uint32_t bits, int shift) {
+    bits &= 0x7FFFFFFFu;
+    return bits != 0 && bits < 0x7F800000u ? (bits >> 23) + (uint32_t)(shift + kKeyBias) : 0u;
+}
+// the exponent that brings codes below 2^q times what the key bounds under 2^15
+__device__ __forceinline__ int exp_of(uint32_t key, int q) { return key ? 141 + kKeyBias - q - (int)key : 0; }
 
 // row of c0 or c1 that row `row` of the product is, or none (padding)
 __device__ __forceinline__ bool out_row(const Mm16Args& a, int64_t row, void** c, int64_t* r) {
@@ -126,7 +145,7 @@ template <int BM, bool PART> __global__ void __launch_bounds__(kMmThreads, 2) k_
     }
     const int nc = n0 + wn * 32 + lr * 8;
     const int last = (a.N - 1) >> 7;
-    const int e[2] = {-(*a.ea + a.eb[min(n0 >> 7, last)]), -(*a.ea + a.eb[min((n0 >> 7) + 1, last)])};
+    const int eb[2] = {exp_of(a.kb[min(n0 >> 7, last)], a.qb), exp_of(a.kb[min((n0 >> 7) + 1, last)], a.qb)};
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int64_t row = m0 + wm * (BM / 2) + t * 16 + col;
@@ -144,11 +163,12 @@ template <int BM, bool PART> __global__ void __launch_bounds__(kMmThreads, 2) k_
         void* c;
         int64_t r;
         if (!out_row(a, row, &c, &r)) continue;
+        const int ea = exp_of(a.ka[row], 0);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = ldexpf(acc[t][2 * half + (k >> 2)][k & 3], e[half]);
+            for (int k = 0; k < 8; ++k) v[k] = ldexpf(acc[t][2 * half + (k >> 2)][k & 3], -(ea + eb[half]));
             put8(c, a.cdt, r, a.N, nc + half * 128, a.N, a.vec, v);
         }
     }
@@ -176,7 +196,7 @@ __global__ void __launch_bounds__(256) k_mm16_join(Mm16Args a) {
                 v[4 + k] += y[k];
             }
         }
-        const int e = -(*a.ea + a.eb[n >> 7]);
+        const int e = -(exp_of(a.ka[row], 0) + exp_of(a.kb[n >> 7], a.qb));
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = ldexpf(v[k], e);
         put8(c, a.cdt, r, a.N, n, a.N, a.vec, v);
@@ -227,78 +247,148 @@ __device__ __forceinline__ void store_t(const TileT& t, uint16_t* dst, int64_t p
 // exponents
 // ---------------------------------------------------------------------------
 
-// the largest finite |v| of 16-bit values, as binary32 bits
-template <int DT> __device__ __forceinline__ uint32_t finite_bits(uint32_t b) {
-    b &= 0x7FFFu;
-    return b < (DT == kBF16 ? 0x7F80u : 0x7C00u) ? abs16_to_f32bits<DT>(b) : 0u;
-}
-// floor(log2) of a positive finite binary32 (0 for 0)
-__device__ __forceinline__ int log2_of(uint32_t bits) { return bits ? ilogbf(__uint_as_float(bits)) : 0; }
-
-// dz = dz' 2^-e with |dz'| < 2^15: |dy| < 2^(p + 1); |dg|, |du| <= 1.13 |dp| |z|
-// < 2^(p + z + 3), the activations' slopes being at most 1.13
-__device__ __forceinline__ int dz_exponent(uint32_t p, uint32_t z, bool gated) {
-    if (p == 0 || (gated && z == 0)) return 0;
-    return gated ? 12 - log2_of(p) - log2_of(z) : 14 - log2_of(p);
-}
-
-struct ExpArgs {
-    const uint16_t* dy;
-    const uint16_t* z;     // or nullptr
-    int64_t ndy, nz;       // their elements; 0: the exponent stays 0
-    uint32_t* top;         // [3]: the largest finite |dy| and |z|, zeroed before, and dz's exponent
-    uint32_t gdy;          // workgroups of that part
+// floor(log2) of the largest finite scale of every row of X and block row of W
+// (0 where there is none), and the keys cleared for k_keys; 16 lanes a row
+struct ScaleArgs {
     const float* xs;       // [M, KB]
     int64_t M;
     const float* ws0;      // [nb, KB] each
     const float* ws1;      // or nullptr
     int nb, KB;
-    int* ex;               // [KB] exponents of X
-    int* ew;               // [KB] of W
-    int qx, qw;            // bits above 1 of the formats' largest values
+    int* ex;               // [M]
+    int* ew;               // [ws1 ? 2 nb : nb]
+    uint32_t* keys;
+    int64_t nkeys;
 };
-
-template <int DT> __global__ void __launch_bounds__(256) k_exps(ExpArgs a) {
-    __shared__ uint32_t lds4[4];
-    if (blockIdx.x < a.gdy) {
-        for (int which = 0; which < 2; ++which) {
-            const uint16_t* p = which ? a.z : a.dy;
-            const int64_t n = which ? a.nz : a.ndy, step = (int64_t)a.gdy * 256 * 8;
-            uint32_t m = 0;
-            for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += step) {
-                union { v4u q; uint16_t e[8]; } u;
-                if (i + 8 <= n) {
-                    const v4u_a2 r = *(const v4u_a2*)(p + i);
-                    u.q = v4u{r.x, r.y, r.z, r.w};
-                } else {
-                    u.q = v4u{0, 0, 0, 0};
-                    for (int k = 0; k < 8; ++k)
-                        if (i + k < n) u.e[k] = p[i + k];
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) m = umax(m, finite_bits<DT>(u.e[k]));
-            }
-            m = block_max256(m, lds4);
-            if (threadIdx.x == 0 && m) atomicMax(a.top + which, m);   // order-independent
-        }
-        return;
-    }
-    const int kb = (int)(blockIdx.x - a.gdy);
-    auto top = [&](const float* s, int64_t rows) {
+__global__ void __launch_bounds__(256) k_scales(ScaleArgs a) {
+    const int64_t total = a.M + (a.ws1 ? 2 : 1) * (int64_t)a.nb;
+    const int64_t first = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int l = (int)threadIdx.x & 15;
+    for (int64_t row = first; row < total; row += (int64_t)gridDim.x * 16) {
+        const float* s;
+        if (row < a.M) s = a.xs + row * a.KB;
+        else if (row < a.M + a.nb) s = a.ws0 + (row - a.M) * a.KB;
+        else s = a.ws1 + (row - a.M - a.nb) * a.KB;
         uint32_t m = 0;
-        for (int64_t r = threadIdx.x; r < rows; r += 256) {
-            const uint32_t b = __float_as_uint(s[r * a.KB + kb]) & 0x7FFFFFFFu;
+        for (int kb = l; kb < a.KB; kb += 16) {
+            const uint32_t b = __float_as_uint(s[kb]) & 0x7FFFFFFFu;
             m = umax(m, b < 0x7F800000u ? b : 0u);
         }
-        return block_max256(m, lds4);
-    };
-    const uint32_t mx = top(a.xs, a.M);
-    uint32_t mw = top(a.ws0, a.nb);
-    if (a.ws1) mw = umax(mw, top(a.ws1, a.nb));
-    if (threadIdx.x == 0) {
-        if (a.gdy == 0 && kb == 0) a.top[0] = a.top[1] = a.top[2] = 0;
-        a.ex[kb] = 14 - a.qx - log2_of(mx);
-        a.ew[kb] = 14 - a.qw - log2_of(mw);
+        m = max_lanes<16>(m);
+        if (l == 0) (row < a.M ? a.ex + row : a.ew + (row - a.M))[0] = m ? (int)(m >> 23) - 127 : 0;
+    }
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.nkeys; i += (int64_t)gridDim.x * 256) a.keys[i] = 0;
+}
+
+// 8 columns of dg (dz for a projection) and du from column c of row m < M;
+// zero from column N on
+template <int DT, bool GATED>
+__device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z, int64_t m, int c, int N, int act,
+                                          float* g, float* u) {
+    ld8<DT>(dy + m * N, c, N, g);
+    if constexpr (GATED) {
+        float zg[8], zu[8];
+        ld8<DT>(z + m * 2 * N, c, N, zg);
+        ld8<DT>(z + m * 2 * N + N, c, N, zu);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float f, d;
+            act_both(act, zg[k], &f, &d);
+            u[k] = c + k < N ? g[k] * f : 0.0f;
+            g[k] = c + k < N ? g[k] * zu[k] * d : 0.0f;
+        }
+    }
+}
+
+// The keys of dz's rows and columns, and of X' and W' per 128 columns of K.
+// Workgroups [0, e0) take 128 x 128 of dz, 16 lanes a row and 8 columns a lane;
+// [e0, e1) 256 rows of X's scales, the rest as many block rows of W's.  The
+// maxima of integers do not depend on the order of the atomics.
+struct KeyArgs {
+    const uint16_t* dy;
+    const uint16_t* z;
+    int64_t M;
+    int N, act;
+    const int* ex;
+    const int* ew;
+    uint32_t* krow;        // [M], or nullptr
+    uint32_t* kcol;        // [Np] of dg, then of du, or nullptr
+    int Np;
+    const float* xs;
+    const float* ws0;
+    const float* ws1;
+    int nb, KB;
+    uint32_t* kx;          // [KB]
+    uint32_t* kw;
+    uint32_t e0, e1, cols; // cols: tiles of dz in a row of them
+};
+constexpr int kKeyRows = 256;
+__device__ __forceinline__ void scale_keys(const float* s, const int* e, int64_t rows, int64_t r0, int KB, uint32_t* out) {
+    const int64_t r1 = r0 + kKeyRows < rows ? r0 + kKeyRows : rows;
+    const int per = KB < 256 ? 256 / KB : 1, rl = KB < 256 ? (int)threadIdx.x / KB : 0;
+    if (rl >= per) return;
+    for (int kb = KB < 256 ? (int)threadIdx.x % KB : (int)threadIdx.x; kb < KB; kb += 256) {
+        uint32_t m = 0;
+        for (int64_t r = r0 + rl; r < r1; r += per) m = umax(m, key_of(__float_as_uint(s[r * KB + kb]), -e[r]));
+        if (m) atomicMax(out + kb, m);
+    }
+}
+template <int DT, bool GATED> __global__ void __launch_bounds__(256) k_keys(KeyArgs a) {
+    if (blockIdx.x >= a.e0) {
+        int64_t i = blockIdx.x - a.e0;
+        if (blockIdx.x < a.e1) return scale_keys(a.xs, a.ex, a.M, i * kKeyRows, a.KB, a.kx);
+        i = blockIdx.x - a.e1;
+        const int64_t per = (a.nb + kKeyRows - 1) / kKeyRows;
+        if (i < per) scale_keys(a.ws0, a.ew, a.nb, i * kKeyRows, a.KB, a.kw);
+        else scale_keys(a.ws1, a.ew + a.nb, a.nb, (i - per) * kKeyRows, a.KB, a.kw);
+        return;
+    }
+    constexpr int H = GATED ? 2 : 1;
+    __shared__ uint32_t lds[4][H][128];
+    const int bx = (int)(blockIdx.x % a.cols), v = (int)threadIdx.x & 15, rl = (int)threadIdx.x >> 4;
+    const int64_t m0 = (int64_t)(blockIdx.x / a.cols) * 128;
+    const int c = bx * 128 + v * 8;
+    int ew[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) ew[h] = a.ew[h * a.nb + bx];   // 128 columns of dz are one block row of W
+    uint32_t kc[H][8];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) kc[h][k] = 0;
+    for (int i = 0; i < 8; ++i) {
+        const int64_t m = m0 + i * 16 + rl;
+        if (m >= a.M) break;
+        float d[H][8];
+        dz_values<DT, GATED>(a.dy, a.z, m, c, a.N, a.act, d[0], d[H - 1]);
+        const int ex = a.ex[m];
+        uint32_t kr = 0;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t b = __float_as_uint(d[h][k]);
+                kr = umax(kr, key_of(b, ew[h]));
+                kc[h][k] = umax(kc[h][k], key_of(b, ex));
+            }
+        kr = max_lanes<16>(kr);
+        if (v == 0 && a.krow && kr) atomicMax(a.krow + m, kr);
+    }
+    if (!a.kcol) return;
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {                       // the wave's four rows
+            uint32_t m = kc[h][k];
+            m = umax(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+            m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+            if ((rl & 3) == 0) lds[rl >> 2][h][v * 8 + k] = m;
+        }
+    __syncthreads();
+    const int h = (int)threadIdx.x >> 7, cl = (int)threadIdx.x & 127;
+    if (h < H && bx * 128 + cl < a.N) {
+        const uint32_t m = umax(umax(lds[0][h][cl], lds[1][h][cl]), umax(lds[2][h][cl], lds[3][h][cl]));
+        if (m) atomicMax(a.kcol + (int64_t)h * a.Np + bx * 128 + cl, m);
     }
 }
 
@@ -310,57 +400,59 @@ struct DzArgs {
     int act;
     uint16_t* dz;          // [M, gated ? 2 Np : Np], or nullptr
     uint16_t* dzt;         // [gated ? 2 Np : Np, Mp], or nullptr
-    const uint32_t* top;   // largest |dy|, |z|
-    int* ez;               // the exponent, for the products
+    const int* ex;         // [M]
+    const int* ew;         // [gated ? 2 nb : nb]
+    int nb;
+    const uint32_t* krow;  // [M]
+    const uint32_t* kcol;  // [gated ? 2 Np : Np]
 };
 
-// dz and its transpose; 256 threads, one 64 x 64 tile a workgroup; thread
-// (i, v) takes 8 columns of the rows 2i and 2i + 1
+// dz 2^ew and the transpose of dz 2^ex, each below its own exponents; 256
+// threads, one 64 x 64 tile a workgroup; thread (i, v) takes 8 columns of the
+// rows 2i and 2i + 1
 template <int DT, bool GATED> __device__ __forceinline__ void dz_tile(const DzArgs& a, uint32_t bx, uint32_t by, TileT* lds) {
-    TileT &tg = lds[0], &tu = lds[1];
+    constexpr int H = GATED ? 2 : 1;
     const int v = (int)threadIdx.x & 7, i = (int)threadIdx.x >> 3;
     const int64_t m = (int64_t)by * 64 + 2 * i;
     const int c = (int)bx * 64 + v * 8;
-    const int ez = dz_exponent(a.top[0], a.top[1], GATED);
-    if (bx == 0 && by == 0 && threadIdx.x == 0) *a.ez = ez;
-    const int64_t zp = 2 * (int64_t)a.N, dp = GATED ? 2 * (int64_t)a.Np : a.Np;
-    float g[2][8], u[2][8];
+    const int64_t dp = (int64_t)H * a.Np;
+    float d[2][H][8];
+    int ex[2] = {0, 0};
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+        if (m + r >= a.M) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[r][k] = u[r][k] = 0.0f;
-        if (m + r < a.M) {
-            ld8<DT>(a.dy + (m + r) * a.N, c, a.N, g[r]);
-            if constexpr (GATED) {
-                float zg[8], zu[8];
-                ld8<DT>(a.z + (m + r) * zp, c, a.N, zg);
-                ld8<DT>(a.z + (m + r) * zp + a.N, c, a.N, zu);
+            for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float f, d;
-                    act_both(a.act, zg[k], &f, &d);
-                    u[r][k] = c + k < a.N ? ldexpf(g[r][k] * f, ez) : 0.0f;
-                    g[r][k] = c + k < a.N ? g[r][k] * zu[k] * d : 0.0f;
-                }
-            }
+                for (int k = 0; k < 8; ++k) d[r][h][k] = 0.0f;
+            continue;
+        }
+        dz_values<DT, GATED>(a.dy, a.z, m + r, c, a.N, a.act, d[r][0], d[r][H - 1]);
+        ex[r] = a.ex[m + r];
+        if (a.dz) {
+            const int e = exp_of(a.krow[m + r], 0);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) g[r][k] = ldexpf(g[r][k], ez);
-            if (a.dz) {
-                *(v4u*)(a.dz + (m + r) * dp + c) = pack_out16<kF16>(g[r]);
-                if constexpr (GATED) *(v4u*)(a.dz + (m + r) * dp + a.Np + c) = pack_out16<kF16>(u[r]);
+            for (int h = 0; h < H; ++h) {
+                const int s = e + a.ew[h * a.nb + (bx >> 1)];
+                float t[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) t[k] = ldexpf(d[r][h][k], s);
+                *(v4u*)(a.dz + (m + r) * dp + (int64_t)h * a.Np + c) = pack_out16<kF16>(t);
             }
         }
     }
     if (!a.dzt) return;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        tg.w[v * 8 + k][i] = pack_f16x2(g[0][k], g[1][k]);
-        if constexpr (GATED) tu.w[v * 8 + k][i] = pack_f16x2(u[0][k], u[1][k]);
-    }
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int e = exp_of(a.kcol[(int64_t)h * a.Np + c + k], 0);
+            lds[h].w[v * 8 + k][i] = pack_f16x2(ldexpf(d[0][h][k], e + ex[0]), ldexpf(d[1][h][k], e + ex[1]));
+        }
     __syncthreads();
-    uint16_t* d = a.dzt + (int64_t)bx * 64 * a.Mp;
-    store_t(tg, d, a.Mp, (int64_t)by * 64);
-    if constexpr (GATED) store_t(tu, d + (int64_t)a.Np * a.Mp, a.Mp, (int64_t)by * 64);
+    uint16_t* t = a.dzt + (int64_t)bx * 64 * a.Mp;
+#pragma unroll
+    for (int h = 0; h < H; ++h) store_t(lds[h], t + (int64_t)h * a.Np * a.Mp, a.Mp, (int64_t)by * 64);
 }
 
 struct DeqTArgs {
@@ -370,7 +462,9 @@ struct DeqTArgs {
     int KB, sh;
     uint16_t* t;           // [K, pitch], this matrix from element `at` of a row
     int64_t pitch, at;
-    const int* e;          // [KB] exponents
+    const int* e;          // exponent of row >> sh that its scales go without
+    const uint32_t* key;   // [KB]
+    int qb;                // codes are below 2^qb
 };
 
 // The transposed dequantized matrix: 64 rows x 128 codes a workgroup; thread
@@ -379,12 +473,13 @@ template <int FMT> __device__ __forceinline__ void deq_tile(const DeqTArgs& a, u
     const int v = (int)threadIdx.x & 7, i = (int)threadIdx.x >> 3;
     const int64_t r0 = (int64_t)by * 64 + 2 * i;
     const int64_t K = (int64_t)a.KB * 128;
+    const int ex = exp_of(a.key[bx], a.qb);
     float f[2][16];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         if (r0 + r < a.R) {
             const v4u c = *(const v4u*)(a.q + (r0 + r) * K + (int64_t)bx * 128 + v * 16);
-            const float s = ldexpf(a.s[((r0 + r) >> a.sh) * a.KB + bx], a.e[bx]);
+            const float s = ldexpf(a.s[((r0 + r) >> a.sh) * a.KB + bx], ex - a.e[(r0 + r) >> a.sh]);
             dec4<FMT>(c.x, f[r]);
             dec4<FMT>(c.y, f[r] + 4);
             dec4<FMT>(c.z, f[r] + 8);
@@ -470,9 +565,9 @@ Plan16 plan16(int64_t M, int64_t N, int64_t K) {
 // c[m, n] = sum_k a[m, k] b[n, k]; rows [0, split) to c0, rows from gap to c1;
 // N % 128 == 0
 void mm16(const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K, void* c0, void* c1, int64_t split,
-          int64_t gap, int cdt, const int* ea, const int* eb, float* part, hipStream_t st) {
+          int64_t gap, int cdt, const uint32_t* ka, const uint32_t* kb, int qb, float* part, hipStream_t st) {
     const Plan16 p = plan16(M, N, K);
-    Mm16Args a{A, B, M, (int)N, (int)(K / 64), 0, 0, c0, c1, split, gap, cdt, 0, ea, eb, p.kper, p.splits, part};
+    Mm16Args a{A, B, M, (int)N, (int)(K / 64), 0, 0, c0, c1, split, gap, cdt, 0, ka, kb, qb, p.kper, p.splits, part};
     a.vec = al(c0, 16) && (!c1 || al(c1, 16));
     a.tn = (uint32_t)((N + 255) / 256);
     a.tm = (uint32_t)((M + p.bm - 1) / p.bm);
@@ -493,10 +588,17 @@ template <typename F> void with_fmt(int f, F&& go) {
     else go(KC<kE5M2>{});
 }
 
+// go(DT, GATED)
+template <typename F> void with_dt(int dt, bool gated, F&& go) {
+    if (dt == kBF16) { if (gated) go(KC<kBF16>{}, std::true_type{}); else go(KC<kBF16>{}, std::false_type{}); }
+    else { if (gated) go(KC<kF16>{}, std::true_type{}); else go(KC<kF16>{}, std::false_type{}); }
+}
+
 struct BwdLayout {
     int64_t Mp, Np, C;     // padded rows and columns; C: columns of dz
     int64_t dz, dzt, wt, xt;
-    int64_t exps;          // two largest magnitudes, the exponent of dz, then [K / 128] of X and of W
+    int64_t ex, ew;        // exponents of the rows of X and the block rows of W
+    int64_t krow, kcol, kx, kw, nkeys;   // keys: M, C and twice K / 128, nkeys in all
     int64_t part;          // the products' partial sums
     int64_t bytes;
 };
@@ -511,7 +613,13 @@ BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated) {
     l.dzt = take(l.C * l.Mp);
     l.wt = take(K * l.C);
     l.xt = take(K * l.Mp);
-    l.exps = take(2 * (4 + K / 64));
+    l.ex = take(2 * M);
+    l.ew = take(4 * ((N + 127) / 128));
+    l.nkeys = M + l.C + K / 64;
+    l.krow = take(2 * l.nkeys);
+    l.kcol = l.krow + 4 * M;
+    l.kx = l.kcol + 4 * l.C;
+    l.kw = l.kx + 4 * (K / 128);
     l.part = take(std::max(plan16(M, K, l.C).part, plan16(gated ? l.Np + N : N, K, l.Mp).part) / 2);
     l.bytes = at;
     return l;
@@ -543,47 +651,44 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
     float* part = (float*)(ws + l.part);
     const int KB = f.K / 128;
     const bool wdx = f.dx != nullptr, wdw = f.dw0 != nullptr;
-    uint32_t* top = (uint32_t*)(ws + l.exps);
-    int *ez = (int*)top + 2, *ex = (int*)top + 4, *ew = ex + KB;
-    // an f16 gradient keeps its exponent (0), and one whose rows are whole
-    // 128-byte steps is dz already
-    const bool plain = !gated && f.dt == kF16, direct = plain && f.N % 64 == 0 && al(f.dy, 16);
-    if (!plain) launch_zero16(top, 6, st);                  // else k_exps clears them
-    const int64_t ndy = plain ? 0 : f.M * f.N, nz = gated ? 2 * ndy : 0;
-    const int qx = f.xfmt == kE4M3 ? 9 : 16, qw = f.wfmt == kE4M3 ? 9 : 16;   // 448 < 2^9, 57344 < 2^16
-    const ExpArgs ea{(const uint16_t*)f.dy, (const uint16_t*)f.z, ndy, nz, top,
-                     (uint32_t)std::min<int64_t>((std::max(ndy, nz) + 2047) / 2048, 1024), f.xs, f.M, f.ws0,
-                     gated ? f.ws1 : nullptr, (f.N + 127) / 128, KB, ex, ew, qx, qw};
-    if (f.dt == kBF16) k_exps<kBF16><<<ea.gdy + KB, 256, 0, st>>>(ea);
-    else k_exps<kF16><<<ea.gdy + KB, 256, 0, st>>>(ea);
+    const int nb = (f.N + 127) / 128;
+    int *ex = (int*)(ws + l.ex), *ew = (int*)(ws + l.ew);
+    uint32_t *krow = (uint32_t*)(ws + l.krow), *kcol = (uint32_t*)(ws + l.kcol), *kx = (uint32_t*)(ws + l.kx),
+             *kw = (uint32_t*)(ws + l.kw);
+    const float* ws1 = gated ? f.ws1 : nullptr;
+    const ScaleArgs sa{f.xs, f.M, f.ws0, ws1, nb, KB, ex, ew, krow, l.nkeys};
+    k_scales<<<(unsigned)std::min<int64_t>((f.M + (gated ? 2 : 1) * nb + 15) / 16, 4096), 256, 0, st>>>(sa);
+    KeyArgs ka{(const uint16_t*)f.dy, (const uint16_t*)f.z, f.M, f.N, f.act, ex, ew, wdx ? krow : nullptr,
+               wdw ? kcol : nullptr, (int)l.Np, f.xs, f.ws0, ws1, nb, KB, kx, kw, 0, 0, (uint32_t)nb};
+    ka.e0 = (uint32_t)nb * (uint32_t)((f.M + 127) / 128);
+    ka.e1 = ka.e0 + (uint32_t)((f.M + kKeyRows - 1) / kKeyRows);
+    const unsigned gk = ka.e1 + (gated ? 2 : 1) * (uint32_t)((nb + kKeyRows - 1) / kKeyRows);
+    with_dt(f.dt, gated, [&](auto DT, auto GT) { k_keys<decltype(DT)::value, decltype(GT)::value><<<gk, 256, 0, st>>>(ka); });
     PrepArgs p{};
+    const int qx = f.xfmt == kE4M3 ? 9 : 16, qw = f.wfmt == kE4M3 ? 9 : 16;   // 448 < 2^9, 57344 < 2^16
     p.dz = DzArgs{(const uint16_t*)f.dy, (const uint16_t*)f.z, f.M, l.Mp, f.N, (int)l.Np, f.act,
-                  wdx && !direct ? dz : nullptr, wdw ? dzt : nullptr, top, ez};
-    p.x = DeqTArgs{f.x, f.xs, f.M, KB, 0, xt, l.Mp, 0, ex};
-    p.w0 = DeqTArgs{f.w0, f.ws0, f.N, KB, 7, wt, l.C, 0, ew};
-    p.w1 = DeqTArgs{f.w1, f.ws1, f.N, KB, 7, wt, l.C, l.Np, ew};
+                  wdx ? dz : nullptr, wdw ? dzt : nullptr, ex, ew, nb, krow, kcol};
+    p.x = DeqTArgs{f.x, f.xs, f.M, KB, 0, xt, l.Mp, 0, ex, kx, qx};
+    p.w0 = DeqTArgs{f.w0, f.ws0, f.N, KB, 7, wt, l.C, 0, ew, kw, qw};
+    p.w1 = DeqTArgs{f.w1, f.ws1, f.N, KB, 7, wt, l.C, l.Np, ew + nb, kw, qw};
     p.dzx = (uint32_t)(l.Np / 64);
     const uint32_t row_tiles = (uint32_t)(l.Mp / 64), w_tiles = wdx ? (uint32_t)KB * p.dzx : 0;
-    p.e0 = p.dz.dz || p.dz.dzt ? p.dzx * row_tiles : 0;
+    p.e0 = p.dzx * row_tiles;
     p.e1 = p.e0 + (wdw ? (uint32_t)KB * row_tiles : 0);
     p.e2 = p.e1 + w_tiles;
     const unsigned g = p.e2 + (gated ? w_tiles : 0);
     with_fmt(f.xfmt, [&](auto X) {
         with_fmt(f.wfmt, [&](auto W) {
             constexpr int XF = decltype(X)::value, WF = decltype(W)::value;
-            if (f.dt == kBF16) {
-                if (gated) k_prep<kBF16, true, XF, WF><<<g, 256, 0, st>>>(p);
-                else k_prep<kBF16, false, XF, WF><<<g, 256, 0, st>>>(p);
-            } else {
-                if (gated) k_prep<kF16, true, XF, WF><<<g, 256, 0, st>>>(p);
-                else k_prep<kF16, false, XF, WF><<<g, 256, 0, st>>>(p);
-            }
+            with_dt(f.dt, gated, [&](auto DT, auto GT) {
+                k_prep<decltype(DT)::value, decltype(GT)::value, XF, WF><<<g, 256, 0, st>>>(p);
+            });
         });
     });
-    if (wdx) mm16(direct ? (const uint16_t*)f.dy : dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, ez, ew, part, st);
+    if (wdx) mm16(dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, krow, kw, qw, part, st);
     if (wdw) {
-        if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, ez, ex, part, st);
-        else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, ez, ex, part, st);
+        if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, kcol, kx, qx, part, st);
+        else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, kcol, kx, qx, part, st);
     }
 }
 

@@ -36,12 +36,16 @@
  *    block's largest product (up to 4e-5 of the sum's rms measured).
  *  - Every sum has a fixed order: the same call gives the same bits.
  *  - NaN and infinities follow the formulas (0 * inf is NaN).
- *  - Backward products take their operands in f16 (the gradient, and the
- *    dequantized X and W, each rounded once after a power of two has brought its
- *    largest finite value just under 2^15: one exponent for the gradient, one
- *    per 128 columns of K for X and for W) and sum in binary32.  The exponents
- *    are taken off the sums, so gradients of any magnitude need no scaling;
- *    values down to 2^-29 of the largest keep 11 bits.
+ *  - Backward products take their operands in f16, each rounded once, and sum
+ *    in binary32.  The largest scale of each row of X, and of each block row of
+ *    W, goes to the gradient's operand as a power of two; then a power of two
+ *    brings the largest finite value of every row (for dx) or column (for dw)
+ *    of the gradient's operand, and of every 128 columns of K of X's and W's,
+ *    under 2^15.  They are taken off the sums.  So a row of dx depends on its own
+ *    row of the gradient alone, a row of X or a block row of W whose gradient is
+ *    zero on nothing else, and gradients of any magnitude need no scaling:
+ *    values down to 2^-29 of the largest of their row, column or 128 columns
+ *    keep 11 bits.
  *  - The gradient of a cast is the identity: gradients are those of the
  *    formulas at the values the codes stand for.
  */
