@@ -186,28 +186,66 @@ template <int FMT> __device__ __forceinline__ void widen_codes(v8i c, v4i (&o)[4
 // ---------------------------------------------------------------------------
 // activations
 // ---------------------------------------------------------------------------
+// Each is g times a probability that vanishes for negative g: the logistic
+// function of w = g (SiLU) or of w = 2 sqrt(2 / pi) (g + 0.044715 g^3) (tanh GELU:
+// 1 + tanh would cancel, and leaves nothing from g = -5.5 on), or the normal
+// distribution, from erfc for the same reason.  Far out, where exp(-w) or erfc
+// leave binary32 before their product with another factor does, the value and
+// the slope are kept with a factor e, a square root of what vanishes, still to
+// be multiplied: act(g) u = (a u) e.
+struct Act {
+    float a, d, e;         // act(g) = a e, act'(g) = d e
+};
 
-__device__ __forceinline__ float act_value(int act, float g) {
-    if (act == kSilu) return g / (1.0f + expf(-g));
-    if (act == kGelu) return g * (0.5f * (1.0f + erff(g * 0.70710678118654752f)));
-    return 0.5f * g * (1.0f + tanhf(0.79788456080286536f * (g + 0.044715f * g * g * g)));
+template <int ACT, bool SLOPE> __device__ __forceinline__ Act act_at(float g) {
+    Act r;
+    r.d = 0.0f;
+    if constexpr (ACT == kGelu) {
+        if (g < -10.0f) {
+            // Phi(g) = phi(g) / -g (1 - 1/g^2 + 3/g^4 - 15/g^6 + 105/g^8 - ...), the next term under 1e-7
+            const float x = g * g, q = 1.0f / x, h = 0.39894228040143268f;
+            const float c = h * (1.0f - q * (1.0f - 3.0f * q * (1.0f - 5.0f * q * (1.0f - 7.0f * q)))) / -g;
+            r.e = expf(-0.25f * x);
+            r.a = g * r.e * c;
+            if (SLOPE) r.d = r.e * (c + h * g);
+        } else {
+            const float c = 0.5f * erfcf(g * -0.70710678118654752f);
+            r.e = 1.0f;
+            r.a = g * c;
+            if (SLOPE) r.d = c + g * (0.39894228040143268f * expf(-0.5f * g * g));
+        }
+        return r;
+    } else {
+        // w and its derivative w1; beyond |g| = 64 the logistic function of the tanh
+        // form's w is 0 or 1, and is taken at 64, where g^3 is finite (a NaN passes)
+        float w = g, w1 = 1.0f, h = g;
+        if constexpr (ACT == kGeluTanh) {
+            const float k = 1.5957691216057308f;
+            h = g > 64.0f ? 64.0f : g < -64.0f ? -64.0f : g;
+            w = k * (h + 0.044715f * h * h * h);
+            w1 = k * (1.0f + 0.134145f * h * h);
+        }
+        const bool tail = w < -60.0f;
+        const float t = expf(tail ? 0.5f * w : -w);
+        const float s = tail ? t : 1.0f / (1.0f + t);
+        r.e = tail ? t : 1.0f;
+        r.a = tail ? g * t : g / (1.0f + t);
+        if (SLOPE) r.d = s * (1.0f + h * ((tail ? 1.0f : 1.0f - s) * w1));
+        return r;
+    }
 }
 
-// act(g) and act'(g)
-__device__ __forceinline__ void act_both(int act, float g, float* a, float* d) {
-    if (act == kSilu) {
-        const float s = 1.0f / (1.0f + expf(-g));
-        *a = g * s;
-        *d = s * (1.0f + g * (1.0f - s));
-    } else if (act == kGelu) {
-        const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
-        *a = g * c;
-        *d = c + g * (0.39894228040143268f * expf(-0.5f * g * g));
-    } else {
-        const float t = tanhf(0.79788456080286536f * (g + 0.044715f * g * g * g));
-        *a = 0.5f * g * (1.0f + t);
-        *d = 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * 0.79788456080286536f * (1.0f + 0.134145f * g * g);
-    }
+// act(g) * u
+template <int ACT> __device__ __forceinline__ float gated_value(float g, float u) {
+    const Act r = act_at<ACT, false>(g);
+    return r.a * u * r.e;
+}
+
+// f(integral_constant) over a runtime activation
+template <typename F> __device__ __forceinline__ void with_act(int act, F&& f) {
+    if (act == kSilu) f(std::integral_constant<int, kSilu>{});
+    else if (act == kGelu) f(std::integral_constant<int, kGelu>{});
+    else f(std::integral_constant<int, kGeluTanh>{});
 }
 
 // ---------------------------------------------------------------------------

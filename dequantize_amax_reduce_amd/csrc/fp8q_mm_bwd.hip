@@ -290,13 +290,15 @@ __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z,
         float zg[8], zu[8];
         ld8<DT>(z + m * 2 * N, c, N, zg);
         ld8<DT>(z + m * 2 * N + N, c, N, zu);
+        with_act(act, [&](auto A) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float f, d;
-            act_both(act, zg[k], &f, &d);
-            u[k] = c + k < N ? g[k] * f : 0.0f;
-            g[k] = c + k < N ? g[k] * zu[k] * d : 0.0f;
-        }
+            for (int k = 0; k < 8; ++k) {
+                // the slope before u: where it is 0, no large dp * u comes first
+                const Act r = act_at<decltype(A)::value, true>(zg[k]);
+                u[k] = c + k < N ? g[k] * r.a * r.e : 0.0f;
+                g[k] = c + k < N ? g[k] * r.d * zu[k] * r.e : 0.0f;
+            }
+        });
     }
 }
 

@@ -238,29 +238,50 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
 
     const int nc = n0 + wn * 32 + lr * 8;                  // this lane's 8 columns of the first half
     if constexpr (OUT == kOutGated) {
-        float p[MT][8];
+        if (a.z) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int64_t row = m0 + wm * (BM / 2) + t * 16 + col;
-            float g[8], u[8];
+            for (int t = 0; t < MT; ++t) {
+                const int64_t row = m0 + wm * (BM / 2) + t * 16 + col;
+                if (row >= a.M) continue;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                g[k] = acc[t][k >> 2][k & 3];
-                u[k] = acc[t][2 + (k >> 2)][k & 3];
-                p[t][k] = act_value(a.act, g[k]) * u[k];
-            }
-            if (row < a.M) {
-                if (a.z) {
-                    put8(a.z, a.zdt, row, 2 * (int64_t)a.N, nc, a.N, a.vec_z, g);
-                    put8((char*)a.z + (int64_t)a.N * (a.zdt == kF32 ? 4 : 2), a.zdt, row, 2 * (int64_t)a.N, nc, a.N,
-                         a.vec_z, u);
+                for (int half = 0; half < 2; ++half) {
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = acc[t][2 * half + (k >> 2)][k & 3];
+                    put8((char*)a.z + half * (int64_t)a.N * (a.zdt == kF32 ? 4 : 2), a.zdt, row, 2 * (int64_t)a.N, nc,
+                         a.N, a.vec_z, v);
                 }
-                if (a.y) put8(a.y, a.ydt, row, a.N, nc, a.N, a.vec_y, p[t]);
             }
         }
-        if (a.q) {
-            __syncthreads();                               // the last stage's reads are done; LDS is free
-            cast_tile<BM, MT>(a, p, (uint32_t*)smem, m0, n0, wm, wn, lane);
+        // a loop for each activation: one body of all three is past what is unrolled
+        with_act(a.act, [&](auto A) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float g = acc[t][k >> 2][k & 3], u = acc[t][2 + (k >> 2)][k & 3];
+                    acc[t][k >> 2][k & 3] = gated_value<decltype(A)::value>(g, u);
+                }
+                __builtin_amdgcn_sched_barrier(0);         // no registers for more than one row tile's exps at once
+            }
+        });
+        float p[MT][8];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) p[t][k] = acc[t][k >> 2][k & 3];
+        if (a.y) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const int64_t row = m0 + wm * (BM / 2) + t * 16 + col;
+                if (row < a.M) put8(a.y, a.ydt, row, a.N, nc, a.N, a.vec_y, p[t]);
+            }
+        }
+        if constexpr (EX) {                                // a cast's sums are binary32
+            if (a.q) {
+                __syncthreads();                           // the last stage's reads are done; LDS is free
+                cast_tile<BM, MT>(a, p, (uint32_t*)smem, m0, n0, wm, wn, lane);
+            }
         }
     } else {
 #pragma unroll
@@ -333,8 +354,14 @@ template <int V, bool CAST> __global__ void __launch_bounds__(256) k_mm_join(Joi
             }
         }
 #pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = g[k];
+        if (a.gated)
+            with_act(a.act, [&](auto A) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) v[k] = gated_value<decltype(A)::value>(g[k], u[k]);
+            });
+#pragma unroll
         for (int k = 0; k < V; ++k) {
-            v[k] = a.gated ? act_value(a.act, g[k]) * u[k] : g[k];
             if (a.z) {
                 put1(a.z, a.zdt, m * W + n + k, g[k]);
                 put1(a.z, a.zdt, m * W + a.N + n + k, u[k]);
@@ -484,7 +511,7 @@ __global__ void __launch_bounds__(512) k_mm_rows(FwdArgs a, float* pbuf) {
                     put1(a.z, a.zdt, at, g);
                     put1(a.z, a.zdt, at + a.N, u);
                 }
-                v = act_value(a.act, g) * u;
+                with_act(a.act, [&](auto A) { v = gated_value<decltype(A)::value>(g, u); });
             }
             const int64_t at = m * (int64_t)a.N + n;
             if (pbuf) pbuf[at] = v;
