@@ -197,7 +197,9 @@ struct Act {
     float a, d, e;         // act(g) = a e, act'(g) = d e
 };
 
-template <int ACT, bool SLOPE> __device__ __forceinline__ Act act_at(float g) {
+// QUICK: the logistic function to 2^-16 only, and never less than exp's smallest
+// normal value, where no more than its exponent counts
+template <int ACT, bool SLOPE, bool QUICK = false> __device__ __forceinline__ Act act_at(float g) {
     Act r;
     r.d = 0.0f;
     if constexpr (ACT == kGelu) {
@@ -226,11 +228,16 @@ template <int ACT, bool SLOPE> __device__ __forceinline__ Act act_at(float g) {
             w1 = k * (1.0f + 0.134145f * h * h);
         }
         const bool tail = w < -60.0f;
-        const float t = expf(tail ? 0.5f * w : -w);
-        const float s = tail ? t : 1.0f / (1.0f + t);
+        const float x = tail ? 0.5f * w : -w;
+        const float t = QUICK ? fmaxf(__expf(x), 0x1p-126f) : expf(x);   // __expf has no subnormal values
         r.e = tail ? t : 1.0f;
-        r.a = tail ? g * t : g / (1.0f + t);
-        if (SLOPE) r.d = s * (1.0f + h * ((tail ? 1.0f : 1.0f - s) * w1));
+        if (!SLOPE) {
+            r.a = tail ? g * t : g / (1.0f + t);
+            return r;
+        }
+        const float s = tail ? t : QUICK ? __builtin_amdgcn_rcpf(1.0f + t) : 1.0f / (1.0f + t);
+        r.a = g * s;
+        r.d = s * (1.0f + h * ((tail ? 1.0f : 1.0f - s) * w1));
         return r;
     }
 }

@@ -55,9 +55,12 @@ struct Mm16Args {
 // binary32 v has a key k > 0 with |v| < 2^(k - kKeyBias - 126), 0 stands for
 // none.  `shift`: the key of v 2^shift.
 constexpr int kKeyBias = 1024;
-__device__ __forceinline__ uint32_t key_of(uint32_t bits, int shift) {
-    bits &= 0x7FFFFFFFu;
-    return bits != 0 && bits < 0x7F800000u ? (bits >> 23) + (uint32_t)(shift + kKeyBias) : 0u;
+__device__ __forceinline__ uint32_t finite_bits(float v) {   // |v|, 0 for NaN and infinity
+    const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? b : 0u;
+}
+__device__ __forceinline__ uint32_t key_of(uint32_t finite, int shift) {
+    return finite ? (finite >> 23) + (uint32_t)(shift + kKeyBias) : 0u;
 }
 // the exponent that brings codes below 2^q times what the key bounds under 2^15
 __device__ __forceinline__ int exp_of(uint32_t key, int q) { return key ? 141 + kKeyBias - q - (int)key : 0; }
@@ -216,10 +219,10 @@ struct TileT {
     uint32_t w[64][33];
 };
 
-// 8 elements from column c of a row (zero from column `cols` on)
-template <int DT> __device__ __forceinline__ void ld8(const uint16_t* row, int c, int cols, float* v) {
+// 8 elements from column c of a row (zero from column `cols` on); FULL: c + 8 <= cols
+template <int DT, bool FULL> __device__ __forceinline__ void ld8(const uint16_t* row, int c, int cols, float* v) {
     HpVec<DT> t;
-    if (c + 8 <= cols) {
+    if (FULL || c + 8 <= cols) {
         const v4u_a2 r = *(const v4u_a2*)(row + c);
         t.r = v4u{r.x, r.y, r.z, r.w};
     } else {
@@ -270,10 +273,7 @@ __global__ void __launch_bounds__(256) k_scales(ScaleArgs a) {
         else if (row < a.M + a.nb) s = a.ws0 + (row - a.M) * a.KB;
         else s = a.ws1 + (row - a.M - a.nb) * a.KB;
         uint32_t m = 0;
-        for (int kb = l; kb < a.KB; kb += 16) {
-            const uint32_t b = __float_as_uint(s[kb]) & 0x7FFFFFFFu;
-            m = umax(m, b < 0x7F800000u ? b : 0u);
-        }
+        for (int kb = l; kb < a.KB; kb += 16) m = umax(m, finite_bits(s[kb]));
         m = max_lanes<16>(m);
         if (l == 0) (row < a.M ? a.ex + row : a.ew + (row - a.M))[0] = m ? (int)(m >> 23) - 127 : 0;
     }
@@ -281,22 +281,22 @@ __global__ void __launch_bounds__(256) k_scales(ScaleArgs a) {
 }
 
 // 8 columns of dg (dz for a projection) and du from column c of row m < M;
-// zero from column N on
-template <int DT, bool GATED>
+// zero from column N on (FULL: there are none); QUICK as in act_at
+template <int DT, bool GATED, bool FULL, bool QUICK>
 __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z, int64_t m, int c, int N, int act,
                                           float* g, float* u) {
-    ld8<DT>(dy + m * N, c, N, g);
+    ld8<DT, FULL>(dy + m * N, c, N, g);
     if constexpr (GATED) {
         float zg[8], zu[8];
-        ld8<DT>(z + m * 2 * N, c, N, zg);
-        ld8<DT>(z + m * 2 * N + N, c, N, zu);
+        ld8<DT, FULL>(z + m * 2 * N, c, N, zg);
+        ld8<DT, FULL>(z + m * 2 * N + N, c, N, zu);
         with_act(act, [&](auto A) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 // the slope before u: where it is 0, no large dp * u comes first
-                const Act r = act_at<decltype(A)::value, true>(zg[k]);
-                u[k] = c + k < N ? g[k] * r.a * r.e : 0.0f;
-                g[k] = c + k < N ? g[k] * r.d * zu[k] * r.e : 0.0f;
+                const Act r = act_at<decltype(A)::value, true, QUICK>(zg[k]);
+                u[k] = FULL || c + k < N ? g[k] * r.a * r.e : 0.0f;
+                g[k] = FULL || c + k < N ? g[k] * r.d * zu[k] * r.e : 0.0f;
             }
         });
     }
@@ -304,7 +304,7 @@ __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z,
 
 // The keys of dz's rows and columns, and of X' and W' per 128 columns of K.
 // Workgroups [0, e0) take 128 x 128 of dz, 16 lanes a row and 8 columns a lane;
-// [e0, e1) 256 rows of X's scales, the rest as many block rows of W's.  The
+// [e0, e1) 32 rows of X's scales, the rest as many block rows of W's.  The
 // maxima of integers do not depend on the order of the atomics.
 struct KeyArgs {
     const uint16_t* dy;
@@ -324,29 +324,42 @@ struct KeyArgs {
     uint32_t* kw;
     uint32_t e0, e1, cols; // cols: tiles of dz in a row of them
 };
-constexpr int kKeyRows = 256;
-__device__ __forceinline__ void scale_keys(const float* s, const int* e, int64_t rows, int64_t r0, int KB, uint32_t* out) {
-    const int64_t r1 = r0 + kKeyRows < rows ? r0 + kKeyRows : rows;
+// A workgroup takes few rows, with 8 loads in flight a thread, so that it does
+// not end after dz's (3001 x 4096 f16: 11.2 us, 16.7 with 256 rows).
+constexpr int kKeyRows = 32;
+__device__ __forceinline__ void scale_keys(const float* s, const int* e, int64_t rows, int64_t r0, int KB, uint32_t* out,
+                                           uint32_t* lds) {
+    const int64_t last = (r0 + kKeyRows < rows ? r0 + kKeyRows : rows) - 1;
     const int per = KB < 256 ? 256 / KB : 1, rl = KB < 256 ? (int)threadIdx.x / KB : 0;
-    if (rl >= per) return;
-    for (int kb = KB < 256 ? (int)threadIdx.x % KB : (int)threadIdx.x; kb < KB; kb += 256) {
+    lds[threadIdx.x] = 0;
+    __syncthreads();
+    for (int kb = KB < 256 ? (int)threadIdx.x % KB : (int)threadIdx.x; rl < per && kb < KB; kb += 256) {
         uint32_t m = 0;
-        for (int64_t r = r0 + rl; r < r1; r += per) m = umax(m, key_of(__float_as_uint(s[r * KB + kb]), -e[r]));
-        if (m) atomicMax(out + kb, m);
+        for (int64_t r = r0 + rl; r <= last; r += 8 * per) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {                   // rows past the last are the last one again
+                const int64_t ri = r + i * per < last ? r + i * per : last;
+                m = umax(m, key_of(finite_bits(s[ri * KB + kb]), -e[ri]));
+            }
+        }
+        if (KB < 256) atomicMax(lds + kb, m);               // LDS; a word of `out` takes 8 ns an atomic
+        else if (m) atomicMax(out + kb, m);
     }
+    __syncthreads();
+    if ((int)threadIdx.x < KB && lds[threadIdx.x]) atomicMax(out + threadIdx.x, lds[threadIdx.x]);
 }
 template <int DT, bool GATED> __global__ void __launch_bounds__(256) k_keys(KeyArgs a) {
-    if (blockIdx.x >= a.e0) {
-        int64_t i = blockIdx.x - a.e0;
-        if (blockIdx.x < a.e1) return scale_keys(a.xs, a.ex, a.M, i * kKeyRows, a.KB, a.kx);
-        i = blockIdx.x - a.e1;
-        const int64_t per = (a.nb + kKeyRows - 1) / kKeyRows;
-        if (i < per) scale_keys(a.ws0, a.ew, a.nb, i * kKeyRows, a.KB, a.kw);
-        else scale_keys(a.ws1, a.ew + a.nb, a.nb, (i - per) * kKeyRows, a.KB, a.kw);
-        return;
-    }
     constexpr int H = GATED ? 2 : 1;
     __shared__ uint32_t lds[4][H][128];
+    if (blockIdx.x >= a.e0) {
+        int64_t i = blockIdx.x - a.e0;
+        if (blockIdx.x < a.e1) return scale_keys(a.xs, a.ex, a.M, i * kKeyRows, a.KB, a.kx, lds[0][0]);
+        i = blockIdx.x - a.e1;
+        const int64_t per = (a.nb + kKeyRows - 1) / kKeyRows;
+        if (i < per) scale_keys(a.ws0, a.ew, a.nb, i * kKeyRows, a.KB, a.kw, lds[0][0]);
+        else scale_keys(a.ws1, a.ew + a.nb, a.nb, (i - per) * kKeyRows, a.KB, a.kw, lds[0][0]);
+        return;
+    }
     const int bx = (int)(blockIdx.x % a.cols), v = (int)threadIdx.x & 15, rl = (int)threadIdx.x >> 4;
     const int64_t m0 = (int64_t)(blockIdx.x / a.cols) * 128;
     const int c = bx * 128 + v * 8;
@@ -358,24 +371,44 @@ template <int DT, bool GATED> __global__ void __launch_bounds__(256) k_keys(KeyA
     for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int k = 0; k < 8; ++k) kc[h][k] = 0;
-    for (int i = 0; i < 8; ++i) {
-        const int64_t m = m0 + i * 16 + rl;
-        if (m >= a.M) break;
-        float d[H][8];
-        dz_values<DT, GATED>(a.dy, a.z, m, c, a.N, a.act, d[0], d[H - 1]);
-        const int ex = a.ex[m];
-        uint32_t kr = 0;
+    // Rows past the end are the last one again, which changes no maximum (but
+    // atomics on one word take 8 ns each: only a row's own lanes make them).
+    // The loads of R rows are in flight at once.
+    auto rows = [&](auto FULL) {
+        constexpr int R = GATED ? 2 : 4;
+#pragma unroll 1
+        for (int i = 0; i < 8; i += R) {
+            float d[R][H][8];
+            int64_t m[R];
+            int ex[R];
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t b = __float_as_uint(d[h][k]);
-                kr = umax(kr, key_of(b, ew[h]));
-                kc[h][k] = umax(kc[h][k], key_of(b, ex));
+            for (int r = 0; r < R; ++r) {
+                m[r] = m0 + (i + r) * 16 + rl;
+                if (m[r] > a.M - 1) m[r] = a.M - 1;
+                ex[r] = a.ex[m[r]];
+                dz_values<DT, GATED, decltype(FULL)::value, true>(a.dy, a.z, m[r], c, a.N, a.act, d[r][0], d[r][H - 1]);
             }
-        kr = max_lanes<16>(kr);
-        if (v == 0 && a.krow && kr) atomicMax(a.krow + m, kr);
-    }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                uint32_t kr = 0;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t b = finite_bits(d[r][h][k]);
+                        top = umax(top, b);
+                        kc[h][k] = umax(kc[h][k], key_of(b, ex[r]));
+                    }
+                    kr = umax(kr, key_of(top, ew[h]));
+                }
+                kr = max_lanes<16>(kr);
+                if (v == 0 && a.krow && kr && m0 + (i + r) * 16 + rl < a.M) atomicMax(a.krow + m[r], kr);
+            }
+        }
+    };
+    if (bx * 128 + 128 <= a.N) rows(std::true_type{});
+    else rows(std::false_type{});
     if (!a.kcol) return;
 #pragma unroll
     for (int h = 0; h < H; ++h)
@@ -429,7 +462,7 @@ template <int DT, bool GATED> __device__ __forceinline__ void dz_tile(const DzAr
                 for (int k = 0; k < 8; ++k) d[r][h][k] = 0.0f;
             continue;
         }
-        dz_values<DT, GATED>(a.dy, a.z, m + r, c, a.N, a.act, d[r][0], d[r][H - 1]);
+        dz_values<DT, GATED, false, false>(a.dy, a.z, m + r, c, a.N, a.act, d[r][0], d[r][H - 1]);
         ex[r] = a.ex[m + r];
         if (a.dz) {
             const int e = exp_of(a.krow[m + r], 0);
