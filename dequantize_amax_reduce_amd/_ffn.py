@@ -344,7 +344,8 @@ def rmsnorm_cast(x, weight, residual=None, eps=1e-6, fp8_format="e4m3fn", per_ch
     * weight cast to fp8 per 128 columns (scale_inv [rows, cols/128]) or per
     row (per_channel_scale=True, scale_inv [rows]).  h has x's dtype and is x
     itself without a residual; h and rstd are what rmsnorm_cast_backward
-    reads.  `out`: those four tensors, caller-allocated."""
+    reads.  `out`: those four tensors, caller-allocated (without a residual, x
+    itself may stand for h; another tensor gets a copy of x)."""
     rows, cols = _flat(x, "x")
     if out is not None:
         q, s, h, rstd = out
@@ -355,7 +356,7 @@ def rmsnorm_cast(x, weight, residual=None, eps=1e-6, fp8_format="e4m3fn", per_ch
         h = x if residual is None else torch.empty_like(x)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     name = "fp8q_rmsnorm_cast_per_channel" if per_channel_scale else "fp8q_rmsnorm_cast_group128"
-    _norm(name, x, weight, q, s, residual, None if residual is None else h, rstd, eps, fp8_format, None)
+    _norm(name, x, weight, q, s, residual, None if h is x else h, rstd, eps, fp8_format, None)
     return q, s, h, rstd
 
 
