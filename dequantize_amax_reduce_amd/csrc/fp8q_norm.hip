@@ -499,21 +499,24 @@ template <int DT, bool WF32> __global__ void __launch_bounds__(1024) k_norm_bwd_
 }
 
 // dweight[c] = sum of part[0 .. parts)[c] in a fixed order: 32 columns a
-// workgroup, 32 row lanes, then a tree over the row lanes in LDS
+// workgroup at a time, 32 row lanes, then a tree over the row lanes in LDS
+// (each word of its first row is read by the thread that writes it next)
 template <int WDT> __global__ void __launch_bounds__(1024) k_norm_dw(const float* part, int64_t parts, int cols, void* dw) {
     __shared__ float lds[32][33];
     const int cl = (int)threadIdx.x & 31, rl = (int)threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + cl;
-    float s = 0.0f;
-    if (c < cols)
-        for (int64_t p = rl; p < parts; p += 32) s += part[p * cols + c];
-    lds[rl][cl] = s;
-    __syncthreads();
-    for (int o = 16; o > 0; o >>= 1) {
-        if (rl < o) lds[rl][cl] += lds[rl + o][cl];
+    for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < cols; c0 += (int64_t)gridDim.x * 32) {
+        const int64_t c = c0 + cl;
+        float s = 0.0f;
+        if (c < cols)
+            for (int64_t p = rl; p < parts; p += 32) s += part[p * cols + c];
+        lds[rl][cl] = s;
         __syncthreads();
+        for (int o = 16; o > 0; o >>= 1) {
+            if (rl < o) lds[rl][cl] += lds[rl + o][cl];
+            __syncthreads();
+        }
+        if (rl == 0 && c < cols) store1<WDT>(dw, c, lds[0][cl]);
     }
-    if (rl == 0 && c < cols) store1<WDT>(dw, c, lds[0][cl]);
 }
 
 constexpr int kNormWaves = 8192;  // waves a launch of the forward pass asks for: what the chip holds at once
@@ -596,7 +599,7 @@ void launch_rmsnorm_bwd(const void* dy, const void* h, int dt, const void* w, in
     else if (dt == kBF16) norm_bwd<kBF16>(wdt == kF32, a, g, st);
     else norm_bwd<kF16>(wdt == kF32, a, g, st);
     if (!dw) return;
-    const unsigned gc = (unsigned)((cols + 31) / 32);
+    const unsigned gc = grid((cols + 31) / 32);            // 1024 threads each: a grid holds fewer than 2^32
     if (wdt == kF32) k_norm_dw<kF32><<<gc, 1024, 0, st>>>(ws, parts, (int)cols, dw);
     else if (wdt == kBF16) k_norm_dw<kBF16><<<gc, 1024, 0, st>>>(ws, parts, (int)cols, dw);
     else k_norm_dw<kF16><<<gc, 1024, 0, st>>>(ws, parts, (int)cols, dw);

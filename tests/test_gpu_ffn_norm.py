@@ -28,3 +28,20 @@ def test_h_is_written_without_a_residual(rows, cols, per_row):
         assert b[2] is xd and torch.equal(xd.cpu(), x)
         for i in (0, 1, 3):
             assert torch.equal(a[i].view(torch.uint8), b[i].view(torch.uint8))
+
+
+def test_backward_of_a_very_long_row():
+    """2^27 + 5 columns: more column tiles of dweight than one grid holds.  One
+    row of equal values: n = 1, so dweight = dy, and dx = dy - mean(dy)."""
+    cols = (1 << 27) + 5
+    h = torch.ones(1, cols, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros(1, cols, dtype=torch.bfloat16, device="cuda")
+    dy[0, ::2] = 0.5
+    dy[0, -1] = 3.0
+    w, rstd = torch.ones(cols, dtype=torch.bfloat16, device="cuda"), torch.ones(1, device="cuda")
+    dw = torch.full((cols,), 7.0, dtype=torch.bfloat16, device="cuda")
+    dx = torch.full_like(dy, 7.0)
+    fq.rmsnorm_cast_backward(dy, h, w, rstd, out=(dx, dw))
+    assert torch.equal(dw, dy[0])
+    mean = 0.25                                             # to 2^-25; dy - mean is exact in bf16
+    assert torch.equal(dx, dy - mean)
