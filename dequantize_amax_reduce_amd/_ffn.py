@@ -2,7 +2,8 @@
 
 Re-exported by the package.  As there, two layers: ``fp8q_*`` mirror the C
 entry points (caller-allocated outputs and workspaces), and the helpers below
-them allocate outputs and workspaces with torch.
+them allocate outputs and workspaces with torch.  Codes are float8 tensors, or
+uint8 ones of the formats x_fmt and w_fmt name (e4m3fn where they do not).
 
     q, s, h, rstd = rmsnorm_cast(x, weight, residual)          # norm -> fp8 per 128-group
     q2, s2, z = gated_linear_fp8_cast(q, s, wg, wgs, wu, wus, keep=torch.bfloat16)
@@ -151,28 +152,35 @@ def _ws(t, need, like, name):
     return t
 
 
-def _x_codes(x, xs, name):
-    """(pointer, format, scale pointer), rows, K of an activation"""
-    f = _fp8(x, None, "x")
+def _x_codes(x, xs, f):
+    """(pointer, format, scale pointer), rows, K of an activation of format f"""
     M, K = _flat(x, "x")
     return (_ptr(x, "x"), f, _f32(xs, M * (K // 128), "x_scale_inv")), M, K
 
 
 def _w_codes(w, ws, K, name):
-    """pointer, format, scale pointer, rows of a weight"""
-    f = _fp8(w, None, name)
+    """pointer, scale pointer, rows of a weight"""
     if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"{name} must be 2-D with {K} columns")
     N = w.shape[0]
-    return _ptr(w, name), f, _f32(ws, ((N + 127) // 128) * (K // 128), "the weight's scale_inv"), N
+    return _ptr(w, name), _f32(ws, ((N + 127) // 128) * (K // 128), "the weight's scale_inv"), N
 
 
-def _pair(w_gate, gs, w_up, us, K):
-    g, gf, gsp, F = _w_codes(w_gate, gs, K, "w_gate")
-    u, uf, usp, F2 = _w_codes(w_up, us, K, "w_up")
-    if F != F2 or gf != uf:
+def _formats(x, x_fmt, w_fmt, *weights):
+    """The formats of x and of the weights, before anything else is asked of
+    them; x_fmt and w_fmt name those of uint8 codes."""
+    xf, wf = _fp8(x, x_fmt, "x"), _fp8(weights[0], w_fmt, "the weight")
+    if len(weights) > 1 and _fp8(weights[1], w_fmt, "w_up") != wf:
         raise ValueError("w_gate and w_up must have the same shape and format")
-    return (g, gsp, u, usp, gf), F
+    return xf, wf
+
+
+def _pair(w_gate, gs, w_up, us, K, f):
+    g, gsp, F = _w_codes(w_gate, gs, K, "w_gate")
+    u, usp, F2 = _w_codes(w_up, us, K, "w_up")
+    if F != F2:
+        raise ValueError("w_gate and w_up must have the same shape and format")
+    return (g, gsp, u, usp, f), F
 
 
 # ---------------------------------------------------------------------------
@@ -234,9 +242,10 @@ def fp8q_linear_workspace_bytes(M: int, N: int, K: int) -> int:
     return lib.fp8q_linear_workspace_bytes(M, N, K)
 
 
-def fp8q_linear(x, x_scale_inv, w, w_scale_inv, y, workspace=None, stream=None) -> None:
-    xa, M, K = _x_codes(x, x_scale_inv, "x")
-    wp, wf, wsp, N = _w_codes(w, w_scale_inv, K, "w")
+def fp8q_linear(x, x_scale_inv, w, w_scale_inv, y, workspace=None, stream=None, x_fmt=None, w_fmt=None) -> None:
+    xf, wf = _formats(x, x_fmt, w_fmt, w)
+    xa, M, K = _x_codes(x, x_scale_inv, xf)
+    wp, wsp, N = _w_codes(w, w_scale_inv, K, "w")
     _same(y, (M, N), y.dtype, "y")
     scratch = _ws(workspace, lib.fp8q_linear_workspace_bytes(M, N, K), x, "fp8q_linear")
     _check(lib.fp8q_linear(*xa, wp, wf, wsp, M, N, K, _ptr(y, "y"), _hp_dtype(y, "y"), _opt(scratch, "workspace"),
@@ -254,9 +263,11 @@ def _grad_dtype(grads):
     return d.pop() if d else None
 
 
-def fp8q_linear_backward(dy, x, x_scale_inv, w, w_scale_inv, dx=None, dw=None, workspace=None, stream=None) -> None:
-    xa, M, K = _x_codes(x, x_scale_inv, "x")
-    wp, wf, wsp, N = _w_codes(w, w_scale_inv, K, "w")
+def fp8q_linear_backward(dy, x, x_scale_inv, w, w_scale_inv, dx=None, dw=None, workspace=None, stream=None,
+                         x_fmt=None, w_fmt=None) -> None:
+    xf, wf = _formats(x, x_fmt, w_fmt, w)
+    xa, M, K = _x_codes(x, x_scale_inv, xf)
+    wp, wsp, N = _w_codes(w, w_scale_inv, K, "w")
     dt = _hp_dtype(dy, "dy")
     _same(dy, (M, N), dy.dtype, "dy")
     _same(dx, (M, K), dy.dtype, "dx")
@@ -282,9 +293,10 @@ def _z_arg(z, M, F):
 
 
 def fp8q_gated_linear(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, h, z=None, activation="silu",
-                      workspace=None, stream=None) -> None:
-    xa, M, K = _x_codes(x, x_scale_inv, "x")
-    pair, F = _pair(w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, K)
+                      workspace=None, stream=None, x_fmt=None, w_fmt=None) -> None:
+    xf, wf = _formats(x, x_fmt, w_fmt, w_gate, w_up)
+    xa, M, K = _x_codes(x, x_scale_inv, xf)
+    pair, F = _pair(w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, K, wf)
     _same(h, (M, F), h.dtype, "h")
     need = lib.fp8q_gated_linear_workspace_bytes(M, F, K, 0)
     scratch = _ws(workspace, need, x, "fp8q_gated_linear")
@@ -294,9 +306,10 @@ def fp8q_gated_linear(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale
 
 
 def fp8q_gated_linear_cast(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, q, scale_inv, z=None,
-                           activation="silu", fmt=None, workspace=None, stream=None) -> None:
-    xa, M, K = _x_codes(x, x_scale_inv, "x")
-    pair, F = _pair(w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, K)
+                           activation="silu", fmt=None, workspace=None, stream=None, x_fmt=None, w_fmt=None) -> None:
+    xf, wf = _formats(x, x_fmt, w_fmt, w_gate, w_up)
+    xa, M, K = _x_codes(x, x_scale_inv, xf)
+    pair, F = _pair(w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, K, wf)
     f = _fp8(q, fmt, "q")
     if q.numel() != M * F:
         raise ValueError("fp8q_gated_linear_cast: q must have M x F elements")
@@ -315,9 +328,11 @@ def fp8q_gated_linear_backward_workspace_bytes(M: int, F: int, K: int) -> int:
 
 
 def fp8q_gated_linear_backward(dp, z, x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, dx=None,
-                               dw_gate=None, dw_up=None, activation="silu", workspace=None, stream=None) -> None:
-    xa, M, K = _x_codes(x, x_scale_inv, "x")
-    pair, F = _pair(w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, K)
+                               dw_gate=None, dw_up=None, activation="silu", workspace=None, stream=None,
+                               x_fmt=None, w_fmt=None) -> None:
+    xf, wf = _formats(x, x_fmt, w_fmt, w_gate, w_up)
+    xa, M, K = _x_codes(x, x_scale_inv, xf)
+    pair, F = _pair(w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, K, wf)
     dt = _hp_dtype(dp, "dp")
     _same(dp, (M, F), dp.dtype, "dp")
     _same(z, (M, 2 * F), dp.dtype, "z")
@@ -368,15 +383,15 @@ def rmsnorm_cast_backward(dy, h, weight, rstd, dh=None, out=None):
     return dx, dw
 
 
-def linear_fp8(x, x_scale_inv, w, w_scale_inv, ret_type=torch.bfloat16, out=None):
+def linear_fp8(x, x_scale_inv, w, w_scale_inv, ret_type=torch.bfloat16, out=None, x_fmt=None, w_fmt=None):
     """y = X W^T for codes x [..., K] with scales per 128-group and w [N, K]
     with scales per 128x128 block."""
     y = out if out is not None else torch.empty((*x.shape[:-1], w.shape[0]), dtype=ret_type, device=x.device)
-    fp8q_linear(x, x_scale_inv, w, w_scale_inv, y, _AUTO)
+    fp8q_linear(x, x_scale_inv, w, w_scale_inv, y, _AUTO, x_fmt=x_fmt, w_fmt=w_fmt)
     return y
 
 
-def linear_fp8_backward(dy, x, x_scale_inv, w, w_scale_inv, grad_type=None, out=None):
+def linear_fp8_backward(dy, x, x_scale_inv, w, w_scale_inv, grad_type=None, out=None, x_fmt=None, w_fmt=None):
     """(dx, dw) of linear_fp8, dx in dy's dtype (bf16 or f16), dw in grad_type
     (dy's dtype by default, or float32)."""
     if out is not None:
@@ -384,12 +399,12 @@ def linear_fp8_backward(dy, x, x_scale_inv, w, w_scale_inv, grad_type=None, out=
     else:
         dx = torch.empty(x.shape, dtype=dy.dtype, device=x.device)
         dw = torch.empty(w.shape, dtype=grad_type or dy.dtype, device=x.device)
-    fp8q_linear_backward(dy, x, x_scale_inv, w, w_scale_inv, dx, dw, _AUTO)
+    fp8q_linear_backward(dy, x, x_scale_inv, w, w_scale_inv, dx, dw, _AUTO, x_fmt=x_fmt, w_fmt=w_fmt)
     return dx, dw
 
 
 def gated_linear_fp8(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, activation="silu",
-                     ret_type=torch.bfloat16, keep=None, out=None):
+                     ret_type=torch.bfloat16, keep=None, out=None, x_fmt=None, w_fmt=None):
     """(h, z): h = act(X Wg^T) * (X Wu^T) in ret_type; z [..., 2F] holds both
     products in `keep`'s dtype for the backward pass, or is None."""
     F = w_gate.shape[0]
@@ -398,12 +413,13 @@ def gated_linear_fp8(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_
     else:
         h = torch.empty((*x.shape[:-1], F), dtype=ret_type, device=x.device)
         z = None if keep is None else torch.empty((*x.shape[:-1], 2 * F), dtype=keep, device=x.device)
-    fp8q_gated_linear(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, h, z, activation, _AUTO)
+    fp8q_gated_linear(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, h, z, activation, _AUTO,
+                      x_fmt=x_fmt, w_fmt=w_fmt)
     return h, z
 
 
 def gated_linear_fp8_cast(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, activation="silu",
-                          fp8_format="e4m3fn", keep=None, out=None):
+                          fp8_format="e4m3fn", keep=None, out=None, x_fmt=None, w_fmt=None):
     """(q, scale_inv, z): gated_linear_fp8's product cast to fp8 per 128-group
     (F % 128 == 0) without a 16-bit copy in between, and z as there."""
     F = w_gate.shape[0]
@@ -414,12 +430,12 @@ def gated_linear_fp8_cast(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_s
         s = torch.empty((_flat(x, "x")[0], F // 128), dtype=torch.float32, device=x.device)
         z = None if keep is None else torch.empty((*x.shape[:-1], 2 * F), dtype=keep, device=x.device)
     fp8q_gated_linear_cast(x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, q, s, z, activation,
-                           fp8_format, _AUTO)
+                           fp8_format, _AUTO, x_fmt=x_fmt, w_fmt=w_fmt)
     return q, s, z
 
 
 def gated_linear_fp8_backward(dp, z, x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv,
-                              activation="silu", grad_type=None, out=None):
+                              activation="silu", grad_type=None, out=None, x_fmt=None, w_fmt=None):
     """(dx, dw_gate, dw_up) from dp, the gradient of the product, and the
     forward's z; dtypes as in linear_fp8_backward."""
     if out is not None:
@@ -429,7 +445,7 @@ def gated_linear_fp8_backward(dp, z, x, x_scale_inv, w_gate, w_gate_scale_inv, w
         dg = torch.empty(w_gate.shape, dtype=grad_type or dp.dtype, device=x.device)
         du = torch.empty(w_up.shape, dtype=grad_type or dp.dtype, device=x.device)
     fp8q_gated_linear_backward(dp, z, x, x_scale_inv, w_gate, w_gate_scale_inv, w_up, w_up_scale_inv, dx, dg, du,
-                               activation, _AUTO)
+                               activation, _AUTO, x_fmt=x_fmt, w_fmt=w_fmt)
     return dx, dg, du
 
 
