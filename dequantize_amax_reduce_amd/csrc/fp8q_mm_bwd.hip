@@ -27,6 +27,7 @@
 // largest that it is added to keeps 11 bits.  bf16 operands, the simpler choice
 // at the same MFMA rate, gave 2.4e-3 where f16 results allow 2.1e-4, and 2.9e-3
 // where bf16 results allow 1.7e-3.
+#include "fp8q_ffn_plan.h"
 #include "fp8q_host.h"
 #include "fp8q_mm.h"
 
@@ -566,42 +567,12 @@ void zero(void* p, int64_t n, int dt, hipStream_t st) {
     if (p && n > 0) launch_zero16(p, n * (dt == kF32 ? 2 : 1), st);
 }
 
-int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// The tile height and the split of the contraction with the least estimated
-// time: a round of 256 workgroups takes the measured microseconds below per
-// step of 64 (4096 x 8192 outputs of 4096-long sums: 200, 232 and 256 us at
-// heights 256, 128 and 64) and about 4 to fill and drain; a split writes
-// binary32 sums that the join reads, at about 5 TB/s and a launch.
-struct Plan16 {
-    int bm, splits, kper;
-    int64_t part;          // bytes of partial sums
-};
-Plan16 plan16(int64_t M, int64_t N, int64_t K) {
-    Plan16 p{};
-    const int64_t KB = K / 64, tn = (N + 255) / 256;
-    double best = 0.0;
-    for (int h = 256; h >= 64; h /= 2) {
-        const double each = h == 256 ? 1.56 : h == 128 ? 0.90 : 0.50;
-        const int64_t tiles = (M + h - 1) / h * tn;
-        for (int64_t s = 1; s == 1 || (s <= 32 && tiles * s <= 512 && KB / s >= 4); s *= 2) {
-            const int64_t kper = (KB + s - 1) / s, n = (KB + kper - 1) / kper;
-            const double t = (double)((tiles * n + 255) / 256) * ((double)kper * each + 4.0) +
-                             (n > 1 ? 3.0 + (double)(n * M * N * 8) / 5e6 : 0.0);
-            if (best > 0.0 && t >= best) continue;
-            best = t;
-            p = Plan16{h, (int)n, (int)kper, n > 1 ? n * M * N * 4 : 0};
-        }
-    }
-    return p;
-}
-
 // c[m, n] = sum_k a[m, k] b[n, k]; rows [0, split) to c0, rows from gap to c1;
-// N % 128 == 0
+// N % 128 == 0; p: plan16 of the product
 void mm16(const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K, void* c0, void* c1, int64_t split,
-          int64_t gap, int cdt, const uint32_t* ka, const uint32_t* kb, int qb, float* part, hipStream_t st) {
-    const Plan16 p = plan16(M, N, K);
+          int64_t gap, int cdt, const Plan16& p, const uint32_t* ka, const uint32_t* kb, int qb, float* part, hipStream_t st) {
     Mm16Args a{A, B, M, (int)N, (int)(K / 64), 0, 0, c0, c1, split, gap, cdt, 0, ka, kb, qb, p.kper, p.splits, part};
     a.vec = al(c0, 16) && (!c1 || al(c1, 16));
     a.tn = (uint32_t)((N + 255) / 256);
@@ -655,7 +626,7 @@ BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated) {
     l.kcol = l.krow + 4 * M;
     l.kx = l.kcol + 4 * l.C;
     l.kw = l.kx + 4 * (K / 128);
-    l.part = take(std::max(plan16(M, K, l.C).part, plan16(gated ? l.Np + N : N, K, l.Mp).part) / 2);
+    l.part = take(std::max(plan_dx(M, N, K, gated).part, plan_dw(M, N, K, gated).part) / 2);
     l.bytes = at;
     return l;
 }
@@ -720,10 +691,12 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
             });
         });
     });
-    if (wdx) mm16(dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, krow, kw, qw, part, st);
+    if (wdx)
+        mm16(dz, wt, f.M, f.K, l.C, f.dx, nullptr, f.M, f.M, f.dt, plan_dx(f.M, f.N, f.K, gated), krow, kw, qw, part, st);
     if (wdw) {
-        if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, kcol, kx, qx, part, st);
-        else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, kcol, kx, qx, part, st);
+        const Plan16 w = plan_dw(f.M, f.N, f.K, gated);
+        if (gated) mm16(dzt, xt, l.Np + f.N, f.K, l.Mp, f.dw0, f.dw1, f.N, l.Np, f.dwdt, w, kcol, kx, qx, part, st);
+        else mm16(dzt, xt, f.N, f.K, l.Mp, f.dw0, nullptr, f.N, f.N, f.dwdt, w, kcol, kx, qx, part, st);
     }
 }
 

@@ -6,6 +6,7 @@
 //
 // Many rows: bound by the matrix cores (k_mm).  Few rows: bound by the
 // weights' bytes (k_mm_rows), whose sums are binary32 throughout.
+#include "fp8q_ffn_plan.h"
 #include "fp8q_host.h"
 #include "fp8q_mm.h"
 
@@ -527,55 +528,6 @@ __global__ void __launch_bounds__(512) k_mm_rows(FwdArgs a, float* pbuf) {
 // launchers
 // ---------------------------------------------------------------------------
 
-constexpr int64_t kRowsMax = 16;       // rows that k_mm_rows takes
-constexpr int64_t kExactMax = 64;      // rows up to which sums are binary32 whatever the outputs
-
-// How a product is tiled: rows a tile, and workgroups over K (splits)
-struct Plan {
-    bool rows;
-    int bm, splits, kper;
-    int64_t tm, tn;
-};
-
-// The tile height and the split of K with the least estimated time.  A round
-// of 256 workgroups takes the measured microseconds below per block of K (8192
-// columns, K = 7168, every round full: fp8 sums 257, 282 and 350 us for 4096
-// rows at heights 256, 128 and 64; binary32 sums 413 and 492 at 128 and 64)
-// and about 4 to fill and drain; a split writes its partial sums and the join
-// reads them, at about 5 TB/s and a launch.  ex: binary32 sums (k_mm's EX),
-// whose tiles are at most 128 rows tall: the widened fragments leave registers
-// for no more.
-Plan plan(int64_t M, int64_t N, int64_t K, bool gated, bool ex) {
-    Plan p{};
-    const int64_t KB = K / 128;
-    if (M <= kRowsMax) {
-        p.rows = true;
-        p.splits = 1;
-        return p;
-    }
-    p.tn = (N + (gated ? 127 : 255)) / (gated ? 128 : 256);
-    double best = 0.0;
-    for (int bm = ex ? 128 : 256; bm >= 64; bm /= 2) {
-        const double block = ex ? (bm == 128 ? 1.84 : 1.10) : (bm == 256 ? 2.30 : bm == 128 ? 1.26 : 0.78);
-        const int64_t tm = (M + bm - 1) / bm, tiles = tm * p.tn;
-        for (int64_t s = 1; s == 1 || (s <= 16 && tiles * s <= 512 && KB / s >= 2); s *= 2) {
-            const int64_t kper = std::max<int64_t>(1, (KB + s - 1) / s);
-            const double t = (double)((tiles * s + 255) / 256) * ((double)kper * block + 4.0) +
-                             (s > 1 ? 3.0 + (double)(s * M * N * (gated ? 16 : 8)) / 5e6 : 0.0);
-            if (best > 0.0 && t >= best) continue;
-            best = t;
-            p.bm = bm;
-            p.tm = tm;
-            p.kper = (int)kper;
-            p.splits = (int)std::max<int64_t>(1, (KB + kper - 1) / kper);
-        }
-    }
-    return p;
-}
-
-int64_t part_bytes(const Plan& p, int64_t M, int64_t N, bool gated) {
-    return p.splits > 1 ? p.splits * M * N * (gated ? 8 : 4) : 0;
-}
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 template <int XF, int WF> void run_rows(const FwdArgs& a, float* pbuf, bool gated, hipStream_t st) {

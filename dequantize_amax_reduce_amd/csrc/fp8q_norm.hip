@@ -8,8 +8,9 @@
 // row stays in registers between its two reductions (the sum of squares, and
 // the amax of the cast), as binary32, so that y comes from the sum before its
 // rounding to the element type.
-#include "fp8q_host.h"
 #include "fp8q_ffn_launch.h"
+#include "fp8q_ffn_plan.h"
+#include "fp8q_host.h"
 
 namespace fp8q {
 
@@ -519,63 +520,44 @@ template <int WDT> __global__ void __launch_bounds__(1024) k_norm_dw(const float
     }
 }
 
-constexpr int kNormWaves = 8192;  // waves a launch of the forward pass asks for: what the chip holds at once
-constexpr int kBwdParts = 512;   // workgroups (and partial dweight rows) of the backward pass
-
 // f(bool_constant) over a runtime flag
 template <typename F> void with_bool(bool b, F&& f) {
     if (b) f(std::true_type{});
     else f(std::false_type{});
 }
 
-// Lane vectors a thread (V) for a row of nv vectors held by one workgroup:
-// two, so that the workgroup is about nv / 2 threads and several fit a CU;
-// one or four where the row is short or long.
-int pick_v(int64_t nv) {
-    if (nv <= 256) return 1;
-    return nv <= 2048 ? 2 : 4;
-}
-int threads_for(int64_t nv, int V) { return (int)std::min<int64_t>(1024, ((nv + V - 1) / V + 63) / 64 * 64); }
-
 template <int DT, int FMT> struct NormCast {
     static void run(bool group, bool wf32, const NormArgs& a, hipStream_t st) {
         constexpr int VE = LaneVE<DT>::value;
-        const int64_t nv = ((int64_t)a.cols + VE - 1) / VE;
+        const NormPlan p = norm_plan(a.rows, ((int64_t)a.cols + VE - 1) / VE);
+        const unsigned g = (unsigned)p.groups;
         with_bool(group, [&](auto G) {
             with_bool(wf32 && DT != kF32, [&](auto W) {
                 constexpr bool GR = decltype(G)::value, WF = decltype(W)::value;
-                if (nv <= 128 && a.rows > 256) {           // short rows: a wave each, no barrier
-                    const unsigned g = (unsigned)std::min<int64_t>((a.rows + 3) / 4, kNormWaves / 4);
-                    if (nv <= 64) k_norm_rows<DT, WF, FMT, GR, true, 1, 256><<<g, 256, 0, st>>>(a);
-                    else k_norm_rows<DT, WF, FMT, GR, true, 2, 256><<<g, 256, 0, st>>>(a);
-                } else if (nv <= 4096) {
-                    const int V = pick_v(nv), T = threads_for(nv, V);
-                    const unsigned g = (unsigned)std::min<int64_t>(a.rows, std::max(256, kNormWaves / (T / 64) / 256 * 256));
-                    if (V == 1) k_norm_rows<DT, WF, FMT, GR, false, 1, 256><<<g, T, 0, st>>>(a);
-                    else if (V == 2 && T <= 512) k_norm_rows<DT, WF, FMT, GR, false, 2, 512><<<g, T, 0, st>>>(a);
-                    else if (V == 2) k_norm_rows<DT, WF, FMT, GR, false, 2, 1024><<<g, T, 0, st>>>(a);
-                    else k_norm_rows<DT, WF, FMT, GR, false, 4, 1024><<<g, T, 0, st>>>(a);
-                } else {
-                    k_norm_long<DT, WF, FMT, GR><<<grid(a.rows), 1024, 0, st>>>(a);
-                }
+                const int T = p.threads;
+                if (p.V == 0) k_norm_long<DT, WF, FMT, GR><<<g, T, 0, st>>>(a);
+                else if (p.wave && p.V == 1) k_norm_rows<DT, WF, FMT, GR, true, 1, 256><<<g, T, 0, st>>>(a);
+                else if (p.wave) k_norm_rows<DT, WF, FMT, GR, true, 2, 256><<<g, T, 0, st>>>(a);
+                else if (p.V == 1) k_norm_rows<DT, WF, FMT, GR, false, 1, 256><<<g, T, 0, st>>>(a);
+                else if (p.V == 2 && T <= 512) k_norm_rows<DT, WF, FMT, GR, false, 2, 512><<<g, T, 0, st>>>(a);
+                else if (p.V == 2) k_norm_rows<DT, WF, FMT, GR, false, 2, 1024><<<g, T, 0, st>>>(a);
+                else k_norm_rows<DT, WF, FMT, GR, false, 4, 1024><<<g, T, 0, st>>>(a);
             });
         });
     }
 };
 
-template <int DT> void norm_bwd(bool wf32, const NormBwdArgs& a, unsigned g, hipStream_t st) {
+template <int DT> void norm_bwd(bool wf32, const NormBwdArgs& a, hipStream_t st) {
     constexpr int VE = LaneVE<DT>::value;
-    const int64_t nv = ((int64_t)a.cols + VE - 1) / VE;
+    const NormPlan p = norm_bwd_plan(a.rows, ((int64_t)a.cols + VE - 1) / VE);
+    const unsigned g = (unsigned)p.groups;
     with_bool(wf32 && DT != kF32, [&](auto W) {
         constexpr bool WF = decltype(W)::value;
-        if (nv <= 2048) {
-            const int V = nv <= 256 ? 1 : 2, T = threads_for(nv, V);
-            if (V == 1) k_norm_bwd<DT, WF, 1, 256><<<g, T, 0, st>>>(a);
-            else if (T <= 512) k_norm_bwd<DT, WF, 2, 512><<<g, T, 0, st>>>(a);
-            else k_norm_bwd<DT, WF, 2, 1024><<<g, T, 0, st>>>(a);
-        } else {
-            k_norm_bwd_long<DT, WF><<<g, 1024, 0, st>>>(a);
-        }
+        const int T = p.threads;
+        if (p.V == 0) k_norm_bwd_long<DT, WF><<<g, T, 0, st>>>(a);
+        else if (p.V == 1) k_norm_bwd<DT, WF, 1, 256><<<g, T, 0, st>>>(a);
+        else if (T <= 512) k_norm_bwd<DT, WF, 2, 512><<<g, T, 0, st>>>(a);
+        else k_norm_bwd<DT, WF, 2, 1024><<<g, T, 0, st>>>(a);
     });
 }
 
@@ -588,16 +570,15 @@ void launch_rmsnorm_cast(bool group, const void* x, int dt, const void* res, con
     dispatch_dt_fmt<NormCast>(dt, fmt, group, wdt == kF32, a, st);
 }
 
-int64_t rmsnorm_bwd_parts(int64_t rows) { return std::min<int64_t>(rows < 1 ? 1 : rows, kBwdParts); }
+int64_t rmsnorm_bwd_parts(int64_t rows) { return norm_bwd_parts(rows); }
 
 void launch_rmsnorm_bwd(const void* dy, const void* h, int dt, const void* w, int wdt, const float* rstd,
                         const void* dh, int64_t rows, int64_t cols, void* dx, void* dw, float* ws, hipStream_t st) {
     const int64_t parts = rmsnorm_bwd_parts(rows);
     const NormBwdArgs a{dy, h, w, rstd, dh, rows, (int)cols, dx, dw ? ws : nullptr};
-    const unsigned g = (unsigned)parts;
-    if (dt == kF32) norm_bwd<kF32>(wdt == kF32, a, g, st);
-    else if (dt == kBF16) norm_bwd<kBF16>(wdt == kF32, a, g, st);
-    else norm_bwd<kF16>(wdt == kF32, a, g, st);
+    if (dt == kF32) norm_bwd<kF32>(wdt == kF32, a, st);
+    else if (dt == kBF16) norm_bwd<kBF16>(wdt == kF32, a, st);
+    else norm_bwd<kF16>(wdt == kF32, a, st);
     if (!dw) return;
     const unsigned gc = grid((cols + 31) / 32);            // 1024 threads each: a grid holds fewer than 2^32
     if (wdt == kF32) k_norm_dw<kF32><<<gc, 1024, 0, st>>>(ws, parts, (int)cols, dw);
