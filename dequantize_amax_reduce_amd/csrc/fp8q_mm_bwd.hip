@@ -5,12 +5,13 @@
 //   [dWg ; dWu] = [dg | du]^T X               contraction over the rows
 //
 // Both products run on one 16-bit MFMA kernel (k_mm16) whose operands are
-// contiguous in the contraction, so the operands are laid out first, in one
-// launch after the exponents' two (k_scales, k_keys; k_prep): dz = [dg | du] and its transpose, the transposed dequantized
-// W, and the transposed dequantized X.  That pass moves 8-10 bytes per element
-// of the operands (8 % of the time of 4096 x 7168 -> 18432); the products then
-// run without a transposing read.  Contractions are padded with zeros to 64
-// elements.
+// contiguous in the contraction, so the operands are laid out first: dz =
+// [dg | du] and its transpose, the transposed dequantized W, and the transposed
+// dequantized X, in one launch (k_prep) after the two that find their exponents
+// (k_scales, k_keys).  It moves 8-10 bytes per element of the operands; the
+// products then run without a transposing read.  Gated, 4096 x 7168 -> 18432:
+// 122 us for the exponents, 389 for the layout, 1774 and 1723 for the products.
+// Contractions are padded with zeros to 64 elements.
 //
 // Operands are rounded to f16 (11 bits), each once, below powers of two that
 // the epilogue takes off the sums again:

@@ -22,7 +22,10 @@
  *  - A workspace is scratch for one call: its contents need no initialisation
  *    and hold nothing the caller reads.  It is 256-byte aligned, owned by the
  *    caller and not shared with a call that may run at the same time.  A NULL
- *    workspace is accepted where the size function gives 0.
+ *    workspace is accepted where the size function gives 0.  A backward pass
+ *    lays its operands out there in f16, on every call: about 4 M C + 2 K (C + M)
+ *    bytes with C = N or 2 F (1.2 GB for M = 4096, K = 7168, F = 18432), and
+ *    binary32 partial sums where a contraction is split.
  *  - Outputs do not overlap inputs or one another unless an entry point says
  *    so.
  *
@@ -34,18 +37,21 @@
  *    cast with its scales); where every output is bf16 or f16 and M > 64, the
  *    fp8 matrix instruction sums the block, with about 16 bits kept below the
  *    block's largest product (up to 4e-5 of the sum's rms measured).
- *  - Every sum has a fixed order: the same call gives the same bits.
+ *  - Every sum has a fixed order: the same call gives the same bits.  The order,
+ *    the splits of K and the kind of sum are chosen from M, N and K, so a row's
+ *    last bits may differ between calls of different M (another kernel from 17
+ *    rows on, the fp8 instruction from 65 on).
  *  - NaN and infinities follow the formulas (0 * inf is NaN).
  *  - Backward products take their operands in f16, each rounded once, and sum
  *    in binary32.  The largest scale of each row of X, and of each block row of
  *    W, goes to the gradient's operand as a power of two; then a power of two
  *    brings the largest finite value of every row (for dx) or column (for dw)
  *    of the gradient's operand, and of every 128 columns of K of X's and W's,
- *    under 2^15.  They are taken off the sums.  So a row of dx depends on its own
- *    row of the gradient alone, a row of X or a block row of W whose gradient is
- *    zero on nothing else, and gradients of any magnitude need no scaling:
- *    values down to 2^-29 of the largest of their row, column or 128 columns
- *    keep 11 bits.
+ *    under 2^15.  They are taken off the sums.  So a row of dx does not depend on
+ *    the other rows of the gradient, a row of X or a block row of W that meets no
+ *    gradient changes nothing whatever its scale, and gradients of any magnitude
+ *    need no scaling: values down to 2^-29 of the largest of their row, column or
+ *    128 columns keep 11 bits.
  *  - The gradient of a cast is the identity: gradients are those of the
  *    formulas at the values the codes stand for.
  */
