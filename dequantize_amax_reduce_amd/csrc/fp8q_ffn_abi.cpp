@@ -268,7 +268,7 @@ static fp8q_status_t backward(fp8q::MmBwd& f, int64_t M, int64_t N, int64_t K, b
     if (st != FP8Q_OK) return st;
     if (!grid_ok(M, K) || !grid_ok(2 * N + 64, K)) return FP8Q_EINVAL;
     // the layout pass: 64 x 64 tiles of dy, 64 x 128 of the codes, 256 threads each
-    const int64_t mt = M / 64 + 1, nt = N / 64 + 1;
+    const int64_t mt = M / 64 + 2, nt = N / 64 + 1;         // rows are padded to 64 or 128
     if (mt * nt + (K / 128) * (mt + 2 * nt) >= int64_t(1) << 24) return FP8Q_EINVAL;
     if (gated && (f.dw0 == nullptr) != (f.dw1 == nullptr) && N > 0 && K > 0) return FP8Q_EINVAL;
     const int64_t n = M * N;

@@ -95,10 +95,18 @@ inline Plan16 plan16(int64_t M, int64_t N, int64_t K) {
     }
     return p;
 }
-// the two products of a backward pass: dx, and the weight gradients (for a
-// gated pair one product, the gate's rows padded to 64)
-inline Plan16 plan_dx(int64_t M, int64_t N, int64_t K, bool gated) { return plan16(M, K, (gated ? 2 : 1) * up64(N)); }
-inline Plan16 plan_dw(int64_t M, int64_t N, int64_t K, bool gated) { return plan16(gated ? up64(N) + N : N, K, up64(M)); }
+// The two products of a backward pass: dx, and the weight gradients (for a
+// gated pair one product, the gate's rows padded to 64).  With a rest the
+// contraction is padded to 128 and half as long again in time.
+inline int64_t rows_padded(int64_t M, bool rest) { return rest ? (M + 127) / 128 * 128 : up64(M); }
+inline Plan16 plan_dx(int64_t M, int64_t N, int64_t K, bool gated, bool rest) {
+    const int64_t C = (gated ? 2 : 1) * up64(N);
+    return plan16(M, K, rest ? C + C / 2 : C);
+}
+inline Plan16 plan_dw(int64_t M, int64_t N, int64_t K, bool gated, bool rest) {
+    const int64_t C = rows_padded(M, rest);
+    return plan16(gated ? up64(N) + N : N, K, rest ? C + C / 2 : C);
+}
 
 // ---------------------------------------------------------------------------
 // norms

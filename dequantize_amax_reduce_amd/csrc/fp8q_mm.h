@@ -150,10 +150,9 @@ __device__ __forceinline__ v8i frag(const char* p0, const char* p1) {
     return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
-// p = sum over 128 codes; FA, FB: formats of the first and second operand
-template <int FA, int FB> __device__ __forceinline__ v4f mfma_fp8(v8i a, v8i b) {
-    const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, FA, FB, 0, 0, 0, 0);
+// c + the sum over 128 codes; FA, FB: formats of the first and second operand
+template <int FA, int FB> __device__ __forceinline__ v4f mfma_fp8(v8i a, v8i b, v4f c = {0.0f, 0.0f, 0.0f, 0.0f}) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, FA, FB, 0, 0, 0, 0);
 }
 
 __device__ __forceinline__ v4f mfma_bf16(v4i a, v4i b, v4f c) {

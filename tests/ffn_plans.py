@@ -60,6 +60,22 @@ BACKWARD = {
     (4100, 1024, 100, True): ((128, 1, 4), (64, 13, 5)),
 }
 
+# (M, K, F) of a gated pair with f16 gradients, whose contractions begin with the
+# rest's steps; a split may hold steps of the rest alone, of both, or of neither
+BACKWARD_REST = {
+    (17, 128, 72): ((64, 1, 6), (64, 1, 3)),
+    (17, 128, 640): ((64, 4, 8), (64, 1, 3)),
+    (513, 128, 64): ((64, 1, 3), (64, 2, 8)),
+    (200, 128, 200): ((64, 1, 12), (64, 1, 6)),
+    (200, 128, 8200): ((64, 30, 13), (128, 1, 6)),
+    (200, 384, 8200): ((64, 30, 13), (256, 1, 6)),
+    (2100, 128, 2053): ((128, 15, 7), (64, 2, 26)),
+    (3000, 128, 2052): ((64, 4, 25), (128, 4, 18)),
+    (4100, 128, 2053): ((256, 15, 7), (256, 15, 7)),
+    (4100, 2048, 72): ((256, 1, 6), (64, 8, 13)),
+    (6000, 640, 72): ((128, 1, 6), (64, 16, 9)),
+}
+
 # (rows, columns, dtype): (a wave a row, lane vectors a thread, threads, rows the grid takes at once)
 NORM = {
     (8300, 256, "bf16"): (True, 1, 256, 8192),
@@ -105,8 +121,8 @@ class Plans:
     def forward(self, M, K, N, gated, exact):
         return self._ask("shim_fwd", 3, (M, N, K), (gated, exact))
 
-    def backward(self, M, K, N, gated):
-        return self._ask("shim_dx", 3, (M, N, K), (gated,)), self._ask("shim_dw", 3, (M, N, K), (gated,))
+    def backward(self, M, K, N, gated, rest=False):
+        return tuple(self._ask(f, 3, (M, N, K), (gated, rest)) for f in ("shim_dx", "shim_dw"))
 
     def norm(self, rows, cols, dt):
         w, *rest = self._ask("shim_norm", 4, (rows, vectors(cols, dt)))

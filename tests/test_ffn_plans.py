@@ -5,7 +5,7 @@ import shutil
 
 import pytest
 
-from ffn_plans import BACKWARD, FORWARD, NORM, NORM_BACKWARD, NORM_ODD, Plans
+from ffn_plans import BACKWARD, BACKWARD_REST, FORWARD, NORM, NORM_BACKWARD, NORM_ODD, Plans
 
 
 @pytest.fixture(scope="module")
@@ -20,6 +20,8 @@ def test_sizes_reach_their_kernels(plans):
         assert plans.forward(*key) == want, key
     for key, want in BACKWARD.items():
         assert plans.backward(*key) == want, key
+    for key, want in BACKWARD_REST.items():
+        assert plans.backward(*key, True, True) == want, key
     for table in (NORM, NORM_ODD):
         for key, want in table.items():
             assert plans.norm(*key) == want, key
@@ -43,6 +45,17 @@ def test_every_variant_is_reached():
         for product in (0, 1):
             got = {(p[product][0], p[product][1] > 1) for k, p in BACKWARD.items() if k[3] == gated and p[product][2] > 2}
             assert got == {(bm, s) for bm in (64, 128, 256) for s in (False, True)}, (gated, product)
+    for product in (0, 1):
+        got = {(p[product][0], p[product][1] > 1) for p in BACKWARD_REST.values() if p[product][2] > 2}
+        assert got == {(bm, s) for bm in (64, 128, 256) for s in (False, True)}, product
+    # splits of the rest's steps alone, of both kinds, and of f16 steps alone
+    kinds = set()
+    for (M, _, F), plan in BACKWARD_REST.items():
+        for (_, splits, kper), C in zip(plan, (2 * ((F + 63) // 64 * 64), (M + 127) // 128 * 128)):
+            for i in range(splits):
+                first, end = i * kper, min((i + 1) * kper, C // 64 + C // 128)
+                kinds.add("rest" if end <= C // 128 else "f16" if first >= C // 128 else "both")
+    assert kinds == {"rest", "both", "f16"}
     for table in (NORM, NORM_ODD, NORM_BACKWARD):
         for (rows, _, _), (_, _, _, at_once) in table.items():
             assert rows > at_once

@@ -7,7 +7,7 @@ import torch
 
 import dequantize_amax_reduce_amd as fq
 import test_gpu_ffn as T
-from ffn_plans import BACKWARD, FORWARD, NORM, NORM_BACKWARD, NORM_ODD
+from ffn_plans import BACKWARD, BACKWARD_REST, FORWARD, NORM, NORM_BACKWARD, NORM_ODD
 from gpu_util import G, TORCH_HP
 from test_gpu_ffn import D, codes, gen_of, rand, up, w64, x64
 
@@ -54,6 +54,33 @@ def test_backward(size):
     else:
         T.test_linear_backward(M, K, N, "f16", "f32", "e4m3fn")
         T.test_linear_backward(M, K, N, "bf16", "bf16", "e5m2")
+
+
+@pytest.mark.parametrize("size", list(BACKWARD_REST), ids=ident)
+@pytest.mark.parametrize("gdt,act", [("f16", "gelu"), ("f32", "silu")])
+def test_gated_backward_f16(size, gdt, act):
+    T.test_gated_backward(*size, "f16", gdt, act)
+
+
+@pytest.mark.parametrize("M,K,F", [(257, 512, 384), (200, 384, 8200), (4100, 128, 2053), (17, 128, 640)])
+def test_f16_gradients_have_one_rounded_operand(M, K, F):
+    """The gradients of a gated pair in f16: their own rounding and that of X' or
+    W', which have the same size in root mean square (an operand's relative error
+    is a sum's), so sqrt(2) of their own; what the rest leaves of dz is a tenth
+    of a rounding (e5m2, 2^-3 at most and half that in root mean square, of the
+    rest and of its partner).  1.5 in all; with dz's rounding it is sqrt(3)."""
+    g = gen_of(M, K, F, "rest")
+    xq, xs = codes(g, M, K, "e4m3fn", M)
+    (gq, gs), (uq, us) = (codes(g, F, K, "e4m3fn", (F + 127) // 128) for _ in range(2))
+    xs, gs, us = (torch.exp(0.3 * rand(g, *t.shape)) * 2.0 ** -6 for t in (xs, gs, us))
+    dp, z = (0.05 * rand(g, M, F)).half(), (1.5 * rand(g, M, 2 * F)).half()
+    X, Wg, Wu = x64(xq, xs), w64(gq, gs), w64(uq, us)
+    a, da = T.act64("silu", z[:, :F].to(D))
+    dg, du = dp.to(D) * z[:, F:].to(D) * da, dp.to(D) * a
+    got = fq.gated_linear_fp8_backward(up(dp), up(z), up(xq), up(xs), up(gq), up(gs), up(uq), up(us))
+    for v, want in zip(got, (dg @ Wg + du @ Wu, dg.t() @ X, du.t() @ X)):
+        e = (v.cpu().to(D) - want).norm()
+        assert e <= 1.5 * (want.half().to(D) - want).norm(), float(e / want.norm())
 
 
 @pytest.mark.parametrize("M,K,N", [s for s in sizes(False, False)] + [(100, 4096, 264)])
@@ -125,8 +152,9 @@ def _same(a, b):
     assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
-@pytest.mark.parametrize("size", list(BACKWARD), ids=ident)
-def test_backward_workspace(size):
+@pytest.mark.parametrize("size,dt", [(k, torch.bfloat16) for k in BACKWARD] +
+                         [((*k, True), torch.float16) for k in BACKWARD_REST], ids=lambda v: ident(v) or str(v))
+def test_backward_workspace(size, dt):
     """A workspace of exactly the documented size between guards, full of NaN
     patterns: nothing is read before it is written, and nothing is written past it."""
     M, K, N, gated = size
@@ -134,8 +162,8 @@ def test_backward_workspace(size):
     xq, xs = codes(g, M, K, "e4m3fn", M)
     w = [codes(g, N, K, "e4m3fn", (N + 127) // 128) for _ in range(1 + gated)]
     args = [up(t) for t in (xq, xs, *(t for p in w for t in p))]
-    dy = up(rand(g, M, N).bfloat16())
-    lead = (dy, up(rand(g, M, 2 * N).bfloat16())) if gated else (dy,)
+    dy = up(rand(g, M, N).to(dt))
+    lead = (dy, up(rand(g, M, 2 * N).to(dt))) if gated else (dy,)
     need = (fq.fp8q_gated_linear_backward_workspace_bytes if gated else fq.fp8q_linear_backward_workspace_bytes)(M, N, K)
     want = (fq.gated_linear_fp8_backward if gated else fq.linear_fp8_backward)(*lead, *args)
     f = fq.fp8q_gated_linear_backward if gated else fq.fp8q_linear_backward

@@ -9,6 +9,8 @@ row of W, dx = (dz 2^ew)(W 2^-ew) and dW = (dz 2^ex)^T (X 2^-ex), and each
 operand is rounded to f16 below a power of two of its own (per row of the
 first, per 128 columns of the second):
 
+(a gated pair's take the scale itself, which is within a factor of two)
+
 * a value is within 2^-11 of itself, or within half an f16 subnormal's unit,
   2^-25 of the scaled value: the largest of a row lies in [2^14, 2^15), so
   2^-39 of it; the codes' bound is 2^q times twice the largest scale's power of
