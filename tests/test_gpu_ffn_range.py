@@ -150,3 +150,30 @@ def test_gated_backward_spread(M, K, F, act, dt):
     near(dx, want, out_tol(want, dt, err), "dx")
     for got, v, ev, what in ((dwg, dg, eg, "dw_gate"), (dwu, du, eu, "dw_up")):
         near(got, v.t() @ X, out_tol(v.t() @ X, "f32", dw_err(v.abs() + ev, xq, xs, M + 64) + ev.t() @ X.abs()), what)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_gated_nan_and_infinity_stay_in_their_row(dt):
+    """A NaN or infinity in one row of dp (or of z) reaches that row of dx and no
+    other, and of the weight gradients the rows of its column."""
+    g = gen_of("gnan", dt)
+    M, K, F = 140, 256, 200
+    T = TORCH_HP[dt]
+    xq, xs = codes(g, M, K, "e4m3fn", M)
+    w = [up(t) for p in (codes(g, F, K, "e4m3fn", 2) for _ in range(2)) for t in p]
+    dp, z = (0.01 * rand(g, M, F)).to(T), rand(g, M, 2 * F).to(T)
+    dp[5] = 0.0
+    call = lambda dp, z: fq.gated_linear_fp8_backward(up(dp), up(z), up(xq), up(xs), *w)
+    clean = call(dp, z)
+    assert all(torch.isfinite(t).all() for t in clean) and (clean[0][5] == 0).all()
+    rest = torch.arange(M) != 5
+    for where, bad in (("dp", float("nan")), ("dp", float("inf")), ("z", float("nan"))):
+        d, y = dp.clone(), z.clone()
+        (d if where == "dp" else y)[5, 7] = bad
+        dx, dg, du = call(d, y)
+        assert not torch.isfinite(dx[5]).any()
+        assert torch.equal(dx.cpu()[rest], clean[0].cpu()[rest])
+        cols = torch.arange(F) != 7
+        for got, want in ((dg, clean[1]), (du, clean[2])):
+            assert not torch.isfinite(got[7]).all()
+            assert torch.equal(got.cpu()[cols], want.cpu()[cols])
