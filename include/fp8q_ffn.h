@@ -84,6 +84,8 @@ typedef enum { FP8Q_SILU = 0, FP8Q_GELU = 1, FP8Q_GELU_TANH = 2 } fp8q_act_t;
  * x, residual, h: [rows, cols] of xdtype.  residual may be NULL (h = x).
  * h may be NULL (not written) and may be x or residual itself (in place).
  * weight: [cols] of wdtype, which is xdtype or FP8Q_F32 (else FP8Q_EDTYPE).
+ * The sum of squares is binary32: a row with values past 1.8e19 gets rstd = 0,
+ * as an infinite mean gives it.
  * rstd: [rows] floats, or NULL.  rows == 0 is a no-op; cols == 0 is a no-op
  * except that the per-channel form writes scale_inv[r] = 1 and, for both,
  * rstd is not written.
