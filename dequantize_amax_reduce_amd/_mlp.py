@@ -1,0 +1,208 @@
+"""Binding of include/fp8q_mlp.h: layer norm and projections with a bias, an
+activation and a residual in their epilogue, on fp8 operands.
+
+Re-exported by the package; laid out as _ffn.py is.
+
+    q, s, h, mean, rstd = layernorm_cast(x, weight, bias, residual)     # norm -> fp8 per 128-group
+    dx, dweight, dbias = layernorm_backward(dn, h, weight, mean, rstd, dh)
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+import re
+
+import torch
+
+from . import _ffn
+from ._ffn import _AUTO, _f32, _flat, _hp_dtype, _opt, _ptr, _same, _stream, _ws
+
+MLP_HEADER_PATH = os.path.join(os.path.dirname(_ffn.FFN_HEADER_PATH), "fp8q_mlp.h")
+
+_P, _I64, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+MLP_SIGNATURES = {
+    "fp8q_layernorm": (_I, [_P, _I, _P, _P, _P, _I, _I64, _I64, _F, _P, _P, _P, _P, _P]),
+    "fp8q_layernorm_cast_group128": (_I, [_P, _I, _P, _P, _P, _I, _I64, _I64, _F, _I, _P, _P, _P, _P, _P, _P]),
+    "fp8q_layernorm_cast_per_channel": (_I, [_P, _I, _P, _P, _P, _I, _I64, _I64, _F, _I, _P, _P, _P, _P, _P, _P]),
+    "fp8q_layernorm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
+    "fp8q_layernorm_backward": (_I, [_P, _P, _I, _P, _I, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P]),
+}
+MLP_FUNCTIONS = tuple(MLP_SIGNATURES)
+
+
+def load_mlp(L):
+    """Set the signatures of these entry points on a library handle."""
+    for name, (res, args) in MLP_SIGNATURES.items():
+        fn = getattr(L, name)
+        fn.restype = res
+        fn.argtypes = args
+    return L
+
+
+def mlp_header_functions() -> list:
+    """Names of the functions include/fp8q_mlp.h declares."""
+    with open(MLP_HEADER_PATH) as f:
+        text = f.read()
+    return sorted(set(re.findall(r"^(?:fp8q_status_t|size_t)\s+(fp8q_\w+)\s*\(", text, re.M)))
+
+
+# set by the package once its own marshalling helpers exist
+lib = _check = _fmt = _fp8 = _FP8_DTYPE = None
+
+
+def _bind(package_lib, helpers):
+    global lib
+    lib = load_mlp(package_lib)
+    globals().update({k: helpers[k] for k in ("_check", "_fmt", "_fp8", "_FP8_DTYPE")})
+
+
+_current = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _call(name, like, tensors, *args):
+    """The C call on `like`'s device (every tensor's), which a launch needs as
+    the thread's current one."""
+    if like.is_cuda:
+        d = like.get_device()
+        for t in tensors:
+            if t is not None and t.get_device() != d:
+                raise ValueError(f"{name}: tensors on different devices")
+        if d != _current():
+            with torch.cuda.device(d):
+                st = getattr(lib, name)(*args)
+                if st:
+                    _check(st, name)
+                return
+    st = getattr(lib, name)(*args)
+    if st:
+        _check(st, name)
+
+
+# ---------------------------------------------------------------------------
+# one function per C entry point
+# ---------------------------------------------------------------------------
+
+def _affine(name, x, weight, bias, dtype_of):
+    cols = x.shape[-1]
+    if weight.numel() != cols:
+        raise ValueError(f"{name}: weight must have {dtype_of}'s last dimension")
+    if bias is not None and (bias.numel() != cols or bias.dtype != weight.dtype):
+        raise ValueError(f"{name}: bias must match weight")
+
+
+def _norm(name, x, weight, bias, y, scale_inv, residual, h, mean, rstd, eps, fmt, stream):
+    rows, cols = _flat(x, "x")
+    dt = _hp_dtype(x, "x")
+    _affine(name, x, weight, bias, "x")
+    _same(residual, (rows, cols), x.dtype, "residual")
+    _same(h, (rows, cols), x.dtype, "h")
+    out = []
+    if name == "fp8q_layernorm":
+        _same(y, (rows, cols), x.dtype, "y")
+        out = [_ptr(y, "y")]
+    else:
+        f = _fp8(y, fmt, "q")
+        if y.numel() != rows * cols:
+            raise ValueError(f"{name}: q must match x")
+        scales = rows if name == "fp8q_layernorm_cast_per_channel" else rows * (cols // 128)
+        out = [f, _ptr(y, "q"), _f32(scale_inv, scales, "scale_inv")]
+    _call(name, x, (weight, bias, y, scale_inv, residual, h, mean, rstd), _ptr(x, "x"), dt, _opt(residual, "residual"),
+          _ptr(weight, "weight"), _opt(bias, "bias"), _hp_dtype(weight, "weight"), rows, cols, eps, *out, _opt(h, "h"),
+          0 if mean is None else _f32(mean, rows, "mean"), 0 if rstd is None else _f32(rstd, rows, "rstd"),
+          _stream(x, stream))
+
+
+def fp8q_layernorm(x, weight, bias, y, residual=None, h=None, mean=None, rstd=None, eps=1e-5, stream=None) -> None:
+    _norm("fp8q_layernorm", x, weight, bias, y, None, residual, h, mean, rstd, eps, None, stream)
+
+
+def fp8q_layernorm_cast_group128(x, weight, bias, q, scale_inv, residual=None, h=None, mean=None, rstd=None, eps=1e-5,
+                                 fmt=None, stream=None) -> None:
+    _norm("fp8q_layernorm_cast_group128", x, weight, bias, q, scale_inv, residual, h, mean, rstd, eps, fmt, stream)
+
+
+def fp8q_layernorm_cast_per_channel(x, weight, bias, q, scale_inv, residual=None, h=None, mean=None, rstd=None,
+                                    eps=1e-5, fmt=None, stream=None) -> None:
+    _norm("fp8q_layernorm_cast_per_channel", x, weight, bias, q, scale_inv, residual, h, mean, rstd, eps, fmt, stream)
+
+
+def fp8q_layernorm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return lib.fp8q_layernorm_backward_workspace_bytes(rows, cols)
+
+
+def fp8q_layernorm_backward(dy, h, weight, mean, rstd, dx, dweight=None, dbias=None, dh=None, workspace=None,
+                            stream=None) -> None:
+    name = "fp8q_layernorm_backward"
+    rows, cols = _flat(h, "h")
+    dt = _hp_dtype(h, "h")
+    for t, n in ((dy, "dy"), (dx, "dx"), (dh, "dh")):
+        _same(t, (rows, cols), h.dtype, n)
+    _affine(name, h, weight, None, "h")
+    for t, n in ((dweight, "dweight"), (dbias, "dbias")):
+        if t is not None and (t.numel() != cols or t.dtype != weight.dtype):
+            raise ValueError(f"{name}: {n} must match weight")
+    need = lib.fp8q_layernorm_backward_workspace_bytes(rows, cols) if dweight is not None or dbias is not None else 0
+    ws = _ws(workspace, need, h, name)
+    _call(name, h, (dy, weight, mean, rstd, dx, dweight, dbias, dh, ws), _ptr(dy, "dy"), _ptr(h, "h"), dt,
+          _ptr(weight, "weight"), _hp_dtype(weight, "weight"), _f32(mean, rows, "mean"), _f32(rstd, rows, "rstd"),
+          _opt(dh, "dh"), rows, cols, _ptr(dx, "dx"), _opt(dweight, "dweight"), _opt(dbias, "dbias"),
+          _opt(ws, "workspace"), _stream(h, stream))
+
+
+# ---------------------------------------------------------------------------
+# helpers that allocate outputs and workspaces
+# ---------------------------------------------------------------------------
+
+def _stats(x, rows, residual):
+    f = lambda: torch.empty(rows, dtype=torch.float32, device=x.device)
+    return x if residual is None else torch.empty_like(x, memory_format=torch.contiguous_format), f(), f()
+
+
+def layernorm(x, weight, bias=None, residual=None, eps=1e-5, out=None):
+    """(y, h, mean, rstd): h = x + residual, y = (h - mean) / sqrt(var + eps) *
+    weight + bias over the last dimension, in x's dtype.  h is x itself without
+    a residual; h, mean and rstd are what layernorm_backward reads.  `out`:
+    those four tensors, caller-allocated (without a residual, x itself may
+    stand for h; another tensor gets a copy of x)."""
+    if out is not None:
+        y, h, mean, rstd = out
+    else:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        h, mean, rstd = _stats(x, _flat(x, "x")[0], residual)
+    _norm("fp8q_layernorm", x, weight, bias, y, None, residual, None if h is x else h, mean, rstd, eps, None, None)
+    return y, h, mean, rstd
+
+
+def layernorm_cast(x, weight, bias=None, residual=None, eps=1e-5, fp8_format="e4m3fn", per_channel_scale=False,
+                   out=None):
+    """(q, scale_inv, h, mean, rstd): layernorm's y cast to fp8 per 128 columns
+    (scale_inv [rows, cols/128]) or per row (per_channel_scale=True, scale_inv
+    [rows]) without a copy in x's dtype in between; h and `out` as there."""
+    rows, cols = _flat(x, "x")
+    if out is not None:
+        q, s, h, mean, rstd = out
+    else:
+        q = torch.empty(x.shape, dtype=_FP8_DTYPE[_fmt(fp8_format)], device=x.device)
+        s = torch.empty((rows,) if per_channel_scale else (rows, cols // 128), dtype=torch.float32, device=x.device)
+        h, mean, rstd = _stats(x, rows, residual)
+    name = "fp8q_layernorm_cast_per_channel" if per_channel_scale else "fp8q_layernorm_cast_group128"
+    _norm(name, x, weight, bias, q, s, residual, None if h is x else h, mean, rstd, eps, fp8_format, None)
+    return q, s, h, mean, rstd
+
+
+def layernorm_backward(dy, h, weight, mean, rstd, dh=None, with_bias=True, out=None):
+    """(dx, dweight, dbias) of layernorm and layernorm_cast; dx is the gradient
+    of x and of the residual, dbias None with with_bias=False.  dh: the gradient
+    that reaches h along the residual path."""
+    if out is not None:
+        dx, dw, db = out
+    else:
+        dx, dw = torch.empty_like(h), torch.empty_like(weight)
+        db = torch.empty_like(weight) if with_bias else None
+    fp8q_layernorm_backward(dy, h, weight, mean, rstd, dx, dw, db if with_bias else None, dh, _AUTO)
+    return dx, dw, db if with_bias else None
+
+
+MLP_NAMES = [n for n in dir() if n.startswith("fp8q_")] + [
+    "MLP_HEADER_PATH", "MLP_FUNCTIONS", "mlp_header_functions", "load_mlp",
+    "layernorm", "layernorm_cast", "layernorm_backward"]

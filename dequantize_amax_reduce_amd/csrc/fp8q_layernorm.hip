@@ -1,0 +1,577 @@
+// fp8q_layernorm.hip -- residual addition, layer norm and the cast of its
+// result to fp8 (or its rounding to the input's type), and the norm's backward
+// pass.
+//
+//   h = x + r;  mean = sum h / C;  rstd = 1 / sqrt(sum (h - mean)^2 / C + eps);
+//   y = ((h - mean) * rstd) * w + b;  q, scale_inv = cast(y).
+//
+// Bound by HBM: x and r are read once, h and y (or its codes and scales)
+// written once.  A row stays in registers between its reductions, as binary32.
+//
+// The mean is m0 + m1: m0 the rounded mean of h, m1 the mean of d = h - m0,
+// which is exact where h is near m0; the variance is mean(d^2) - m1^2.  So a
+// row of values far from zero keeps the bits that its deviations have in h.
+// (With m0 alone a constant row of 1000s, whose y is b, would be off by what
+// m0's rounding leaves: 6e-5 / sqrt(eps), 2 % of the weight at eps = 1e-5.)
+#include "fp8q_ffn_plan.h"
+#include "fp8q_mlp_launch.h"
+#include "fp8q_rows.h"
+
+namespace fp8q {
+
+namespace {
+
+// sums of two values over the lanes of a row, as row_sum; lds: 32 words
+template <bool WAVE> __device__ __forceinline__ void row_sum2(float& a, float& b, float* lds) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (WAVE) return;
+    const int nw = (int)blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+        lds[threadIdx.x >> 6] = a;
+        lds[16 + (threadIdx.x >> 6)] = b;
+    }
+    lds_barrier();
+    a = lds[0];
+    b = lds[16];
+    for (int i = 1; i < nw; ++i) {
+        a += lds[i];
+        b += lds[16 + i];
+    }
+}
+
+// rstd from the mean of d^2 and that of d (a NaN passes the clamp)
+__device__ __forceinline__ float rstd_of(float s2, float m1, float n, float eps) {
+    const float v = s2 / n - m1 * m1;
+    return 1.0f / sqrtf((v < 0.0f ? 0.0f : v) + eps);
+}
+
+// y of one lane vector from d = h - m0
+template <int VE> __device__ __forceinline__ void norm_y(float* d, float m1, float rs, const float* w, const float* b) {
+#pragma unroll
+    for (int k = 0; k < VE; ++k) d[k] = __builtin_fmaf((d[k] - m1) * rs, w[k], b[k]);
+}
+
+// VE weights from column c, kept as loaded; WF32: they are binary32 whatever
+// the activations are
+template <int DT, bool WF32> struct Affine {
+    static constexpr bool kWide = WF32 && DT != kF32;
+    v4u r[kWide ? 2 : 1];
+    __device__ __forceinline__ void load(const void* w, int c) {
+        const v4u_a2* p = (const v4u_a2*)((const char*)w + (int64_t)c * (kWide ? 4 : ESize<DT>::value));
+#pragma unroll
+        for (int i = 0; i < (kWide ? 2 : 1); ++i) r[i] = v4u{p[i].x, p[i].y, p[i].z, p[i].w};
+    }
+    __device__ __forceinline__ void clear() {
+        for (v4u& x : r) x = v4u{0, 0, 0, 0};
+    }
+    // the asm keeps the compiler from widening once for all rows, which holds twice the registers
+    __device__ __forceinline__ void widen(float* v) {
+#pragma unroll
+        for (int i = 0; i < (kWide ? 2 : 1); ++i) {
+            asm volatile("" : "+v"(r[i]));
+            widen16<kWide ? kF32 : DT>(r[i], v + 4 * i);
+        }
+    }
+};
+
+// Where a thread's lane vector v of a row stands: from column c, of which the
+// first `dup` elements are another lane's.  The last vector of a row whose width
+// is not whole vectors ends at the row's end instead of past it, and so repeats
+// elements of the one before: they are computed again, to the same bits, stored
+// twice and summed once, and no access has a partial path.  (Such paths, taken by
+// one lane, held a mask for every element across the loop: 20 to 250 spilled
+// registers.)  Vectors past the end are all `dup`, and are not stored.
+template <int VE> struct Place {
+    int c, dup;
+    __device__ __forceinline__ Place(int at, int cols) {
+        c = at + VE <= cols ? at : cols - VE;
+        dup = min(at - c, VE);
+    }
+    __device__ __forceinline__ bool in() const { return dup < VE; }
+};
+
+template <int DT, bool NT> __device__ __forceinline__ v4u ld_at(const void* row, int c) {
+    const v4u_a2* p = (const v4u_a2*)((const char*)row + (int64_t)c * ESize<DT>::value);
+    const v4u_a2 t = NT ? __builtin_nontemporal_load(p) : *p;
+    return v4u{t.x, t.y, t.z, t.w};
+}
+template <int DT, bool NT> __device__ __forceinline__ void st_at(void* row, int c, const float* y) {
+    const v4u t = pack_out16<DT>(y);
+    v4u_a2* d = (v4u_a2*)((char*)row + (int64_t)c * ESize<DT>::value);
+    if constexpr (NT) __builtin_nontemporal_store(v4u_a2{t.x, t.y, t.z, t.w}, d);
+    else *d = v4u_a2{t.x, t.y, t.z, t.w};
+}
+
+// One row per workgroup (or, WAVE, per wave) at a time, V lane vectors a
+// thread.  A workgroup takes several rows, so that weight and bias are read
+// once and the next row's loads are in flight through the reductions and stores
+// of this one (TB, the most threads: up to 512 leave the registers for that).
+// A reduction's LDS words are written again after another reduction's barrier.
+template <int DT, bool WF32, int FMT, int TO, bool WAVE, int V, int TB>
+__global__ void __launch_bounds__(TB) k_ln_rows(LayerNorm a) {
+    constexpr bool PF = TB <= 512, NT = TO == kToGroup;
+    constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
+    __shared__ float lds_s[16], lds_d[32];
+    __shared__ uint32_t lds_m[16];
+    const int cols = (int)a.cols;
+    const float fc = (float)cols;
+    const int lanes = WAVE ? 64 : (int)blockDim.x;
+    const int t = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+    const int per = WAVE ? (int)blockDim.x >> 6 : 1;        // rows a workgroup takes at once
+    const int64_t first = (int64_t)blockIdx.x * per + (WAVE ? threadIdx.x >> 6 : 0), next = (int64_t)gridDim.x * per;
+    if (first >= a.rows) return;                            // whole waves; whole workgroups unless WAVE
+    auto place = [&](int v) { return Place<VE>((v * lanes + t) * VE, cols); };
+    v4u xv[V], rv[V];
+    auto load = [&](int64_t row) {
+        const int64_t off = row * a.cols * ES;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = place(v).c;
+            xv[v] = ld_at<DT, NT>((const char*)a.x + off, c);
+            if (a.res) rv[v] = ld_at<DT, NT>((const char*)a.res + off, c);
+        }
+    };
+    load(first);
+    constexpr bool HOLD = V <= 2;                           // four vectors leave no registers for them
+    Affine<DT, WF32> w[V], b[V];
+    auto load_wb = [&](int v) {
+        w[v].load(a.w, place(v).c);
+        if (a.b) b[v].load(a.b, place(v).c);
+        else b[v].clear();
+    };
+    if (HOLD)
+#pragma unroll
+        for (int v = 0; v < V; ++v) load_wb(v);
+    for (int64_t row = first; row < a.rows; row += next) {
+        float h[V][VE];
+        float s = 0.0f;
+        // the asm keeps the compiler from holding a mask for every element across the rows
+        int dup[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            dup[v] = place(v).dup;
+            asm volatile("" : "+v"(dup[v]));
+            sum_h<DT>(xv[v], rv[v], a.res != nullptr, h[v]);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) s += k >= dup[v] ? h[v][k] : 0.0f;
+        }
+        if (PF && row + next < a.rows) load(row + next);
+        const float m0 = row_sum<WAVE>(s, lds_s) / fc;
+        if (a.h) {
+            void* hr = (char*)a.h + row * a.cols * ES;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (place(v).in()) st_at<DT, NT>(hr, place(v).c, h[v]);
+        }
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+                h[v][k] -= m0;
+                const float d = k >= dup[v] ? h[v][k] : 0.0f;
+                s1 += d;
+                s2 = __builtin_fmaf(d, d, s2);
+            }
+        row_sum2<WAVE>(s1, s2, lds_d);
+        const float m1 = s1 / fc, rs = rstd_of(s2, m1, fc, a.eps);
+        if (t == 0) {
+            if (a.mean) a.mean[row] = m0 + m1;
+            if (a.rstd) a.rstd[row] = rs;
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float wv[VE], bv[VE];
+            if (!HOLD) load_wb(v);
+            w[v].widen(wv);
+            b[v].widen(bv);
+            norm_y<VE>(h[v], m1, rs, wv, bv);
+            if constexpr (TO == kToRow)                     // elements seen twice change no maximum
+#pragma unroll
+                for (int k = 0; k < VE; ++k) m = umax(m, __float_as_uint(h[v][k]) & 0x7FFFFFFFu);
+            if (!HOLD) __builtin_amdgcn_sched_barrier(0);   // no registers for several vectors' weights at once
+        }
+        float scale = 0.0f;
+        bool satur = false;
+        if constexpr (TO == kToRow) scale = row_scale<FMT>(row_max<WAVE>(m, lds_m), a.sinv + row, t == 0, &satur);
+        uint8_t* yr = (uint8_t*)a.y + row * a.cols * (TO == kToPlain ? ES : 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Place<VE> p = place(v);
+            if constexpr (TO == kToPlain) {
+                if (p.in()) st_at<DT, NT>(yr, p.c, h[v]);
+            } else if constexpr (TO == kToGroup) {
+                // whole vectors; the lanes of a group stay together for its maximum
+                cast_vec<DT, FMT, true>(h[v], (v * lanes + t) * VE, cols, yr, a.sinv + row * (cols >> 7), 0.0f, false);
+            } else if (p.in()) {
+                float q[VE];
+#pragma unroll
+                for (int k = 0; k < VE; ++k) q[k] = satur ? sat<FMT>(h[v][k] * scale) : h[v][k] * scale;
+                st_codes<FMT, VE, false>(yr, p.c, p.c + VE, q);
+            }
+        }
+        if (!PF && row + next < a.rows) load(row + next);
+    }
+}
+
+// one lane vector's part of the long rows' outputs
+template <int DT, int FMT, int TO>
+__device__ __forceinline__ void put_y(const LayerNorm& a, int64_t row, int c, const float* y, float scale, bool satur) {
+    if constexpr (TO == kToPlain) {
+        if (c < (int)a.cols) st_row<DT, false>((char*)a.y + row * a.cols * ESize<DT>::value, c, (int)a.cols, y);
+    } else {
+        cast_vec<DT, FMT, TO == kToGroup>(y, c, (int)a.cols, (uint8_t*)a.y + row * a.cols,
+                                          TO == kToGroup ? a.sinv + row * (a.cols >> 7) : nullptr, scale, satur);
+    }
+}
+
+// Rows too long for registers, or shorter than a vector: passes over the row, the later ones mostly from
+// cache.  h and y are written in the last pass, after a lane's own reads of the
+// same columns, so that they may be x or the residual itself.
+template <int DT, bool WF32, int FMT, int TO> __global__ void __launch_bounds__(1024) k_ln_long(LayerNorm a) {
+    constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
+    __shared__ float lds_s[16], lds_d[32];
+    __shared__ uint32_t lds_m[16];
+    const int cols = (int)a.cols, step = (int)blockDim.x * VE, c0 = (int)threadIdx.x * VE;
+    const float fc = (float)cols;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const int64_t off = row * a.cols * ES;
+        const void* xr = (const char*)a.x + off;
+        const void* rr = a.res ? (const char*)a.res + off : nullptr;
+        float s = 0.0f;
+        for (int64_t c = c0; c < cols; c += step) {
+            float h[VE];
+            load_h<DT>(xr, rr, (int)c, cols, h);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) s += h[k];
+        }
+        const float m0 = row_sum<false>(s, lds_s) / fc;
+        // d of the columns from c on, zero past the row's end
+        auto diff = [&](int64_t c, float* d) {
+            load_h<DT>(xr, rr, (int)c, cols, d);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) d[k] = c + k < cols ? d[k] - m0 : 0.0f;
+        };
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int64_t c = c0; c < cols; c += step) {
+            float d[VE];
+            diff(c, d);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+                s1 += d[k];
+                s2 = __builtin_fmaf(d[k], d[k], s2);
+            }
+        }
+        row_sum2<false>(s1, s2, lds_d);
+        const float m1 = s1 / fc, rs = rstd_of(s2, m1, fc, a.eps);
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = m0 + m1;
+            if (a.rstd) a.rstd[row] = rs;
+        }
+        auto affine = [&](int64_t c, float* d) {
+            float w[VE], b[VE];
+            ld_weight<DT, WF32>(a.w, (int)c, cols, w);
+            ld_weight<DT, WF32>(a.b ? a.b : a.w, (int)c, a.b ? cols : 0, b);
+            norm_y<VE>(d, m1, rs, w, b);
+        };
+        float scale = 0.0f;
+        bool satur = false;
+        if constexpr (TO == kToRow) {
+            uint32_t m = 0;
+            for (int64_t c = c0; c < cols; c += step) {
+                float d[VE];
+                diff(c, d);
+                affine(c, d);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) m = umax(m, c + k < cols ? __float_as_uint(d[k]) & 0x7FFFFFFFu : 0u);
+            }
+            scale = row_scale<FMT>(row_max<false>(m, lds_m), a.sinv + row, threadIdx.x == 0, &satur);
+        }
+        void* hr = a.h ? (char*)a.h + off : nullptr;
+        const int64_t end = ((int64_t)cols + step - 1) / step * step;      // whole waves stay in the group max
+        for (int64_t cc = c0; cc < end; cc += step) {
+            const int c = (int)(cc < cols ? cc : cols);
+            float d[VE];
+            load_h<DT>(xr, rr, c, cols, d);
+            if (hr && c < cols) st_row<DT>(hr, c, cols, d);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) d[k] -= m0;
+            affine(c, d);
+            put_y<DT, FMT, TO>(a, row, c, d, scale, satur);
+        }
+        __syncthreads();                                    // the first reduction's LDS is used again
+    }
+}
+
+// ---------------------------------------------------------------------------
+// backward: n = (h - mean) rstd, dn = dy w,
+// dx = (dn - mean(dn) - n mean(dn n)) rstd + dh, and over the rows
+// dweight = sum dy n, dbias = sum dy.  Each workgroup takes every G-th row and
+// keeps its columns' sums in registers; the G partial rows are summed in order
+// by a second kernel, so the result does not depend on timing.
+// ---------------------------------------------------------------------------
+
+struct LnBwdArgs {
+    LayerNormBwd f;
+    float* pw;             // [gridDim.x][cols] partial dweight, or nullptr
+    float* pb;             // the same of dbias
+};
+
+// dy and h stay as loaded and are widened again after the reduction: that holds
+// half the registers, which the next row's loads take.
+template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB, 4) k_ln_bwd(LnBwdArgs g) {
+    const LayerNormBwd& a = g.f;
+    constexpr bool PF = TB <= 512;
+    constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
+    __shared__ float lds[2][32];
+    const int T = (int)blockDim.x, t = (int)threadIdx.x, cols = (int)a.cols;
+    const float fc = (float)cols;
+    auto place = [&](int v) { return Place<VE>((v * T + t) * VE, cols); };
+    Affine<DT, WF32> w[V];
+    float aw[V][VE], ab[V][VE];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        w[v].load(a.w, place(v).c);
+#pragma unroll
+        for (int k = 0; k < VE; ++k) aw[v][k] = ab[v][k] = 0.0f;
+    }
+    int flip = 0;
+    v4u dyr[V], hr[V], dyn[V], hn[V], dhr[V];
+    float rs = 0.0f, mu = 0.0f, rsn = 0.0f, mun = 0.0f;
+    auto load = [&](int64_t row) {
+        const int64_t off = row * a.cols * ES;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            dyn[v] = ld_at<DT, true>((const char*)a.dy + off, place(v).c);
+            hn[v] = ld_at<DT, true>((const char*)a.h + off, place(v).c);
+        }
+        rsn = a.rstd[row];
+        mun = a.mean[row];
+    };
+    // n and dy of one lane vector
+    auto widen = [&](int v, float* n, float* dy) {
+        asm volatile("" : "+v"(dyr[v]), "+v"(hr[v]));
+        widen16<DT>(dyr[v], dy);
+        widen16<DT>(hr[v], n);
+#pragma unroll
+        for (int k = 0; k < VE; ++k) n[k] = (n[k] - mu) * rs;
+    };
+    if ((int64_t)blockIdx.x < a.rows) load(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+        const int64_t off = row * a.cols * ES;
+        rs = rsn;
+        mu = mun;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            dyr[v] = dyn[v];
+            hr[v] = hn[v];
+        }
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float wv[VE], n[VE], dy[VE];
+            int dup = place(v).dup;
+            asm volatile("" : "+v"(dup));                   // no mask for every element held across the rows
+            widen(v, n, dy);
+            w[v].widen(wv);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+                aw[v][k] = __builtin_fmaf(dy[k], n[k], aw[v][k]);
+                ab[v][k] += dy[k];
+                const float dn = k >= dup ? dy[k] * wv[k] : 0.0f, nk = k >= dup ? n[k] : 0.0f;
+                s1 += dn;
+                s2 = __builtin_fmaf(dn, nk, s2);
+            }
+            __builtin_amdgcn_sched_barrier(0);              // one vector widened at a time
+        }
+        if (a.dh)
+#pragma unroll
+            for (int v = 0; v < V; ++v) dhr[v] = ld_at<DT, true>((const char*)a.dh + off, place(v).c);
+        if (PF && row + gridDim.x < a.rows) load(row + gridDim.x);   // in flight through the reduction and the stores
+        // dx over dh: elements that two lanes hold are loaded by both before either stores them
+        // (dy and h have been used, so their loads are done)
+        if (a.dx == a.dh)
+#pragma unroll
+            for (int v = 0; v < V; ++v) asm volatile("" : "+v"(dhr[v]));
+        row_sum2<false>(s1, s2, lds[flip]);
+        const float m1 = s1 / fc, m2 = s2 / fc;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float wv[VE], n[VE], dy[VE], o[VE];
+            widen(v, n, dy);
+            w[v].widen(wv);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) o[k] = __builtin_fmaf(-n[k], m2, dy[k] * wv[k] - m1) * rs;
+            if (a.dh) {
+                float d[VE];
+                widen16<DT>(dhr[v], d);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) o[k] += d[k];
+            }
+            if (place(v).in()) st_at<DT, true>((char*)a.dx + off, place(v).c, o);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (!PF && row + gridDim.x < a.rows) load(row + gridDim.x);
+    }
+    auto put = [&](float* part, const float (&s)[V][VE]) {
+        if (!part) return;
+        float* p = part + (int64_t)blockIdx.x * a.cols;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                if (k >= place(v).dup) p[place(v).c + k] = s[v][k];
+    };
+    put(g.pw, aw);
+    put(g.pb, ab);
+}
+
+// Rows too long for registers, or shorter than a vector: the row is read twice, and the sums over the
+// rows live in the workgroup's own partial rows (zeroed first; each word is
+// touched by one thread only).
+template <int DT, bool WF32> __global__ void __launch_bounds__(1024) k_ln_bwd_long(LnBwdArgs g) {
+    const LayerNormBwd& a = g.f;
+    constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
+    __shared__ float lds[2][32];
+    const int cols = (int)a.cols, step = (int)blockDim.x * VE, c0 = (int)threadIdx.x * VE;
+    const float fc = (float)cols;
+    float* pw = g.pw ? g.pw + (int64_t)blockIdx.x * a.cols : nullptr;
+    float* pb = g.pb ? g.pb + (int64_t)blockIdx.x * a.cols : nullptr;
+    for (float* p : {pw, pb})
+        if (p)
+            for (int64_t c = c0; c < cols; c += step)
+                for (int k = 0; k < VE; ++k)
+                    if (c + k < cols) p[c + k] = 0.0f;
+    int flip = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+        const int64_t off = row * a.cols * ES;
+        const float rs = a.rstd[row], mu = a.mean[row];
+        // dy, w and n of the columns from c on (dy and w zero past the row's end)
+        auto load = [&](int64_t c, float* dy, float* w, float* n) {
+            widen16<DT>(ld_row<DT>((const char*)a.dy + off, (int)c, cols), dy);
+            widen16<DT>(ld_row<DT>((const char*)a.h + off, (int)c, cols), n);
+            ld_weight<DT, WF32>(a.w, (int)c, cols, w);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) n[k] = (n[k] - mu) * rs;
+        };
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int64_t c = c0; c < cols; c += step) {
+            float dy[VE], w[VE], n[VE];
+            load(c, dy, w, n);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+                s1 += dy[k] * w[k];
+                s2 = __builtin_fmaf(dy[k] * w[k], n[k], s2);
+                if (pw && c + k < cols) pw[c + k] = __builtin_fmaf(dy[k], n[k], pw[c + k]);
+                if (pb && c + k < cols) pb[c + k] += dy[k];
+            }
+        }
+        row_sum2<false>(s1, s2, lds[flip]);
+        const float m1 = s1 / fc, m2 = s2 / fc;
+        for (int64_t c = c0; c < cols; c += step) {
+            float dy[VE], w[VE], n[VE], o[VE];
+            load(c, dy, w, n);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) o[k] = __builtin_fmaf(-n[k], m2, dy[k] * w[k] - m1) * rs;
+            if (a.dh) {
+                float d[VE];
+                widen16<DT>(ld_row<DT>((const char*)a.dh + off, (int)c, cols), d);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) o[k] += d[k];
+            }
+            st_row<DT>((char*)a.dx + off, (int)c, cols, o);
+        }
+    }
+}
+
+// out[c] = sum of part[0 .. parts)[c] in a fixed order: 32 columns a workgroup
+// at a time, 32 row lanes, then a tree over the row lanes in LDS.  y = 1: the
+// second output, from the second half of the partial rows.
+template <int DT> __global__ void __launch_bounds__(1024) k_column_sums(const float* part, int64_t parts, int64_t cols,
+                                                                        void* out0, void* out1) {
+    __shared__ float lds[32][33];
+    const int cl = (int)threadIdx.x & 31, rl = (int)threadIdx.x >> 5;
+    void* out = blockIdx.y ? out1 : out0;
+    if (!out) return;
+    if (blockIdx.y) part += parts * cols;
+    for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < cols; c0 += (int64_t)gridDim.x * 32) {
+        const int64_t c = c0 + cl;
+        float s = 0.0f;
+        if (c < cols)
+            for (int64_t p = rl; p < parts; p += 32) s += part[p * cols + c];
+        lds[rl][cl] = s;
+        __syncthreads();
+        for (int o = 16; o > 0; o >>= 1) {
+            if (rl < o) lds[rl][cl] += lds[rl + o][cl];
+            __syncthreads();
+        }
+        if (rl == 0 && c < cols) store1<DT>(out, c, lds[0][cl]);
+    }
+}
+
+template <int DT, bool WF, int FMT, int TO> void ln_rows(const LayerNorm& a, hipStream_t st) {
+    constexpr int VE = LaneVE<DT>::value;
+    const NormPlan p = norm_plan(a.rows, (a.cols + VE - 1) / VE);
+    const unsigned g = (unsigned)p.groups;
+    const int T = p.threads;
+    if (p.V == 0 || a.cols < VE) k_ln_long<DT, WF, FMT, TO><<<g, T, 0, st>>>(a);
+    else if (p.wave && p.V == 1) k_ln_rows<DT, WF, FMT, TO, true, 1, 256><<<g, T, 0, st>>>(a);
+    else if (p.wave) k_ln_rows<DT, WF, FMT, TO, true, 2, 256><<<g, T, 0, st>>>(a);
+    else if (p.V == 1) k_ln_rows<DT, WF, FMT, TO, false, 1, 256><<<g, T, 0, st>>>(a);
+    else if (p.V == 2 && T <= 512) k_ln_rows<DT, WF, FMT, TO, false, 2, 512><<<g, T, 0, st>>>(a);
+    else if (p.V == 2) k_ln_rows<DT, WF, FMT, TO, false, 2, 1024><<<g, T, 0, st>>>(a);
+    else k_ln_rows<DT, WF, FMT, TO, false, 4, 1024><<<g, T, 0, st>>>(a);
+}
+
+template <int DT, bool WF> void ln_to(const LayerNorm& a, hipStream_t st) {
+    if (a.to == kToPlain) return ln_rows<DT, WF, kE4M3, kToPlain>(a, st);
+    with_bool(a.fmt == kE5M2, [&](auto F) {
+        constexpr int FMT = decltype(F)::value ? kE5M2 : kE4M3;
+        if (a.to == kToGroup) ln_rows<DT, WF, FMT, kToGroup>(a, st);
+        else ln_rows<DT, WF, FMT, kToRow>(a, st);
+    });
+}
+
+template <int DT, bool WF> void ln_bwd(const LnBwdArgs& a, hipStream_t st) {
+    constexpr int VE = LaneVE<DT>::value;
+    const NormPlan p = norm_bwd_plan(a.f.rows, (a.f.cols + VE - 1) / VE);
+    const unsigned g = (unsigned)p.groups;
+    const int T = p.threads;
+    if (p.V == 0 || a.f.cols < VE) k_ln_bwd_long<DT, WF><<<g, T, 0, st>>>(a);
+    else if (p.V == 1) k_ln_bwd<DT, WF, 1, 256><<<g, T, 0, st>>>(a);
+    else if (T <= 512) k_ln_bwd<DT, WF, 2, 512><<<g, T, 0, st>>>(a);
+    else k_ln_bwd<DT, WF, 2, 1024><<<g, T, 0, st>>>(a);
+}
+
+// go(DT, WF32) over the types of the activations and of the weight
+template <typename F> void with_types(int dt, int wdt, F&& go) {
+    if (dt == kF32) go(KC<kF32>{}, std::false_type{});
+    else if (dt == kBF16) with_bool(wdt == kF32, [&](auto W) { go(KC<kBF16>{}, W); });
+    else with_bool(wdt == kF32, [&](auto W) { go(KC<kF16>{}, W); });
+}
+
+}  // namespace
+
+void launch_layernorm(const LayerNorm& a, hipStream_t st) {
+    with_types(a.dt, a.wdt, [&](auto DT, auto W) { ln_to<decltype(DT)::value, decltype(W)::value>(a, st); });
+}
+
+int64_t layernorm_bwd_parts(int64_t rows) { return norm_bwd_parts(rows); }
+
+void launch_column_sums(const float* part, int64_t parts, int64_t cols, void* out0, void* out1, int dt, hipStream_t st) {
+    const dim3 g(grid((cols + 31) / 32), out1 ? 2 : 1);     // 1024 threads each: a grid holds fewer than 2^32
+    if (dt == kF32) k_column_sums<kF32><<<g, 1024, 0, st>>>(part, parts, cols, out0, out1);
+    else if (dt == kBF16) k_column_sums<kBF16><<<g, 1024, 0, st>>>(part, parts, cols, out0, out1);
+    else k_column_sums<kF16><<<g, 1024, 0, st>>>(part, parts, cols, out0, out1);
+}
+
+void launch_layernorm_bwd(const LayerNormBwd& f, hipStream_t st) {
+    const int64_t parts = layernorm_bwd_parts(f.rows);
+    const LnBwdArgs a{f, f.dw ? f.ws : nullptr, f.db ? f.ws + parts * f.cols : nullptr};
+    with_types(f.dt, f.wdt, [&](auto DT, auto W) { ln_bwd<decltype(DT)::value, decltype(W)::value>(a, st); });
+    if (f.dw || f.db) launch_column_sums(f.ws, parts, f.cols, f.dw, f.db, f.wdt, st);
+}
+
+}  // namespace fp8q

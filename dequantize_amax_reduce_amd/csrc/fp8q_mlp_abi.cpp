@@ -1,0 +1,118 @@
+// fp8q_mlp_abi.cpp -- the C ABI declared in include/fp8q_mlp.h.
+//
+// As in fp8q_abi.cpp, every entry point validates its arguments on the host
+// first (no HIP call, no side effect) and only then enqueues kernels.
+#include "fp8q_mlp.h"
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "fp8q_ffn_check.h"
+#include "fp8q_mlp_launch.h"
+
+namespace {
+
+// n zeros of an element type
+void zeros(void* p, int64_t n, int dt, hipStream_t st) {
+    if (!p || n == 0) return;
+    if (dt == FP8Q_F32) fp8q::launch_fill_f32((float*)p, n, 0.0f, st);
+    else fp8q::launch_zero16(p, n, st);
+}
+
+fp8q_status_t layernorm(const fp8q::LayerNorm& a, void* stream) {
+    const bool plain = a.to == fp8q::kToPlain, group = a.to == fp8q::kToGroup;
+    if (!valid_dtype(a.dt) || (!plain && !valid_fmt(a.fmt)) || (a.wdt != a.dt && a.wdt != FP8Q_F32)) return FP8Q_EDTYPE;
+    if (a.rows < 0 || a.cols < 0) return FP8Q_EINVAL;
+    if (group && a.cols % 128 != 0) return FP8Q_ESHAPE;
+    if (a.rows > kMaxNormRows || a.cols > kMaxNormCols) return FP8Q_EINVAL;
+    const int64_t n = a.rows * a.cols, es = esize(a.dt), we = esize(a.wdt);
+    const int64_t sc = plain ? 0 : group ? a.rows * (a.cols / 128) : a.rows;
+    if (a.rows == 0) return FP8Q_OK;
+    if ((n > 0 && (!a.x || !a.w || !a.y)) || (sc > 0 && !a.sinv)) return FP8Q_EINVAL;
+    if (!aligned(a.x, es) || !aligned(a.res, es) || !aligned(a.h, es) || !aligned(a.w, we) || !aligned(a.b, we) ||
+        (plain && !aligned(a.y, es)) || !aligned(a.sinv, 4) || !aligned(a.mean, 4) || !aligned(a.rstd, 4))
+        return FP8Q_EALIGN;
+    const Buf out[] = {{a.y, plain ? n * es : n}, {a.h, n * es}, {a.sinv, 4 * sc}, {a.mean, a.mean ? 4 * a.rows : 0},
+                       {a.rstd, a.rstd ? 4 * a.rows : 0}, {a.w, a.cols * we}, {a.b, a.cols * we}};
+    if (bad_overlap(out, 7, 5)) return FP8Q_EINVAL;
+    // h, and y in x's type, may be x or the residual itself; otherwise the outputs meet nothing
+    for (const void* in : {a.x, a.res})
+        for (int i = 0; i < 5; ++i)
+            if (overlap(out[i], {in, n * es}) && !(out[i].p == in && (i == 1 || (i == 0 && plain)))) return FP8Q_EINVAL;
+    if (a.cols == 0) {
+        if (a.to != fp8q::kToRow) return FP8Q_OK;
+        fp8q::launch_fill_f32(a.sinv, a.rows, 1.0f, S(stream));
+        return launched();
+    }
+    fp8q::launch_layernorm(a, S(stream));
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+// ---------------------------------------------------------------------------
+// layer norm
+// ---------------------------------------------------------------------------
+
+fp8q_status_t fp8q_layernorm(const void* x, fp8q_dtype_t xdtype, const void* residual, const void* weight,
+                             const void* bias, fp8q_dtype_t wdtype, int64_t rows, int64_t cols, float eps, void* y,
+                             void* h, float* mean, float* rstd, void* stream) {
+    return layernorm({x, xdtype, residual, weight, bias, wdtype, rows, cols, eps, fp8q::kToPlain, 0, y, nullptr, h, mean,
+                      rstd}, stream);
+}
+
+fp8q_status_t fp8q_layernorm_cast_group128(const void* x, fp8q_dtype_t xdtype, const void* residual,
+                                           const void* weight, const void* bias, fp8q_dtype_t wdtype, int64_t rows,
+                                           int64_t cols, float eps, fp8q_fmt_t fmt, uint8_t* q, float* scale_inv,
+                                           void* h, float* mean, float* rstd, void* stream) {
+    return layernorm({x, xdtype, residual, weight, bias, wdtype, rows, cols, eps, fp8q::kToGroup, fmt, q, scale_inv, h,
+                      mean, rstd}, stream);
+}
+
+fp8q_status_t fp8q_layernorm_cast_per_channel(const void* x, fp8q_dtype_t xdtype, const void* residual,
+                                              const void* weight, const void* bias, fp8q_dtype_t wdtype, int64_t rows,
+                                              int64_t cols, float eps, fp8q_fmt_t fmt, uint8_t* q, float* scale_inv,
+                                              void* h, float* mean, float* rstd, void* stream) {
+    return layernorm({x, xdtype, residual, weight, bias, wdtype, rows, cols, eps, fp8q::kToRow, fmt, q, scale_inv, h,
+                      mean, rstd}, stream);
+}
+
+size_t fp8q_layernorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0 || rows > kMaxNormRows || cols > kMaxNormCols) return 0;
+    return (size_t)(fp8q::layernorm_bwd_parts(rows) * cols * 8);
+}
+
+fp8q_status_t fp8q_layernorm_backward(const void* dy, const void* h, fp8q_dtype_t dtype, const void* weight,
+                                      fp8q_dtype_t wdtype, const float* mean, const float* rstd, const void* dh,
+                                      int64_t rows, int64_t cols, void* dx, void* dweight, void* dbias,
+                                      void* workspace, void* stream) {
+    if (!valid_dtype(dtype) || (wdtype != dtype && wdtype != FP8Q_F32)) return FP8Q_EDTYPE;
+    if (rows < 0 || cols < 0 || rows > kMaxNormRows || cols > kMaxNormCols) return FP8Q_EINVAL;
+    const int64_t n = rows * cols, es = esize(dtype), we = esize(wdtype);
+    if (cols == 0) return FP8Q_OK;
+    if (n > 0 && (!dy || !h || !weight || !mean || !rstd || !dx)) return FP8Q_EINVAL;
+    if (!aligned(dy, es) || !aligned(h, es) || !aligned(dh, es) || !aligned(dx, es) || !aligned(weight, we) ||
+        !aligned(dweight, we) || !aligned(dbias, we) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return FP8Q_EALIGN;
+    const int64_t wsb = dweight || dbias ? (int64_t)fp8q_layernorm_backward_workspace_bytes(rows, cols) : 0;
+    const fp8q_status_t st = check_ws(workspace, wsb);
+    if (st != FP8Q_OK) return st;
+    // dx may be dy or dh, but then that tensor still may not meet another output
+    const Buf b[] = {{dx, n * es}, {dweight, cols * we}, {dbias, cols * we}, {workspace, wsb},
+                     {dy, dx == dy ? 0 : n * es}, {dh, dx == dh ? 0 : n * es}, {h, n * es}, {weight, cols * we},
+                     {mean, 4 * rows}, {rstd, 4 * rows}};
+    if (bad_overlap(b, 10, 4)) return FP8Q_EINVAL;
+    if (rows == 0) {
+        zeros(dweight, cols, wdtype, S(stream));
+        zeros(dbias, cols, wdtype, S(stream));
+        return dweight || dbias ? launched() : FP8Q_OK;
+    }
+    fp8q::launch_layernorm_bwd({dy, h, dtype, weight, wdtype, mean, rstd, dh, rows, cols, dx, dweight, dbias,
+                                (float*)workspace}, S(stream));
+    return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,80 @@
+/*
+ * fp8q_mlp.h -- C ABI of the operators of blocks with layer norm and biased
+ * projections: what fp8q_ffn.h offers for blocks with RMS norm and gated
+ * projections, for AMD Instinct MI355X (gfx950).
+ *
+ * The conventions of fp8q.h and fp8q_ffn.h hold (device pointers, dense
+ * row-major tensors, fp8 activations and weights and their scales as there,
+ * asynchronous on `stream`, arguments validated on the host before any HIP
+ * call, no allocation, no state kept, the same limits, workspaces and
+ * numerics; a row's result does not depend on the other rows), and the calling
+ * thread's current device is the one that holds the tensors.
+ */
+#ifndef FP8Q_MLP_H
+#define FP8Q_MLP_H
+
+#include "fp8q_ffn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Residual addition, layer norm, and its result in x's type or cast to fp8:
+ *   h = x (+ residual, in binary32);  mean[r] = mean_c h[r, c];
+ *   rstd[r] = 1 / sqrt(mean_c (h[r, c] - mean[r])^2 + eps);
+ *   y = ((h - mean[r]) * rstd[r]) * weight[c] (+ bias[c]), in binary32, from the
+ *   sum before its rounding to xdtype;
+ *   fp8q_layernorm:                  y rounded once to xdtype;
+ *   fp8q_layernorm_cast_group128:    q, scale_inv = the cast of y per 128
+ *     columns, by fp8q_cast_per_group128's rule (scale_inv [rows, cols/128];
+ *     cols % 128 != 0 -> FP8Q_ESHAPE);
+ *   fp8q_layernorm_cast_per_channel: per row, by fp8q_cast_per_channel's rule
+ *     (scale_inv [rows]).
+ * x, residual, h, y: [rows, cols] of xdtype.  residual may be NULL (h = x).
+ * h may be NULL (not written) and may be x or residual itself (in place); y may
+ * be x or residual itself where it is not h.
+ * weight, bias: [cols] of wdtype, which is xdtype or FP8Q_F32 (else
+ * FP8Q_EDTYPE); bias may be NULL.  mean, rstd: [rows] floats, or NULL.
+ * The mean is taken twice, the second time of the differences from the first,
+ * so that rows far from zero lose nothing but h's own rounding.  Sums are
+ * binary32: a row whose sum passes 3.4e38 gets NaN, and one whose differences
+ * pass 1.8e19 gets rstd = 0, as an infinite variance gives it.
+ * rows == 0 is a no-op; cols == 0 is a no-op except that the per-channel form
+ * writes scale_inv[r] = 1 (mean and rstd are not written).
+ */
+fp8q_status_t fp8q_layernorm(const void* x, fp8q_dtype_t xdtype, const void* residual, const void* weight,
+                             const void* bias, fp8q_dtype_t wdtype, int64_t rows, int64_t cols, float eps, void* y,
+                             void* h, float* mean, float* rstd, void* stream);
+fp8q_status_t fp8q_layernorm_cast_group128(const void* x, fp8q_dtype_t xdtype, const void* residual,
+                                           const void* weight, const void* bias, fp8q_dtype_t wdtype, int64_t rows,
+                                           int64_t cols, float eps, fp8q_fmt_t fmt, uint8_t* q, float* scale_inv,
+                                           void* h, float* mean, float* rstd, void* stream);
+fp8q_status_t fp8q_layernorm_cast_per_channel(const void* x, fp8q_dtype_t xdtype, const void* residual,
+                                              const void* weight, const void* bias, fp8q_dtype_t wdtype, int64_t rows,
+                                              int64_t cols, float eps, fp8q_fmt_t fmt, uint8_t* q, float* scale_inv,
+                                              void* h, float* mean, float* rstd, void* stream);
+
+/*
+ * Backward of the layer norm (the cast passes gradients through).  dy [rows,
+ * cols] is the gradient of y; h, mean and rstd are the forward's; dh (or NULL)
+ * is the gradient that reaches h along the residual path:
+ *   n = (h - mean) * rstd;  dn = dy * weight;
+ *   dx = (dn - mean_c(dn) - n * mean_c(dn * n)) * rstd + dh;
+ *   dweight[c] = sum_r dy * n;  dbias[c] = sum_r dy.
+ * dx (the gradient of x and of the residual alike) may be dy or dh itself.
+ * dy, h, dh, dx: dtype; weight, dweight, dbias: wdtype (dtype or FP8Q_F32).
+ * dweight and dbias may be NULL each.  rows == 0 writes zeros to them.
+ * workspace: fp8q_layernorm_backward_workspace_bytes(rows, cols) bytes, needed
+ * only with dweight or dbias.
+ */
+size_t fp8q_layernorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+fp8q_status_t fp8q_layernorm_backward(const void* dy, const void* h, fp8q_dtype_t dtype, const void* weight,
+                                      fp8q_dtype_t wdtype, const float* mean, const float* rstd, const void* dh,
+                                      int64_t rows, int64_t cols, void* dx, void* dweight, void* dbias,
+                                      void* workspace, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* FP8Q_MLP_H */

@@ -1,0 +1,43 @@
+// Host-only stand-ins for the launchers of layer norm and biased projections
+// (fp8q_mlp_launch.h), for the sanitizer build of fp8q_mlp_abi.cpp.  Each checks
+// the preconditions that the ABI layer promises and counts its calls.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+#include <stdlib.h>
+
+#include "fp8q_mlp_launch.h"
+
+namespace {
+long g_calls = 0;
+void need(bool ok) {
+    if (!ok) abort();
+}
+bool al(const void* p, uintptr_t a) { return (uintptr_t)p % a == 0; }
+}  // namespace
+
+extern "C" long fp8q_mlp_stub_count(void) { return g_calls; }
+extern "C" void fp8q_mlp_stub_reset(void) { g_calls = 0; }
+
+hipError_t hipGetLastError(void) { return hipSuccess; }
+
+namespace fp8q {
+
+void launch_fill_f32(float* p, int64_t n, float, hipStream_t) { need(p && n > 0); ++g_calls; }
+void launch_zero16(void* p, int64_t n, hipStream_t) { need(p && n > 0); ++g_calls; }
+
+void launch_layernorm(const LayerNorm& a, hipStream_t) {
+    need(a.x && a.w && a.y && a.rows > 0 && a.cols > 0);
+    need(a.to == kToPlain || (a.sinv && (a.to == kToRow || a.cols % 128 == 0)));
+    ++g_calls;
+}
+
+int64_t layernorm_bwd_parts(int64_t rows) { return rows < 512 ? rows : 512; }
+
+void launch_layernorm_bwd(const LayerNormBwd& a, hipStream_t) {
+    need(a.dy && a.h && a.w && a.mean && a.rstd && a.dx && a.rows > 0 && a.cols > 0);
+    need((!a.dw && !a.db) || (a.ws && al(a.ws, 256)));
+    ++g_calls;
+}
+
+}  // namespace fp8q
