@@ -4,6 +4,8 @@ activation and a residual in their epilogue, on fp8 operands.
 Re-exported by the package; laid out as _ffn.py is.
 
     q, s, h, mean, rstd = layernorm_cast(x, weight, bias, residual)     # norm -> fp8 per 128-group
+    p, ps, z = linear_act_fp8_cast(q, s, w1, w1s, b1, "gelu", keep=torch.bfloat16)
+    y, _ = linear_act_fp8(p, ps, w2, w2s, b2, residual=h)               # the new residual stream
     dx, dweight, dbias = layernorm_backward(dn, h, weight, mean, rstd, dh)
 """
 from __future__ import annotations
@@ -15,9 +17,12 @@ import re
 import torch
 
 from . import _ffn
-from ._ffn import _AUTO, _f32, _flat, _hp_dtype, _opt, _ptr, _same, _stream, _ws
+from ._ffn import _AUTO, _CODES, _f32, _flat, _formats, _hp_dtype, _opt, _ptr, _same, _stream, _w_codes, _ws, _x_codes
 
 MLP_HEADER_PATH = os.path.join(os.path.dirname(_ffn.FFN_HEADER_PATH), "fp8q_mlp.h")
+
+IDENTITY, RELU = 3, 4
+_ACT = {**_ffn._ACT, None: IDENTITY, "identity": IDENTITY, "relu": RELU, IDENTITY: IDENTITY, RELU: RELU}
 
 _P, _I64, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 MLP_SIGNATURES = {
@@ -26,6 +31,9 @@ MLP_SIGNATURES = {
     "fp8q_layernorm_cast_per_channel": (_I, [_P, _I, _P, _P, _P, _I, _I64, _I64, _F, _I, _P, _P, _P, _P, _P, _P]),
     "fp8q_layernorm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
     "fp8q_layernorm_backward": (_I, [_P, _P, _I, _P, _I, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P]),
+    "fp8q_linear_act_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I]),
+    "fp8q_linear_act": (_I, _CODES + _CODES + [_I64, _I64, _I64, _P, _I, _I, _P, _P, _I, _P, _I, _P, _P]),
+    "fp8q_linear_act_cast": (_I, _CODES + _CODES + [_I64, _I64, _I64, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P]),
 }
 MLP_FUNCTIONS = tuple(MLP_SIGNATURES)
 
@@ -149,6 +157,61 @@ def fp8q_layernorm_backward(dy, h, weight, mean, rstd, dx, dweight=None, dbias=N
           _opt(ws, "workspace"), _stream(h, stream))
 
 
+def _activation(name) -> int:
+    if name not in _ACT:
+        raise TypeError(f"unknown activation {name!r} (use None, 'relu', 'silu', 'gelu' or 'gelu_tanh')")
+    return _ACT[name]
+
+
+def _typed(t, shape, name):
+    """pointer and type of an optional [M, N] tensor of any element type"""
+    if t is None:
+        return 0, 0
+    _same(t, shape, t.dtype, name)
+    return _ptr(t, name), _hp_dtype(t, name)
+
+
+def _projection(name, x, xs, w, ws, bias, x_fmt, w_fmt):
+    """the arguments that the entry points have in common, M, N, K"""
+    xf, wf = _formats(x, x_fmt, w_fmt, w)
+    xa, M, K = _x_codes(x, xs, xf)
+    wp, wsp, N = _w_codes(w, ws, K, "w")
+    if bias is not None and bias.numel() != N:
+        raise ValueError(f"{name}: bias must have w's rows")
+    b = (0, 0) if bias is None else (_ptr(bias, "bias"), _hp_dtype(bias, "bias"))
+    return (*xa, wp, wf, wsp, M, N, K, *b), M, N, K
+
+
+def fp8q_linear_act_workspace_bytes(M: int, N: int, K: int, cast: bool) -> int:
+    return lib.fp8q_linear_act_workspace_bytes(M, N, K, int(bool(cast)))
+
+
+def fp8q_linear_act(x, x_scale_inv, w, w_scale_inv, bias, y, residual=None, z=None, activation=None, workspace=None,
+                    stream=None, x_fmt=None, w_fmt=None) -> None:
+    name = "fp8q_linear_act"
+    act = _activation(activation)
+    args, M, N, K = _projection(name, x, x_scale_inv, w, w_scale_inv, bias, x_fmt, w_fmt)
+    _same(residual, (M, N), y.dtype, "residual")
+    scratch = _ws(workspace, lib.fp8q_linear_act_workspace_bytes(M, N, K, 0), x, name)
+    _call(name, x, (x_scale_inv, w, w_scale_inv, bias, residual, y, z, scratch), *args, act, _opt(residual, "residual"),
+          *_typed(y, (M, N), "y"), *_typed(z, (M, N), "z"), _opt(scratch, "workspace"), _stream(x, stream))
+
+
+def fp8q_linear_act_cast(x, x_scale_inv, w, w_scale_inv, bias, q, scale_inv, z=None, activation=None, fmt=None,
+                         workspace=None, stream=None, x_fmt=None, w_fmt=None) -> None:
+    name = "fp8q_linear_act_cast"
+    act = _activation(activation)
+    args, M, N, K = _projection(name, x, x_scale_inv, w, w_scale_inv, bias, x_fmt, w_fmt)
+    f = _fp8(q, fmt, "q")
+    if q.numel() != M * N:
+        raise ValueError(f"{name}: q must have M x N elements")
+    if N % 128 == 0:
+        _f32(scale_inv, M * (N // 128), "scale_inv")
+    scratch = _ws(workspace, lib.fp8q_linear_act_workspace_bytes(M, N, K, 1), x, name)
+    _call(name, x, (x_scale_inv, w, w_scale_inv, bias, q, scale_inv, z, scratch), *args, act, f, _ptr(q, "q"),
+          _ptr(scale_inv, "scale_inv"), *_typed(z, (M, N), "z"), _opt(scratch, "workspace"), _stream(x, stream))
+
+
 # ---------------------------------------------------------------------------
 # helpers that allocate outputs and workspaces
 # ---------------------------------------------------------------------------
@@ -203,6 +266,41 @@ def layernorm_backward(dy, h, weight, mean, rstd, dh=None, with_bias=True, out=N
     return dx, dw, db if with_bias else None
 
 
+def linear_act_fp8(x, x_scale_inv, w, w_scale_inv, bias=None, activation=None, residual=None, ret_type=torch.bfloat16,
+                   keep=None, out=None, x_fmt=None, w_fmt=None):
+    """(y, z): z = X W^T + bias for codes x [..., K] with scales per 128-group
+    and w [N, K] with scales per 128x128 block; y = act(z) + residual in
+    ret_type (the residual's dtype where there is one).  activation: None,
+    'relu', 'silu', 'gelu' or 'gelu_tanh'.  z is returned in `keep`'s dtype for
+    the backward pass, or is None.  `out`: y and z (or None), caller-allocated;
+    y may be the residual itself."""
+    if out is not None:
+        y, z = out
+    else:
+        shape = (*x.shape[:-1], w.shape[0])
+        y = torch.empty(shape, dtype=ret_type if residual is None else residual.dtype, device=x.device)
+        z = None if keep is None else torch.empty(shape, dtype=keep, device=x.device)
+    fp8q_linear_act(x, x_scale_inv, w, w_scale_inv, bias, y, residual, z, activation, _AUTO, x_fmt=x_fmt, w_fmt=w_fmt)
+    return y, z
+
+
+def linear_act_fp8_cast(x, x_scale_inv, w, w_scale_inv, bias=None, activation=None, fp8_format="e4m3fn", keep=None,
+                        out=None, x_fmt=None, w_fmt=None):
+    """(q, scale_inv, z): linear_act_fp8's act(z) cast to fp8 per 128-group (N %
+    128 == 0) without a 16-bit copy in between, and z as there."""
+    N = w.shape[0]
+    if out is not None:
+        q, s, z = out
+    else:
+        shape = (*x.shape[:-1], N)
+        q = torch.empty(shape, dtype=_FP8_DTYPE[_fmt(fp8_format)], device=x.device)
+        s = torch.empty((_flat(x, "x")[0], N // 128), dtype=torch.float32, device=x.device)
+        z = None if keep is None else torch.empty(shape, dtype=keep, device=x.device)
+    fp8q_linear_act_cast(x, x_scale_inv, w, w_scale_inv, bias, q, s, z, activation, fp8_format, _AUTO, x_fmt=x_fmt,
+                         w_fmt=w_fmt)
+    return q, s, z
+
+
 MLP_NAMES = [n for n in dir() if n.startswith("fp8q_")] + [
-    "MLP_HEADER_PATH", "MLP_FUNCTIONS", "mlp_header_functions", "load_mlp",
-    "layernorm", "layernorm_cast", "layernorm_backward"]
+    "IDENTITY", "RELU", "MLP_HEADER_PATH", "MLP_FUNCTIONS", "mlp_header_functions", "load_mlp",
+    "layernorm", "layernorm_cast", "layernorm_backward", "linear_act_fp8", "linear_act_fp8_cast"]

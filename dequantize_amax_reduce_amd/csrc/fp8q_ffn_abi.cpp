@@ -139,10 +139,6 @@ fp8q_status_t fp8q_rmsnorm_backward(const void* dy, const void* h, fp8q_dtype_t 
 // projections
 // ---------------------------------------------------------------------------
 
-static bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t max_m) {
-    return check_sizes(M, N, K, max_m) == FP8Q_OK && M > 0 && N > 0;
-}
-
 size_t fp8q_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (!sizes_ok(M, N, K, kMaxFwdRows)) return 0;
     return (size_t)fp8q::mm_fwd_workspace(M, N, K, false, false);

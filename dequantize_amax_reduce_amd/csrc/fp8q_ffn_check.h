@@ -16,6 +16,7 @@ constexpr int64_t kMaxTiles = (int64_t(1) << 23) - 1;   // workgroups of 512 thr
 inline bool valid_dtype(int dt) { return dt == FP8Q_F32 || dt == FP8Q_BF16 || dt == FP8Q_F16; }
 inline bool valid_fmt(int f) { return f == FP8Q_E4M3FN || f == FP8Q_E5M2; }
 inline bool valid_act(int a) { return a == FP8Q_SILU || a == FP8Q_GELU || a == FP8Q_GELU_TANH; }
+inline bool valid_unary(int a) { return valid_act(a) || a == FP8Q_IDENTITY || a == FP8Q_RELU; }
 inline bool half_dtype(int dt) { return dt == FP8Q_BF16 || dt == FP8Q_F16; }
 inline int64_t esize(int dt) { return dt == FP8Q_F32 ? 4 : 2; }
 inline bool aligned(const void* p, int64_t a) { return ((uintptr_t)p % (uintptr_t)a) == 0; }
@@ -73,5 +74,9 @@ inline fp8q_status_t check_ws(const void* ws, int64_t bytes) {
 constexpr int64_t kMaxFwdRows = int64_t(1) << 31;
 // no tiling of an [M, N] product has more tiles than this
 inline bool grid_ok(int64_t M, int64_t N) { return (M / 64 + 1) * (N / 128 + 1) <= kMaxTiles; }
+
+inline bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t max_m) {
+    return check_sizes(M, N, K, max_m) == FP8Q_OK && M > 0 && N > 0;
+}
 
 }  // namespace

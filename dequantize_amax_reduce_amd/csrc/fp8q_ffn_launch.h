@@ -9,7 +9,7 @@
 
 namespace fp8q {
 
-enum { kSilu = 0, kGelu = 1, kGeluTanh = 2 };
+enum { kSilu = 0, kGelu = 1, kGeluTanh = 2, kIdentity = 3, kRelu = 4 };
 
 // All launchers enqueue on `st` and never synchronise.  Preconditions
 // (checked by the ABI layer): sizes > 0 unless stated, pointers valid and

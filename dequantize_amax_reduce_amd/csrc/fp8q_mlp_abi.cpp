@@ -49,6 +49,40 @@ fp8q_status_t layernorm(const fp8q::LayerNorm& a, void* stream) {
     return launched();
 }
 
+fp8q_status_t linear_act(fp8q::MmAct& e, int64_t M, int64_t N, int64_t K, void* stream) {
+    fp8q::MmFwd& f = e.f;
+    if (!valid_fmt(f.xfmt) || !valid_fmt(f.wfmt) || !valid_unary(f.act) || (e.bias && !valid_dtype(e.bdt)) ||
+        (f.z && !valid_dtype(f.zdt)))
+        return FP8Q_EDTYPE;
+    fp8q_status_t st = check_sizes(M, N, K, kMaxFwdRows);
+    if (st != FP8Q_OK) return st;
+    if (!grid_ok(M, N)) return FP8Q_EINVAL;
+    if (M == 0 || N == 0) return FP8Q_OK;
+    if (f.q ? !f.sinv : !f.y) return FP8Q_EINVAL;
+    for (const Codes& c : {Codes{f.x, f.xs, M, M}, Codes{f.w0, f.ws0, N, blocks(N)}}) {
+        st = check_codes(c, K);
+        if (st != FP8Q_OK) return st;
+    }
+    const int64_t n = M * N, ye = esize(f.ydt);
+    if (!aligned(f.y, ye) || !aligned(e.res, ye) || (f.z && !aligned(f.z, esize(f.zdt))) || !aligned(f.sinv, 4) ||
+        (e.bias && !aligned(e.bias, esize(e.bdt))))
+        return FP8Q_EALIGN;
+    const int64_t wsb = fp8q::mm_fwd_workspace(M, N, K, false, f.q != nullptr);
+    st = check_ws(f.ws, wsb);
+    if (st != FP8Q_OK) return st;
+    const int64_t KB = K / 128;
+    // y may be the residual
+    const Buf b[] = {{f.y, n * ye}, {f.z, f.z ? n * esize(f.zdt) : 0}, {f.q, n}, {f.sinv, 4 * M * (N / 128)}, {f.ws, wsb},
+                     {e.res, e.res == f.y ? 0 : n * ye}, {e.bias, e.bias ? N * esize(e.bdt) : 0}, {f.x, M * K},
+                     {f.xs, 4 * M * KB}, {f.w0, N * K}, {f.ws0, 4 * blocks(N) * KB}};
+    if (bad_overlap(b, 11, 5)) return FP8Q_EINVAL;
+    f.M = M;
+    f.N = (int)N;
+    f.K = (int)K;
+    fp8q::launch_mm_act(e, S(stream));
+    return launched();
+}
+
 }  // namespace
 
 extern "C" {
@@ -113,6 +147,44 @@ fp8q_status_t fp8q_layernorm_backward(const void* dy, const void* h, fp8q_dtype_
     fp8q::launch_layernorm_bwd({dy, h, dtype, weight, wdtype, mean, rstd, dh, rows, cols, dx, dweight, dbias,
                                 (float*)workspace}, S(stream));
     return launched();
+}
+
+// ---------------------------------------------------------------------------
+// projection with an epilogue
+// ---------------------------------------------------------------------------
+
+size_t fp8q_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K, int cast) {
+    if (!sizes_ok(M, N, K, kMaxFwdRows)) return 0;
+    return (size_t)fp8q::mm_fwd_workspace(M, N, K, false, cast != 0);
+}
+
+fp8q_status_t fp8q_linear_act(const uint8_t* x, fp8q_fmt_t xfmt, const float* x_scale_inv, const uint8_t* w,
+                              fp8q_fmt_t wfmt, const float* w_scale_inv, int64_t M, int64_t N, int64_t K,
+                              const void* bias, fp8q_dtype_t bdtype, fp8q_act_t act, const void* residual, void* y,
+                              fp8q_dtype_t ydtype, void* z, fp8q_dtype_t zdtype, void* workspace, void* stream) {
+    if (!valid_dtype(ydtype)) return FP8Q_EDTYPE;
+    fp8q::MmAct e{};
+    fp8q::MmFwd& f = e.f;
+    f.x = x; f.xs = x_scale_inv; f.w0 = w; f.ws0 = w_scale_inv; f.xfmt = xfmt; f.wfmt = wfmt; f.act = act;
+    f.y = y; f.ydt = ydtype; f.z = z; f.zdt = zdtype; f.ws = workspace;
+    e.bias = bias; e.bdt = bdtype; e.res = residual;
+    return linear_act(e, M, N, K, stream);
+}
+
+fp8q_status_t fp8q_linear_act_cast(const uint8_t* x, fp8q_fmt_t xfmt, const float* x_scale_inv, const uint8_t* w,
+                                   fp8q_fmt_t wfmt, const float* w_scale_inv, int64_t M, int64_t N, int64_t K,
+                                   const void* bias, fp8q_dtype_t bdtype, fp8q_act_t act, fp8q_fmt_t fmt, uint8_t* q,
+                                   float* scale_inv, void* z, fp8q_dtype_t zdtype, void* workspace, void* stream) {
+    if (!valid_fmt(fmt)) return FP8Q_EDTYPE;
+    if (M < 0 || N < 0) return FP8Q_EINVAL;
+    if (N % 128 != 0) return FP8Q_ESHAPE;
+    if (M > 0 && N > 0 && !q) return FP8Q_EINVAL;
+    fp8q::MmAct e{};
+    fp8q::MmFwd& f = e.f;
+    f.x = x; f.xs = x_scale_inv; f.w0 = w; f.ws0 = w_scale_inv; f.xfmt = xfmt; f.wfmt = wfmt; f.act = act;
+    f.q = q; f.qfmt = fmt; f.sinv = scale_inv; f.z = z; f.zdt = zdtype; f.ws = workspace;
+    e.bias = bias; e.bdt = bdtype;
+    return linear_act(e, M, N, K, stream);
 }
 
 }  // extern "C"

@@ -50,4 +50,16 @@ void launch_layernorm_bwd(const LayerNormBwd& a, hipStream_t st);
 // out1 likewise of the `parts` rows after those; either may be null
 void launch_column_sums(const float* part, int64_t parts, int64_t cols, void* out0, void* out1, int dt, hipStream_t st);
 
+// One projection with an epilogue: z = X W^T + bias (kept in f.z [M, N] where
+// asked), then act(z) + res to f.y, or the group cast of act(z) to f.q.  f.w1,
+// f.ws1 and f.gated are unused; the workspace is mm_fwd_workspace's of a
+// projection.
+struct MmAct {
+    MmFwd f;
+    const void* bias;    // [N] of bdt, or nullptr
+    int bdt;
+    const void* res;     // [M, N] of f.ydt, or nullptr; may be f.y
+};
+void launch_mm_act(const MmAct& a, hipStream_t st);
+
 }  // namespace fp8q

@@ -59,6 +59,15 @@ __device__ __forceinline__ void lds_dma4_at(uint32_t lds, const void* addr) {   
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(addr)
                  : "memory", "m0");
 }
+// one element of a runtime type a lane, 16-bit ones zero-extended to the word
+__device__ __forceinline__ void lds_dma_elem(uint32_t lds, const void* base, int dt, int64_t e) {
+    if (dt == kF32) {
+        lds_dma4_at(lds, (const float*)base + e);
+        return;
+    }
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" ::"s"(lds), "v"((const uint16_t*)base + e)
+                 : "memory", "m0");
+}
 #pragma clang diagnostic pop
 // all but this wave's N newest LDS loads have landed, and its LDS reads have returned
 template <int N = 0> __device__ __forceinline__ void dma_wait() {
@@ -201,7 +210,11 @@ struct Act {
 template <int ACT, bool SLOPE, bool QUICK = false> __device__ __forceinline__ Act act_at(float g) {
     Act r;
     r.d = 0.0f;
-    if constexpr (ACT == kGelu) {
+    if constexpr (ACT == kIdentity) {
+        return Act{g, 1.0f, 1.0f};
+    } else if constexpr (ACT == kRelu) {
+        return Act{g < 0.0f ? 0.0f : g, g <= 0.0f ? 0.0f : 1.0f, 1.0f};   // a NaN passes
+    } else if constexpr (ACT == kGelu) {
         if (g < -10.0f) {
             // Phi(g) = phi(g) / -g (1 - 1/g^2 + 3/g^4 - 15/g^6 + 105/g^8 - ...), the next term under 1e-7
             const float x = g * g, q = 1.0f / x, h = 0.39894228040143268f;
@@ -247,11 +260,24 @@ template <int ACT> __device__ __forceinline__ float gated_value(float g, float u
     return r.a * u * r.e;
 }
 
-// f(integral_constant) over a runtime activation
+// act(g)
+template <int ACT> __device__ __forceinline__ float unary_value(float g) {
+    const Act r = act_at<ACT, false>(g);
+    return r.a * r.e;
+}
+
+// f(integral_constant) over a runtime activation; with_unary: those of a
+// projection without a gate
 template <typename F> __device__ __forceinline__ void with_act(int act, F&& f) {
     if (act == kSilu) f(std::integral_constant<int, kSilu>{});
     else if (act == kGelu) f(std::integral_constant<int, kGelu>{});
     else f(std::integral_constant<int, kGeluTanh>{});
+}
+
+template <typename F> __device__ __forceinline__ void with_unary(int act, F&& f) {
+    if (act == kIdentity) f(std::integral_constant<int, kIdentity>{});
+    else if (act == kRelu) f(std::integral_constant<int, kRelu>{});
+    else with_act(act, f);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,46 @@
+// fp8q_mm_act.hip -- a projection on fp8 operands with bias, activation and
+// residual in its epilogue, or with the group cast of the activation.
+//
+//   z = X W^T + b;  y = act(z) + r, or q, scale_inv = cast(act(z))
+//
+// The kernels are in fp8q_mm_fwd.h: the epilogue runs where the tile's sums are
+// in registers (k_mm), where the splits of a contraction are joined
+// (k_mm_join), or where the waves' sums of few rows meet (k_mm_rows).
+#include "fp8q_mlp_launch.h"
+#include "fp8q_mm_fwd.h"
+
+namespace fp8q {
+
+void launch_mm_act(const MmAct& e, hipStream_t st) {
+    const MmFwd& f = e.f;
+    const bool ex = f.M <= kExactMax || f.q || (f.y && f.ydt == kF32) || (f.z && f.zdt == kF32);
+    const Plan p = plan(f.M, f.N, f.K, false, ex);
+    // a cast of up to 16 rows goes through binary32 values in the workspace: a
+    // workgroup of k_mm_rows has no whole group of 128 columns
+    float* pbuf = f.q && p.rows ? (float*)f.ws : nullptr;
+    const FwdArgs a{f.x, f.xs, f.w0, f.ws0, nullptr, nullptr, f.M, f.N, f.K / 128, (uint32_t)p.tm, (uint32_t)p.tn, f.act,
+                    f.y, f.ydt, f.q, f.qfmt, f.sinv, f.z, f.zdt, f.N % 8 == 0, 0, 0, p.kper, (float*)f.ws,
+                    e.bias, e.bdt, e.res};
+    if (p.splits > 1)
+        launch_mm_partial(a, f.xfmt, f.wfmt, p, ex, st);
+    else
+        with_formats(f.xfmt, f.wfmt, [&](auto X, auto W) {
+            constexpr int XF = decltype(X)::value, WF = decltype(W)::value;
+            if (p.rows) return run_rows<XF, WF, kOutAct>(a, pbuf, st);
+            with_tile(p, ex, [&](auto BM, auto EX) {
+                k_mm<XF, WF, decltype(BM)::value, kOutAct, decltype(EX)::value>
+                    <<<(unsigned)(p.tm * p.tn), kMmThreads, 0, st>>>(a);
+            });
+        });
+    if (p.splits > 1) {
+        const JoinArgs j{a.part, p.splits, f.M, f.N, 0, f.act, f.y, f.ydt, f.z, f.zdt, f.q, f.qfmt, f.sinv, e.bias, e.bdt, e.res};
+        const int V = f.N % 4 == 0 ? 4 : 1;
+        const unsigned g = (unsigned)std::min<int64_t>((f.M * (f.N / V) + 255) / 256, 4096);
+        if (f.q) k_mm_join<4, true, true><<<g, 256, 0, st>>>(j);
+        else if (V == 4) k_mm_join<4, false, true><<<g, 256, 0, st>>>(j);
+        else k_mm_join<1, false, true><<<g, 256, 0, st>>>(j);
+    }
+    if (pbuf) launch_group128_cast(pbuf, kF32, f.M * (f.N / 128), f.qfmt, f.q, f.sinv, st);
+}
+
+}  // namespace fp8q

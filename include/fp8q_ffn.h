@@ -69,8 +69,9 @@ extern "C" {
 #endif
 
 /* activation of the gate: x / (1 + exp(-x)); x * Phi(x) with the error
- * function; and its tanh form x/2 * (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
-typedef enum { FP8Q_SILU = 0, FP8Q_GELU = 1, FP8Q_GELU_TANH = 2 } fp8q_act_t;
+ * function; and its tanh form x/2 * (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)));
+ * of the projections of fp8q_mlp.h also x and max(x, 0), which a gate refuses */
+typedef enum { FP8Q_SILU = 0, FP8Q_GELU = 1, FP8Q_GELU_TANH = 2, FP8Q_IDENTITY = 3, FP8Q_RELU = 4 } fp8q_act_t;
 
 /*
  * Residual addition, root-mean-square norm, cast to fp8:

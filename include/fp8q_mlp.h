@@ -74,6 +74,29 @@ fp8q_status_t fp8q_layernorm_backward(const void* dy, const void* h, fp8q_dtype_
                                       int64_t rows, int64_t cols, void* dx, void* dweight, void* dbias,
                                       void* workspace, void* stream);
 
+/*
+ * One projection with a bias, an activation and a residual in its epilogue:
+ *   z = X W^T (+ bias[n]) in binary32  [M, N];
+ *   fp8q_linear_act:      y = act(z) (+ residual), rounded once to ydtype;
+ *   fp8q_linear_act_cast: q, scale_inv = the per-128-group cast of act(z) (from
+ *     binary32, fp8q_cast_per_group128's rule); N % 128 != 0 -> FP8Q_ESHAPE.
+ * act: any fp8q_act_t.  bias: [N] of bdtype, any element type, or NULL.
+ * residual: [M, N] of ydtype, or NULL; y may be the residual itself (in place).
+ * z (or NULL): [M, N] of zdtype, each value rounded once: what the backward
+ * pass reads.  K == 0 gives z = bias; M == 0 or N == 0 is a no-op.
+ * workspace: fp8q_linear_act_workspace_bytes(M, N, K, cast) bytes, cast = 1 for
+ *   fp8q_linear_act_cast.
+ */
+size_t fp8q_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K, int cast);
+fp8q_status_t fp8q_linear_act(const uint8_t* x, fp8q_fmt_t xfmt, const float* x_scale_inv, const uint8_t* w,
+                              fp8q_fmt_t wfmt, const float* w_scale_inv, int64_t M, int64_t N, int64_t K,
+                              const void* bias, fp8q_dtype_t bdtype, fp8q_act_t act, const void* residual, void* y,
+                              fp8q_dtype_t ydtype, void* z, fp8q_dtype_t zdtype, void* workspace, void* stream);
+fp8q_status_t fp8q_linear_act_cast(const uint8_t* x, fp8q_fmt_t xfmt, const float* x_scale_inv, const uint8_t* w,
+                                   fp8q_fmt_t wfmt, const float* w_scale_inv, int64_t M, int64_t N, int64_t K,
+                                   const void* bias, fp8q_dtype_t bdtype, fp8q_act_t act, fp8q_fmt_t fmt, uint8_t* q,
+                                   float* scale_inv, void* z, fp8q_dtype_t zdtype, void* workspace, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,4 +40,18 @@ void launch_layernorm_bwd(const LayerNormBwd& a, hipStream_t) {
     ++g_calls;
 }
 
+int64_t mm_fwd_workspace(int64_t M, int64_t N, int64_t, bool gated, bool cast) {
+    need(M > 0 && N > 0 && !gated);
+    return cast && M <= 64 ? M * N * 4 : M <= 200 ? 16 * M * N : 0;
+}
+
+void launch_mm_act(const MmAct& e, hipStream_t) {
+    const MmFwd& a = e.f;
+    need(a.M > 0 && a.N > 0 && a.K >= 0 && a.K % 128 == 0 && a.act >= 0 && a.act <= kRelu);
+    need(a.K == 0 || (a.x && a.xs && a.w0 && a.ws0 && al(a.x, 16) && al(a.w0, 16)));
+    need((a.y != nullptr) != (a.q != nullptr) && !(a.q && e.res));
+    need(!a.q || (a.sinv && a.N % 128 == 0));
+    ++g_calls;
+}
+
 }  // namespace fp8q

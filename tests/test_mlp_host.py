@@ -110,6 +110,83 @@ def test_layernorm_backward_errors():
     assert L.fp8q_layernorm_backward_workspace_bytes(-4, 250) == 0
 
 
+def _act(cast=False, **k):
+    a = dict(x=at(1), xf=E4, xs=at(2), w=at(3), wf=E4, wsc=at(4), M=300, N=256, K=256, b=at(5), bdt=BF16, act=1)
+    a.update(dict(fmt=E4, q=at(7), s=at(8)) if cast else dict(res=at(6), y=at(7), ydt=BF16))
+    a.update(z=at(9), zdt=BF16, ws=at(10), st=None)
+    a.update(k)
+    return (L.fp8q_linear_act_cast if cast else L.fp8q_linear_act)(*a.values())
+
+
+@pytest.mark.parametrize("cast", [False, True])
+def test_linear_act_errors(cast):
+    f = lambda **k: _act(cast, **k)
+    out = "q" if cast else "y"
+    for bad in (5, -1):
+        assert f(act=bad) == fq.EDTYPE
+    for k in ("xf", "wf", "bdt", "zdt") + (("fmt",) if cast else ("ydt",)):
+        assert f(**{k: 7}) == fq.EDTYPE, k
+    assert f(K=130) == fq.ESHAPE
+    for k in ("M", "N", "K"):
+        assert f(**{k: -128}) == fq.EINVAL, k
+    assert f(M=2 ** 31 + 1) == fq.EINVAL
+    assert f(N=2 ** 21 + 128) == fq.EINVAL
+    assert f(K=2 ** 21 + 128) == fq.EINVAL
+    assert f(M=2 ** 31, N=2 ** 21) == fq.EINVAL            # more tiles than a grid holds
+    for k in ("x", "xs", "w", "wsc", out):
+        assert f(**{k: None}) == fq.EINVAL, k
+    for k in ("x", "w"):
+        assert f(**{k: P(A + 8)}) == fq.EALIGN, k
+    for k in ("xs", "wsc"):
+        assert f(**{k: P(A + 2)}) == fq.EALIGN, k
+    for k in ("b", "z") + (() if cast else ("y", "res")):
+        assert f(**{k: P(A + 1)}) == fq.EALIGN, k
+    assert f(b=P(A + 2), bdt=F32) == fq.EALIGN
+    assert f(z=at(7)) == fq.EINVAL                         # z = the output
+    assert f(z=at(5, 64)) == fq.EINVAL                     # z meets the bias
+    assert f(**{out: at(3)}) == fq.EINVAL
+    assert f(**{out: at(5)}) == fq.EINVAL
+    if cast:
+        assert f(N=200) == fq.ESHAPE
+        assert f(s=None) == fq.EINVAL
+        assert f(s=P(A + 2)) == fq.EALIGN
+        assert L.fp8q_linear_act_workspace_bytes(8, 256, 256, 1) >= 8 * 256 * 4
+        assert f(M=8, ws=None) == fq.EINVAL
+    else:
+        assert f(y=at(6, 2)) == fq.EINVAL                  # y meets the residual but is not it
+        assert f(z=at(6)) == fq.EINVAL
+        need = L.fp8q_linear_act_workspace_bytes(100, 128, 1 << 15, 0)
+        assert need > 0
+        assert f(M=100, N=128, K=1 << 15, ydt=F32, bdt=F32, ws=None) == fq.EINVAL
+        assert f(M=100, N=128, K=1 << 15, ydt=F32, bdt=F32, ws=P(A + 16)) == fq.EALIGN
+        assert f(M=100, N=128, K=1 << 15, ydt=F32, bdt=F32, ws=at(6)) == fq.EINVAL
+    assert f(M=0, x=None, ws=None) == fq.OK
+    assert f(N=0, w=None, ws=None) == fq.OK
+    assert L.fp8q_linear_act_workspace_bytes(-1, 128, 128, 0) == 0
+
+
+def test_python_linear_act_refuses():
+    E = torch.float8_e4m3fn
+    x, xs = torch.zeros(4, 256).to(E), torch.zeros(4, 2)
+    w, ws = torch.zeros(200, 256).to(E), torch.zeros(2, 2)
+    with pytest.raises(ValueError):                        # host tensors
+        fq.linear_act_fp8(x, xs, w, ws)
+    with pytest.raises(ValueError):                        # scales of another shape
+        fq.linear_act_fp8(x, torch.zeros(4, 3), w, ws)
+    with pytest.raises(ValueError):
+        fq.linear_act_fp8(x, xs, w, ws, torch.zeros(199))
+    with pytest.raises(TypeError):                         # not codes
+        fq.linear_act_fp8(x.float(), xs, w, ws)
+    with pytest.raises(TypeError):
+        fq.linear_act_fp8(x, xs, w, ws, activation="swish2")
+    with pytest.raises(TypeError):
+        fq.linear_act_fp8(x, xs, w, ws, x_fmt="e5m2")
+    with pytest.raises(ValueError):                        # residual of another type than y
+        fq.linear_act_fp8(x, xs, w, ws, residual=torch.zeros(4, 200), out=(torch.zeros(4, 200).half(), None))
+    with pytest.raises((ValueError, TypeError)):
+        fq.linear_act_fp8_cast(x, xs, w, ws)               # 200 columns are no groups
+
+
 def test_python_layernorm_refuses():
     x, w = torch.zeros(4, 128), torch.zeros(128)
     with pytest.raises(ValueError):                        # host tensors
