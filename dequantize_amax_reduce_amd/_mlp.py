@@ -6,7 +6,9 @@ Re-exported by the package; laid out as _ffn.py is.
     q, s, h, mean, rstd = layernorm_cast(x, weight, bias, residual)     # norm -> fp8 per 128-group
     p, ps, z = linear_act_fp8_cast(q, s, w1, w1s, b1, "gelu", keep=torch.bfloat16)
     y, _ = linear_act_fp8(p, ps, w2, w2s, b2, residual=h)               # the new residual stream
-    dx, dweight, dbias = layernorm_backward(dn, h, weight, mean, rstd, dh)
+    dp, dw2, db2 = linear_act_fp8_backward(dy, None, p, ps, w2, w2s)
+    dn, dw1, db1 = linear_act_fp8_backward(dp, z, q, s, w1, w1s, "gelu")
+    dx, dweight, dbias = layernorm_backward(dn, h, weight, mean, rstd, dy)
 """
 from __future__ import annotations
 
@@ -34,6 +36,8 @@ MLP_SIGNATURES = {
     "fp8q_linear_act_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I]),
     "fp8q_linear_act": (_I, _CODES + _CODES + [_I64, _I64, _I64, _P, _I, _I, _P, _P, _I, _P, _I, _P, _P]),
     "fp8q_linear_act_cast": (_I, _CODES + _CODES + [_I64, _I64, _I64, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P]),
+    "fp8q_linear_act_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "fp8q_linear_act_backward": (_I, [_P, _P, _I] + _CODES + _CODES + [_I64, _I64, _I64, _I, _P, _P, _P, _I, _P, _P]),
 }
 MLP_FUNCTIONS = tuple(MLP_SIGNATURES)
 
@@ -212,6 +216,36 @@ def fp8q_linear_act_cast(x, x_scale_inv, w, w_scale_inv, bias, q, scale_inv, z=N
           _ptr(scale_inv, "scale_inv"), *_typed(z, (M, N), "z"), _opt(scratch, "workspace"), _stream(x, stream))
 
 
+def fp8q_linear_act_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return lib.fp8q_linear_act_backward_workspace_bytes(M, N, K)
+
+
+def fp8q_linear_act_backward(dy, z, x, x_scale_inv, w, w_scale_inv, dx=None, dw=None, dbias=None, activation=None,
+                             workspace=None, stream=None, x_fmt=None, w_fmt=None) -> None:
+    name = "fp8q_linear_act_backward"
+    act, g = _activation(activation), _ffn._grad_dtype((dw, dbias))
+    xf, wf = _formats(x, x_fmt, w_fmt, w)
+    xa, M, K = _x_codes(x, x_scale_inv, xf)
+    wp, wsp, N = _w_codes(w, w_scale_inv, K, "w")
+    dt = _hp_dtype(dy, "dy")
+    _same(dy, (M, N), dy.dtype, "dy")
+    _same(dx, (M, K), dy.dtype, "dx")
+    if act == IDENTITY:
+        z = None
+    elif z is None:
+        raise ValueError(f"{name}: an activation's gradient needs z")
+    _same(z, (M, N), dy.dtype, "z")
+    if dw is not None:
+        _same(dw, (N, K), dw.dtype, "dw")
+    if dbias is not None and dbias.numel() != N:
+        raise ValueError(f"{name}: dbias must have w's rows")
+    gdt = dt if g is None else _hp_dtype(dw if dw is not None else dbias, "dw")
+    scratch = _ws(workspace, lib.fp8q_linear_act_backward_workspace_bytes(M, N, K), x, name)
+    _call(name, x, (dy, z, x_scale_inv, w, w_scale_inv, dx, dw, dbias, scratch), _ptr(dy, "dy"), _opt(z, "z"), dt, *xa, wp,
+          wf, wsp, M, N, K, act, _opt(dx, "dx"), _opt(dw, "dw"), _opt(dbias, "dbias"), gdt, _opt(scratch, "workspace"),
+          _stream(x, stream))
+
+
 # ---------------------------------------------------------------------------
 # helpers that allocate outputs and workspaces
 # ---------------------------------------------------------------------------
@@ -301,6 +335,25 @@ def linear_act_fp8_cast(x, x_scale_inv, w, w_scale_inv, bias=None, activation=No
     return q, s, z
 
 
+def linear_act_fp8_backward(dy, z, x, x_scale_inv, w, w_scale_inv, activation=None, grad_type=None, with_bias=True,
+                            out=None, x_fmt=None, w_fmt=None):
+    """(dx, dw, dbias) of linear_act_fp8 and of linear_act_fp8_cast from dy and
+    the forward's z (None without an activation), dx in dy's dtype (bf16 or
+    f16), dw and dbias in grad_type (dy's dtype by default, or float32); dbias is
+    None with with_bias=False.  The residual's gradient is dy itself."""
+    if out is not None:
+        dx, dw, db = out
+    else:
+        dx = torch.empty(x.shape, dtype=dy.dtype, device=x.device)
+        dw = torch.empty(w.shape, dtype=grad_type or dy.dtype, device=x.device)
+        db = torch.empty(w.shape[0], dtype=dw.dtype, device=x.device) if with_bias else None
+    if not with_bias:
+        db = None
+    fp8q_linear_act_backward(dy, z, x, x_scale_inv, w, w_scale_inv, dx, dw, db, activation, _AUTO, x_fmt=x_fmt, w_fmt=w_fmt)
+    return dx, dw, db
+
+
 MLP_NAMES = [n for n in dir() if n.startswith("fp8q_")] + [
     "IDENTITY", "RELU", "MLP_HEADER_PATH", "MLP_FUNCTIONS", "mlp_header_functions", "load_mlp",
-    "layernorm", "layernorm_cast", "layernorm_backward", "linear_act_fp8", "linear_act_fp8_cast"]
+    "layernorm", "layernorm_cast", "layernorm_backward", "linear_act_fp8", "linear_act_fp8_cast",
+    "linear_act_fp8_backward"]

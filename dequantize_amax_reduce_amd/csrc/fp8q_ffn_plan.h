@@ -99,8 +99,12 @@ inline Plan16 plan16(int64_t M, int64_t N, int64_t K) {
 // gated pair one product, the gate's rows padded to 64).  With a rest the
 // contraction is padded to 128 and half as long again in time.
 inline int64_t rows_padded(int64_t M, bool rest) { return rest ? (M + 127) / 128 * 128 : up64(M); }
+// columns of dz: of a gated pair twice N padded to 64, so a multiple of 128
+inline int64_t dz_columns(int64_t N, bool gated, bool rest) {
+    return gated ? 2 * up64(N) : rest ? (N + 127) / 128 * 128 : up64(N);
+}
 inline Plan16 plan_dx(int64_t M, int64_t N, int64_t K, bool gated, bool rest) {
-    const int64_t C = (gated ? 2 : 1) * up64(N);
+    const int64_t C = dz_columns(N, gated, rest);
     return plan16(M, K, rest ? C + C / 2 : C);
 }
 inline Plan16 plan_dw(int64_t M, int64_t N, int64_t K, bool gated, bool rest) {

@@ -187,4 +187,54 @@ fp8q_status_t fp8q_linear_act_cast(const uint8_t* x, fp8q_fmt_t xfmt, const floa
     return linear_act(e, M, N, K, stream);
 }
 
+size_t fp8q_linear_act_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (!sizes_ok(M, N, K, kMaxRows)) return 0;
+    return (size_t)fp8q::mm_act_bwd_workspace(M, N, K);
+}
+
+fp8q_status_t fp8q_linear_act_backward(const void* dy, const void* z, fp8q_dtype_t dtype, const uint8_t* x,
+                                       fp8q_fmt_t xfmt, const float* x_scale_inv, const uint8_t* w, fp8q_fmt_t wfmt,
+                                       const float* w_scale_inv, int64_t M, int64_t N, int64_t K, fp8q_act_t act,
+                                       void* dx, void* dw, void* dbias, fp8q_dtype_t dwdtype, void* workspace,
+                                       void* stream) {
+    if (!half_dtype(dtype) || !valid_fmt(xfmt) || !valid_fmt(wfmt) || !valid_unary(act) ||
+        (dwdtype != dtype && dwdtype != FP8Q_F32))
+        return FP8Q_EDTYPE;
+    fp8q_status_t st = check_sizes(M, N, K, kMaxRows);
+    if (st != FP8Q_OK) return st;
+    if (!grid_ok(M, K) || !grid_ok(2 * N + 64, K)) return FP8Q_EINVAL;
+    // the layout pass: 64 x 64 tiles of dy, 64 x 128 of the codes, 256 threads each
+    const int64_t mt = M / 64 + 2, nt = N / 64 + 2;         // both are padded to 64 or 128
+    if (mt * nt + (K / 128) * (mt + nt) >= int64_t(1) << 24) return FP8Q_EINVAL;
+    const int64_t n = M * N;
+    const void* zin = act == FP8Q_IDENTITY ? nullptr : z;
+    if (n > 0 && (!dy || (act != FP8Q_IDENTITY && !z))) return FP8Q_EINVAL;
+    const bool products = K > 0 && (dx || dw);
+    if (n > 0 && products) {
+        for (const Codes& c : {Codes{x, x_scale_inv, M, M}, Codes{w, w_scale_inv, N, 0}}) {
+            st = check_codes(c, K);
+            if (st != FP8Q_OK) return st;
+        }
+    }
+    const int64_t we = esize(dwdtype), KB = K / 128;
+    if (!aligned(dy, 2) || !aligned(zin, 2) || !aligned(dx, 2) || !aligned(dw, we) || !aligned(dbias, we)) return FP8Q_EALIGN;
+    if (!products && !dbias) return FP8Q_OK;
+    const int64_t wsb = fp8q::mm_act_bwd_workspace(M, N, K);
+    st = check_ws(workspace, wsb);
+    if (st != FP8Q_OK) return st;
+    const Buf b[] = {{dx, M * K * 2}, {dw, N * K * we}, {dbias, N * we}, {workspace, wsb}, {dy, n * 2}, {zin, n * 2},
+                     {x, M * K}, {x_scale_inv, 4 * M * KB}, {w, N * K}, {w_scale_inv, 4 * blocks(N) * KB}};
+    if (bad_overlap(b, 10, 4)) return FP8Q_EINVAL;
+    // empty outputs: dx without rows, dw and dbias without columns
+    const bool any = (dx && M > 0 && K > 0) || (dw && N > 0 && K > 0) || (dbias && N > 0);
+    if (!any) return FP8Q_OK;
+    fp8q::MmActBwd e{};
+    fp8q::MmBwd& f = e.f;
+    f.dy = dy; f.z = zin; f.dt = dtype; f.x = x; f.xs = x_scale_inv; f.w0 = w; f.ws0 = w_scale_inv;
+    f.M = M; f.N = (int)N; f.K = (int)K; f.xfmt = xfmt; f.wfmt = wfmt; f.act = act;
+    f.dx = dx; f.dw0 = dw; f.dwdt = dwdtype; f.ws = workspace; e.db = dbias;
+    fp8q::launch_mm_act_bwd(e, S(stream));
+    return launched();
+}
+
 }  // extern "C"

@@ -62,4 +62,14 @@ struct MmAct {
 };
 void launch_mm_act(const MmAct& a, hipStream_t st);
 
+// Its backward: dz = dy act'(z), f.dx, f.dw0 and db, each or null (not all
+// three); f.z is null where act is the identity.  f.w1, f.ws1, f.dw1 and f.gated
+// are unused; any of f.M, f.N and f.K may be 0 (sums over nothing are zeros).
+struct MmActBwd {
+    MmBwd f;
+    void* db;            // [N] of f.dwdt, or nullptr
+};
+int64_t mm_act_bwd_workspace(int64_t M, int64_t N, int64_t K);
+void launch_mm_act_bwd(const MmActBwd& a, hipStream_t st);
+
 }  // namespace fp8q

@@ -1,6 +1,7 @@
 // fp8q_mm_bwd.hip -- the backward products of the projections.
 //
-//   dg = dp u act'(g), du = dp act(g)         (a projection: dg = dy)
+//   dg = dp u act'(g), du = dp act(g)         (a projection: dg = dy, with an
+//                                              activation dg = dy act'(z), dbias = sum_m dg)
 //   dx = [dg | du] [Wg ; Wu]                  contraction over the columns
 //   [dWg ; dWu] = [dg | du]^T X               contraction over the rows
 //
@@ -32,13 +33,14 @@
 // results allow 2.1e-4, and 2.9e-3 where bf16 results allow 1.7e-3.
 //
 // An f16 gradient keeps as many bits as an operand, so each operand's rounding
-// shows: of a gated pair, whose dz is computed, both (3.6e-4; a projection's f16
+// shows: of a dz that is computed, both (3.6e-4 of a gated pair; a projection's f16
 // dy is exact as it is).  There dz has a rest beside it, dz - f16(dz) as e5m2, and
 // the contraction starts with the rest's products by X' or W' as e5m2, on the
 // fp8 instruction at twice the rate: 2.4e-4 to 2.8e-4, for half the products'
 // time more (4096 x 7168 -> 18432: 2644 and 2565 us).
 #include "fp8q_ffn_plan.h"
 #include "fp8q_host.h"
+#include "fp8q_mlp_launch.h"
 #include "fp8q_mm.h"
 
 namespace fp8q {
@@ -62,7 +64,9 @@ struct Mm16Args {
     float* part;           // [splits][M][N] sums as they are, where splits > 1
 };
 
-constexpr bool has_rest(int dt, bool gated) { return gated && dt == kF16; }
+// what dz is made of: dy itself, a gated pair's, or dy and one activation's slope
+enum { kOfLinear = 0, kOfGated = 1, kOfUnary = 2 };
+constexpr bool has_rest(int dt, int mode) { return mode != kOfLinear && dt == kF16; }
 
 // Keys hold exponents in a form that an unsigned max folds: a finite nonzero
 // binary32 v has a key k > 0 with |v| < 2^(k - kKeyBias - 126), 0 stands for
@@ -319,7 +323,7 @@ __device__ __forceinline__ float rest_of(float v, uint32_t half) {
 // ---------------------------------------------------------------------------
 
 // the largest finite scale of every row of X and block row of W (1 where there
-// is none; a projection's down to its power of two), and the keys cleared for
+// is none; where dz is dy itself, down to its power of two), and the keys cleared for
 // k_keys; 16 lanes a row
 struct ScaleArgs {
     const float* xs;       // [M, KB]
@@ -331,6 +335,7 @@ struct ScaleArgs {
     float* sw;             // [ws1 ? 2 nb : nb]
     uint32_t* keys;
     int64_t nkeys;
+    bool whole;            // as they are; else their powers of two
 };
 __global__ void __launch_bounds__(256) k_scales(ScaleArgs a) {
     const int64_t total = a.M + (a.ws1 ? 2 : 1) * (int64_t)a.nb;
@@ -344,19 +349,30 @@ __global__ void __launch_bounds__(256) k_scales(ScaleArgs a) {
         uint32_t m = 0;
         for (int kb = l; kb < a.KB; kb += 16) m = umax(m, finite_bits(s[kb]));
         m = max_lanes<16>(m);
-        if (!a.ws1 && m) m = umax(m & 0x7F800000u, 0x00800000u);
+        if (!a.whole && m) m = umax(m & 0x7F800000u, 0x00800000u);
         if (l == 0) (row < a.M ? a.sx + row : a.sw + (row - a.M))[0] = m ? __uint_as_float(m) : 1.0f;
     }
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.nkeys; i += (int64_t)gridDim.x * 256) a.keys[i] = 0;
 }
 
-// 8 columns of dg (dz for a projection) and du from column c of row m < M;
+// 8 columns of dg (dz without a gate) and du from column c of row m < M;
 // zero from column N on (FULL: there are none); QUICK as in act_at
-template <int DT, bool GATED, bool FULL, bool QUICK>
+template <int DT, int MODE, bool FULL, bool QUICK>
 __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z, int64_t m, int c, int N, int act,
                                           float* g, float* u) {
     ld8<DT, FULL>(dy + m * N, c, N, g);
-    if constexpr (GATED) {
+    if constexpr (MODE == kOfUnary) {
+        float zv[8];
+        ld8<DT, FULL>(z + m * N, c, N, zv);
+        with_unary(act, [&](auto A) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const Act r = act_at<decltype(A)::value, true, QUICK>(zv[k]);
+                g[k] = FULL || c + k < N ? g[k] * r.d * r.e : 0.0f;
+            }
+        });
+    }
+    if constexpr (MODE == kOfGated) {
         float zg[8], zu[8];
         ld8<DT, FULL>(z + m * 2 * N, c, N, zg);
         ld8<DT, FULL>(z + m * 2 * N + N, c, N, zu);
@@ -419,8 +435,8 @@ __device__ __forceinline__ void scale_keys(const float* s, const float* top, int
     __syncthreads();
     if ((int)threadIdx.x < KB && lds[threadIdx.x]) atomicMax(out + threadIdx.x, lds[threadIdx.x]);
 }
-template <int DT, bool GATED> __global__ void __launch_bounds__(256) k_keys(KeyArgs a) {
-    constexpr int H = GATED ? 2 : 1;
+template <int DT, int MODE> __global__ void __launch_bounds__(256) k_keys(KeyArgs a) {
+    constexpr int H = MODE == kOfGated ? 2 : 1;
     __shared__ uint32_t lds[4][H][128];
     if (blockIdx.x >= a.e0) {
         int64_t i = blockIdx.x - a.e0;
@@ -446,7 +462,7 @@ template <int DT, bool GATED> __global__ void __launch_bounds__(256) k_keys(KeyA
     // atomics on one word take 8 ns each: only a row's own lanes make them).
     // The loads of R rows are in flight at once.
     auto rows = [&](auto FULL) {
-        constexpr int R = GATED ? 2 : 4;
+        constexpr int R = MODE == kOfLinear ? 4 : 2;
 #pragma unroll 1
         for (int i = 0; i < 8; i += R) {
             float d[R][H][8];
@@ -457,7 +473,7 @@ template <int DT, bool GATED> __global__ void __launch_bounds__(256) k_keys(KeyA
                 m[r] = m0 + (i + r) * 16 + rl;
                 if (m[r] > a.M - 1) m[r] = a.M - 1;
                 ex[r] = exponent_of(a.sx[m[r]]);
-                dz_values<DT, GATED, decltype(FULL)::value, true>(a.dy, a.z, m[r], c, a.N, a.act, d[r][0], d[r][H - 1]);
+                dz_values<DT, MODE, decltype(FULL)::value, true>(a.dy, a.z, m[r], c, a.N, a.act, d[r][0], d[r][H - 1]);
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -511,14 +527,15 @@ struct DzArgs {
     int nb;
     const uint32_t* krow;  // [M]
     const uint32_t* kcol;  // [gated ? 2 Np : Np]
+    float* bias;           // [Mp / 64][N] sums of 64 rows of dz each, or nullptr
 };
 
 // dz sw and the transpose of dz sx, each below its own exponents; 256
 // threads, one 64 x 64 tile a workgroup; thread (i, v) takes 8 columns of the
 // rows 2i and 2i + 1
-template <int DT, bool GATED, bool REST>
+template <int DT, int MODE, bool BIAS, bool REST>
 __device__ __forceinline__ void dz_tile(const DzArgs& a, uint32_t bx, uint32_t by, TileT* lds, TileT8* lds8) {
-    constexpr int H = GATED ? 2 : 1, E = REST ? 3 : 2;      // bytes an element takes of a row
+    constexpr int H = MODE == kOfGated ? 2 : 1, E = REST ? 3 : 2;   // bytes an element takes of a row
     const int v = (int)threadIdx.x & 7, i = (int)threadIdx.x >> 3;
     const int64_t m = (int64_t)by * 64 + 2 * i;
     const int c = (int)bx * 64 + v * 8;
@@ -534,8 +551,8 @@ __device__ __forceinline__ void dz_tile(const DzArgs& a, uint32_t bx, uint32_t b
                 for (int k = 0; k < 8; ++k) d[r][h][k] = 0.0f;
             continue;
         }
-        dz_values<DT, GATED, false, false>(a.dy, a.z, m + r, c, a.N, a.act, d[r][0], d[r][H - 1]);
-        sx[r] = a.sx[m + r];
+        dz_values<DT, MODE, false, false>(a.dy, a.z, m + r, c, a.N, a.act, d[r][0], d[r][H - 1]);
+        if (!BIAS || a.dzt) sx[r] = a.sx[m + r];
         if (a.dz) {
             const int e = exp_of(a.krow[m + r], 0);
             char* row = a.dz + (m + r) * C * E;
@@ -555,6 +572,23 @@ __device__ __forceinline__ void dz_tile(const DzArgs& a, uint32_t bx, uint32_t b
                     *(v2u*)(row + at) = v2u{enc4<kE5M2>(t[0], t[1], t[2], t[3]), enc4<kE5M2>(t[4], t[5], t[6], t[7])};
                 }
             }
+        }
+    }
+    if constexpr (BIAS) {
+        if (a.bias) {                                       // the wave's 16 rows, then the four waves
+            float* sums = (float*)lds;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float s = d[0][0][k] + d[1][0][k];
+                s += __shfl_xor(s, 8, 64);
+                s += __shfl_xor(s, 16, 64);
+                s += __shfl_xor(s, 32, 64);
+                if ((i & 7) == 0) sums[(i >> 3) * 64 + v * 8 + k] = s;
+            }
+            __syncthreads();
+            const int t = (int)threadIdx.x, col = (int)bx * 64 + t;
+            if (t < 64 && col < a.N) a.bias[(int64_t)by * a.N + col] = (sums[t] + sums[64 + t]) + (sums[128 + t] + sums[192 + t]);
+            __syncthreads();                                // the tiles are written there next
         }
     }
     if (!a.dzt) return;
@@ -642,13 +676,13 @@ struct PrepArgs {
     DeqTArgs x, w0, w1;
     uint32_t e0, e1, e2, dzx;
 };
-template <int DT, bool GATED, int XF, int WF> __global__ void __launch_bounds__(256) k_prep(PrepArgs a) {
-    constexpr bool REST = has_rest(DT, GATED);
+template <int DT, int MODE, bool BIAS, int XF, int WF> __global__ void __launch_bounds__(256) k_prep(PrepArgs a) {
+    constexpr bool REST = has_rest(DT, MODE);
     __shared__ TileT lds[2];
     __shared__ __attribute__((aligned(16))) TileT8 lds8[REST ? 2 : 1];
     const uint32_t b = blockIdx.x;
     if (b < a.e0) {
-        dz_tile<DT, GATED, REST>(a.dz, b % a.dzx, b / a.dzx, lds, lds8);
+        dz_tile<DT, MODE, BIAS, REST>(a.dz, b % a.dzx, b / a.dzx, lds, lds8);
     } else if (b < a.e1) {
         const uint32_t i = b - a.e0;
         deq_tile<XF, REST>(a.x, i % (uint32_t)a.x.KB, i / (uint32_t)a.x.KB, lds, lds8);
@@ -702,10 +736,15 @@ template <typename F> void with_fmt(int f, F&& go) {
     else go(KC<kE5M2>{});
 }
 
-// go(DT, GATED)
-template <typename F> void with_dt(int dt, bool gated, F&& go) {
-    if (dt == kBF16) { if (gated) go(KC<kBF16>{}, std::true_type{}); else go(KC<kBF16>{}, std::false_type{}); }
-    else { if (gated) go(KC<kF16>{}, std::true_type{}); else go(KC<kF16>{}, std::false_type{}); }
+// go(DT, MODE)
+template <typename F> void with_dt(int dt, int mode, F&& go) {
+    auto of = [&](auto DT) {
+        if (mode == kOfLinear) go(DT, KC<kOfLinear>{});
+        else if (mode == kOfGated) go(DT, KC<kOfGated>{});
+        else go(DT, KC<kOfUnary>{});
+    };
+    if (dt == kBF16) of(KC<kBF16>{});
+    else of(KC<kF16>{});
 }
 
 struct BwdLayout {
@@ -719,8 +758,8 @@ struct BwdLayout {
 BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated, bool rest) {
     BwdLayout l;
     l.Mp = rows_padded(M, rest);
-    l.Np = up64(N);
-    l.C = gated ? 2 * l.Np : l.Np;
+    l.C = dz_columns(N, gated, rest);
+    l.Np = gated ? l.C / 2 : l.C;
     int64_t at = 0;
     auto take = [&](int64_t bytes) { const int64_t p = at; at += up256(bytes); return p; };
     const int e = rest ? 3 : 2;                             // bytes an element
@@ -746,21 +785,14 @@ void launch_zero16(void* p, int64_t n, hipStream_t st) {
     k_zero16<<<(unsigned)std::min<int64_t>((n + 255) / 256, 65536), 256, 0, st>>>((uint16_t*)p, n);
 }
 
-int64_t mm_bwd_workspace(int64_t M, int64_t N, int64_t K, bool gated) {
-    if (M == 0 || N == 0 || K == 0) return 0;
-    // enough for either type of gradient, which is not known here
-    return std::max(layout(M, N, K, gated, false).bytes, layout(M, N, K, gated, has_rest(kF16, gated)).bytes);
-}
+namespace {
 
-void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
-    const bool gated = f.gated;
-    if (f.M == 0 || f.N == 0 || f.K == 0) {
-        zero(f.dx, f.M * f.K, f.dt, st);
-        zero(f.dw0, (int64_t)f.N * f.K, f.dwdt, st);
-        zero(f.dw1, (int64_t)f.N * f.K, f.dwdt, st);
-        return;
-    }
-    const bool rest = has_rest(f.dt, gated);
+int64_t bias_rows(int64_t M) { return (M + 127) / 128 * 2; }  // sums of 64 rows, padded as M is with a rest
+
+// dx, the weight gradients and, of a projection, the partial sums of dbias
+// (bias: [bias_rows(M)][N] floats, or nullptr); sizes > 0
+void run_bwd(const MmBwd& f, int mode, float* bias, hipStream_t st) {
+    const bool gated = mode == kOfGated, rest = has_rest(f.dt, mode);
     const BwdLayout l = layout(f.M, f.N, f.K, gated, rest);
     char* ws = (char*)f.ws;
     char *dz = ws + l.dz, *dzt = ws + l.dzt, *wt = ws + l.wt, *xt = ws + l.xt;
@@ -772,18 +804,18 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
     uint32_t *krow = (uint32_t*)(ws + l.krow), *kcol = (uint32_t*)(ws + l.kcol), *kx = (uint32_t*)(ws + l.kx),
              *kw = (uint32_t*)(ws + l.kw);
     const float* ws1 = gated ? f.ws1 : nullptr;
-    const ScaleArgs sa{f.xs, f.M, f.ws0, ws1, nb, KB, sx, sw, krow, l.nkeys};
+    const ScaleArgs sa{f.xs, f.M, f.ws0, ws1, nb, KB, sx, sw, krow, l.nkeys, mode != kOfLinear};
     k_scales<<<(unsigned)std::min<int64_t>((f.M + (gated ? 2 : 1) * nb + 15) / 16, 4096), 256, 0, st>>>(sa);
     KeyArgs ka{(const uint16_t*)f.dy, (const uint16_t*)f.z, f.M, f.N, f.act, sx, sw, wdx ? krow : nullptr,
                wdw ? kcol : nullptr, (int)l.Np, f.xs, f.ws0, ws1, nb, KB, kx, kw, 0, 0, (uint32_t)nb};
     ka.e0 = (uint32_t)nb * (uint32_t)((f.M + 127) / 128);
     ka.e1 = ka.e0 + (uint32_t)((f.M + kKeyRows - 1) / kKeyRows);
     const unsigned gk = ka.e1 + (gated ? 2 : 1) * (uint32_t)((nb + kKeyRows - 1) / kKeyRows);
-    with_dt(f.dt, gated, [&](auto DT, auto GT) { k_keys<decltype(DT)::value, decltype(GT)::value><<<gk, 256, 0, st>>>(ka); });
+    with_dt(f.dt, mode, [&](auto DT, auto MD) { k_keys<decltype(DT)::value, decltype(MD)::value><<<gk, 256, 0, st>>>(ka); });
     PrepArgs p{};
     const int qx = f.xfmt == kE4M3 ? 9 : 16, qw = f.wfmt == kE4M3 ? 9 : 16;   // 448 < 2^9, 57344 < 2^16
     p.dz = DzArgs{(const uint16_t*)f.dy, (const uint16_t*)f.z, f.M, l.Mp, f.N, (int)l.Np, f.act,
-                  wdx ? dz : nullptr, wdw ? dzt : nullptr, sx, sw, nb, krow, kcol};
+                  wdx ? dz : nullptr, wdw ? dzt : nullptr, sx, sw, nb, krow, kcol, bias};
     p.x = DeqTArgs{f.x, f.xs, f.M, KB, 0, xt, l.Mp, 0, sx, kx, qx};
     p.w0 = DeqTArgs{f.w0, f.ws0, f.N, KB, 7, wt, l.C, 0, sw, kw, qw};
     p.w1 = DeqTArgs{f.w1, f.ws1, f.N, KB, 7, wt, l.C, l.Np, sw + nb, kw, qw};
@@ -796,8 +828,12 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
     with_fmt(f.xfmt, [&](auto X) {
         with_fmt(f.wfmt, [&](auto W) {
             constexpr int XF = decltype(X)::value, WF = decltype(W)::value;
-            with_dt(f.dt, gated, [&](auto DT, auto GT) {
-                k_prep<decltype(DT)::value, decltype(GT)::value, XF, WF><<<g, 256, 0, st>>>(p);
+            with_dt(f.dt, mode, [&](auto DT, auto MD) {
+                constexpr int T = decltype(DT)::value, MODE = decltype(MD)::value;
+                // an activation without a gate comes with a bias more often than not: one instance serves both
+                if constexpr (MODE == kOfUnary) k_prep<T, MODE, true, XF, WF><<<g, 256, 0, st>>>(p);
+                else if (MODE == kOfLinear && bias) k_prep<T, kOfLinear, true, XF, WF><<<g, 256, 0, st>>>(p);
+                else k_prep<T, MODE, false, XF, WF><<<g, 256, 0, st>>>(p);
             });
         });
     });
@@ -807,6 +843,62 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
     if (wdw)
         mm16(dzt, xt, gated ? l.Np + f.N : f.N, f.K, l.Mp, rest, f.dw0, gated ? f.dw1 : nullptr, f.N, gated ? l.Np : f.N,
              f.dwdt, plan_dw(f.M, f.N, f.K, gated, rest), kcol, kx, qx, part, st);
+}
+
+}  // namespace
+
+int64_t mm_bwd_workspace(int64_t M, int64_t N, int64_t K, bool gated) {
+    if (M == 0 || N == 0 || K == 0) return 0;
+    // enough for either type of gradient, which is not known here
+    return std::max(layout(M, N, K, gated, false).bytes, layout(M, N, K, gated, gated).bytes);
+}
+
+void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
+    if (f.M == 0 || f.N == 0 || f.K == 0) {
+        zero(f.dx, f.M * f.K, f.dt, st);
+        zero(f.dw0, (int64_t)f.N * f.K, f.dwdt, st);
+        zero(f.dw1, (int64_t)f.N * f.K, f.dwdt, st);
+        return;
+    }
+    run_bwd(f, f.gated ? kOfGated : kOfLinear, nullptr, st);
+}
+
+int64_t mm_act_bwd_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M == 0 || N == 0) return 0;
+    const int64_t products = K == 0 ? 0 : std::max(layout(M, N, K, false, false).bytes, layout(M, N, K, false, true).bytes);
+    return products + bias_rows(M) * N * 4;
+}
+
+void launch_mm_act_bwd(const MmActBwd& e, hipStream_t st) {
+    const MmBwd& f = e.f;
+    if (f.M == 0 || f.N == 0) {
+        zero(f.dx, f.M * f.K, f.dt, st);
+        zero(f.dw0, (int64_t)f.N * f.K, f.dwdt, st);
+        zero(e.db, f.N, f.dwdt, st);
+        return;
+    }
+    const int mode = f.act == kIdentity ? kOfLinear : kOfUnary;
+    const bool products = f.K > 0 && (f.dx || f.dw0), rest = has_rest(f.dt, mode);
+    float* bias = e.db ? (float*)((char*)f.ws + (products ? layout(f.M, f.N, f.K, false, rest).bytes : 0)) : nullptr;
+    const int64_t tiles = (products ? rows_padded(f.M, rest) : up64(f.M)) / 64;
+    if (products) {
+        run_bwd(f, mode, bias, st);
+    } else {                                                // dbias alone: the tiles of dz, none laid out
+        PrepArgs p{};
+        p.dz.dy = (const uint16_t*)f.dy;
+        p.dz.z = (const uint16_t*)f.z;
+        p.dz.M = f.M;
+        p.dz.N = f.N;
+        p.dz.act = f.act;
+        p.dz.bias = bias;
+        p.dzx = (uint32_t)(up64(f.N) / 64);
+        p.e0 = p.e1 = p.e2 = p.dzx * (uint32_t)tiles;
+        with_dt(f.dt, mode, [&](auto DT, auto MD) {
+            if constexpr (decltype(MD)::value != kOfGated)
+                k_prep<decltype(DT)::value, decltype(MD)::value, true, kE4M3, kE4M3><<<p.e0, 256, 0, st>>>(p);
+        });
+    }
+    if (e.db) launch_column_sums(bias, tiles, f.N, e.db, nullptr, f.dwdt, st);
 }
 
 }  // namespace fp8q

@@ -97,6 +97,27 @@ fp8q_status_t fp8q_linear_act_cast(const uint8_t* x, fp8q_fmt_t xfmt, const floa
                                    const void* bias, fp8q_dtype_t bdtype, fp8q_act_t act, fp8q_fmt_t fmt, uint8_t* q,
                                    float* scale_inv, void* z, fp8q_dtype_t zdtype, void* workspace, void* stream);
 
+/*
+ * Its backward, from dy [M, N] (the gradient of y or of the cast's values; the
+ * residual's gradient is dy itself) and the forward's z [M, N]:
+ *   dz = dy * act'(z) in binary32;  dx [M, K] = dz W;  dw [N, K] = dz^T X;
+ *   dbias[n] = sum_m dz, in binary32 from the unrounded dz.
+ * act' of FP8Q_RELU is 0 from 0 down.  With FP8Q_IDENTITY dz = dy and z is not
+ * read (it may be NULL).  dy and z are bf16 or f16 (FP8Q_F32 -> FP8Q_EDTYPE); dx
+ * has their type, dw and dbias dwdtype: that type or FP8Q_F32.  dx, dw and dbias
+ * may each be NULL (not computed).  The operands of the two products, their
+ * precision and the limits are those of fp8q_linear_backward, with an activation
+ * those of fp8q_gated_linear_backward.  M == 0 writes dw = 0 and dbias = 0, N == 0
+ * dx = 0.
+ * workspace: fp8q_linear_act_backward_workspace_bytes(M, N, K) bytes.
+ */
+size_t fp8q_linear_act_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+fp8q_status_t fp8q_linear_act_backward(const void* dy, const void* z, fp8q_dtype_t dtype, const uint8_t* x,
+                                       fp8q_fmt_t xfmt, const float* x_scale_inv, const uint8_t* w, fp8q_fmt_t wfmt,
+                                       const float* w_scale_inv, int64_t M, int64_t N, int64_t K, fp8q_act_t act,
+                                       void* dx, void* dw, void* dbias, fp8q_dtype_t dwdtype, void* workspace,
+                                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -54,4 +54,17 @@ void launch_mm_act(const MmAct& e, hipStream_t) {
     ++g_calls;
 }
 
+int64_t mm_act_bwd_workspace(int64_t M, int64_t N, int64_t K) { return M && N ? (K ? 2 << 20 : 1 << 20) : 0; }
+
+void launch_mm_act_bwd(const MmActBwd& e, hipStream_t) {
+    const MmBwd& a = e.f;
+    need(a.M >= 0 && a.N >= 0 && a.K >= 0 && a.K % 128 == 0 && (a.dx || a.dw0 || e.db));
+    need((a.dt == kBF16 || a.dt == kF16) && (a.dwdt == a.dt || a.dwdt == kF32) && a.act >= 0 && a.act <= kRelu);
+    if (a.M > 0 && a.N > 0) {
+        need(a.dy && (a.z != nullptr) == (a.act != kIdentity) && a.ws && al(a.ws, 256));
+        if (a.K > 0 && (a.dx || a.dw0)) need(a.x && a.xs && a.w0 && a.ws0 && al(a.x, 16) && al(a.w0, 16));
+    }
+    ++g_calls;
+}
+
 }  // namespace fp8q

@@ -8,9 +8,10 @@ import pytest
 import torch
 
 import dequantize_amax_reduce_amd as fq
-from ffn_plans import FORWARD
+from ffn_plans import BACKWARD, FORWARD
+from mlp_plans import BACKWARD_REST
 from gpu_util import G, TORCH_HP
-from test_gpu_ffn import D, FP8, act64, cast_close, codes, gen_of, near, out_tol, rand, sum_err, up, w64, x64
+from test_gpu_ffn import BWD, D, FP8, act64, bwd_err, cast_close, codes, gen_of, near, out_tol, rand, sum_err, up, w64, x64
 
 pytestmark = pytest.mark.gpu
 
@@ -194,22 +195,165 @@ def test_offsets_past_32_bits():
     near(y[rows.cuda()], v + 1, out_tol(v + 1, "bf16", err + 2.0 ** -23), "far rows")
 
 
-@pytest.mark.parametrize("M", [1, 40, 200])
-def test_streams_graphs_and_two_at_once(M):
-    """Twice, two calls at once on two streams, and replayed from a graph with
-    eager calls between: the same bits every time."""
-    g = gen_of("lasg", M)
-    K, N = 1152, 384
+# ---------------------------------------------------------------------------
+# backward
+# ---------------------------------------------------------------------------
+
+def backward_case(M, K, N, dt, gdt, act, xf="e4m3fn", wf="e4m3fn", only=True):
+    g = gen_of(M, K, N, act, "b")
+    T, GT = TORCH_HP[dt], TORCH_HP[gdt]
+    xq, xs, wq, ws = operands(g, M, K, N, xf, wf)
+    X, W = x64(xq, xs), w64(wq, ws)
+    dy = (0.05 * rand(g, M, N)).to(T)
+    z = None if act is None else (2 * rand(g, M, N)).to(T)
+    slope = torch.ones(1, dtype=D) if act is None else unary64(act, z.to(D))[1]
+    dz = dy.to(D) * slope
+    # the slope's own binary32 evaluation: a few roundings of max(1, |z|) terms
+    ez = torch.zeros(1, dtype=D) if act in (None, "relu") else dy.to(D).abs() * 2.0 ** -19 * (1 + z.to(D).abs())
+    args = (up(dy), None if z is None else up(z), up(xq), up(xs), up(wq), up(ws))
+    out = (G.empty((M, K), dtype=T), G.empty((N, K), dtype=GT), G.empty(N, dtype=GT))
+    dx, dw, db = fq.linear_act_fp8_backward(*args, act, out=out)
+    a = dz.abs() + ez
+    near(dx, dz @ W, out_tol(dz @ W, dt, bwd_err(a, W.abs(), N + 128) + (ez + 0 * dz) @ W.abs()), "dx")
+    near(dw, dz.t() @ X, out_tol(dz.t() @ X, gdt, bwd_err(a.t(), X.abs(), M + 128) + (ez + 0 * dz).t() @ X.abs()), "dw")
+    # 16 rows and 4 waves of a tile, then M / 64 tiles over 32 lanes
+    depth = 8 + M // 2048 + 6
+    near(db, dz.sum(0), out_tol(dz.sum(0), gdt, a.sum(0) * depth * 2.0 ** -24 + (ez + 0 * dz).sum(0)), "dbias")
+    if not only:
+        return
+    # each alone, with a workspace of just its size between guards: the same bits
+    ws_ = G.empty(fq.fp8q_linear_act_backward_workspace_bytes(M, N, K), dtype=torch.uint8)
+    for i in range(3):
+        o = [torch.empty_like(t) if j == i else None for j, t in enumerate(out)]
+        fq.fp8q_linear_act_backward(*args, *o, act, ws_)
+        assert torch.equal(o[i], out[i]), i
+
+
+@pytest.mark.parametrize("M,K,N", BWD)
+@pytest.mark.parametrize("dt,gdt,act,xf,wf", [("bf16", "bf16", "gelu", "e4m3fn", "e4m3fn"), ("f16", "f16", "silu", "e5m2", "e4m3fn"),
+                                              ("f16", "f32", None, "e4m3fn", "e5m2"), ("bf16", "f32", "relu", "e5m2", "e5m2"),
+                                              ("bf16", "bf16", None, "e4m3fn", "e4m3fn"), ("f16", "f16", "gelu_tanh", "e4m3fn", "e4m3fn")])
+def test_backward(M, K, N, dt, gdt, act, xf, wf):
+    backward_case(M, K, N, dt, gdt, act, xf, wf)
+
+
+@pytest.mark.parametrize("M,K,N", [k[:3] for k in BACKWARD if not k[3]])
+def test_backward_every_tiling(M, K, N):
+    backward_case(M, K, N, "bf16", "f32", "gelu", only=False)
+
+
+@pytest.mark.parametrize("M,K,N", list(BACKWARD_REST))
+def test_backward_every_tiling_with_a_rest(M, K, N):
+    """f16 gradients through an activation: the contraction begins with the
+    rest's steps, whole and split"""
+    backward_case(M, K, N, "f16", "f16", "gelu", only=False)
+
+
+def test_f16_gradients_keep_their_bits():
+    """The rest of dz that f16 leaves goes through the product: in root mean
+    square within 1.5 times the outputs' own rounding (a quarter of 2^-11 over
+    sqrt(3) of f16's smallest step to largest, 2.1e-4)."""
+    g = gen_of("bits")
+    M, K, N = 500, 640, 700
+    xq, xs, wq, ws = operands(g, M, K, N)
+    dy, z = (0.05 * rand(g, M, N)).half(), (2 * rand(g, M, N)).half()
+    X, W = x64(xq, xs), w64(wq, ws)
+    dz = dy.to(D) * unary64("gelu", z.to(D))[1]
+    dx, dw, _ = fq.linear_act_fp8_backward(up(dy), up(z), up(xq), up(xs), up(wq), up(ws), "gelu")
+    for got, want in ((dx, dz @ W), (dw, dz.t() @ X)):
+        assert float((got.cpu().to(D) - want).norm() / want.norm()) < 3.2e-4
+
+
+def test_gradients_against_differences():
+    """sum(dy * act(X W^T + b)) along each gradient, in binary64, by central
+    differences: bf16 gradients, within 2^-8 of their value an element, less in
+    norm; z as the forward pass keeps it."""
+    g = gen_of("lad")
+    M, K, N = 70, 256, 200
+    xq, xs, wq, ws = operands(g, M, K, N)
+    X, W, b = x64(xq, xs), w64(wq, ws), rand(g, N).bfloat16()
+    dy = rand(g, M, N).bfloat16()
+    for act in ("silu", "gelu", "gelu_tanh", None):
+        f = lambda X, W, b: (dy.to(D) * unary64(act, X @ W.t() + b)[0]).sum()
+        _, z = fq.linear_act_fp8(up(xq), up(xs), up(wq), up(ws), up(b), act, keep=torch.bfloat16)
+        grads = fq.linear_act_fp8_backward(up(dy), z, up(xq), up(xs), up(wq), up(ws), act)
+        for i, grad in enumerate(grads):
+            d = grad.cpu().to(D)
+            step = 1e-5 * d / d.norm()
+            at = lambda t: f(*[v.to(D) + (t if j == i else 0) for j, v in enumerate((X, W, b))])
+            slope = (at(step) - at(-step)) / 2e-5
+            assert abs(slope - d.norm()) <= 2.0 ** -6 * d.norm(), (act, i, float(slope), float(d.norm()))
+
+
+@pytest.mark.parametrize("act", [None, "gelu"])
+def test_backward_empty(act):
+    E = torch.float8_e4m3fn
+    e = lambda r, c: torch.zeros(r, c, device="cuda").to(E)
+    f = lambda r, c: torch.zeros(r, c, device="cuda")
+    b = lambda r, c: torch.zeros(r, c, device="cuda", dtype=torch.bfloat16)
+    for gd in (torch.bfloat16, torch.float32):
+        dw, db = G.full((70, 128), 5.0, dtype=gd), G.full((70,), 5.0, dtype=gd)
+        fq.fp8q_linear_act_backward(b(0, 70), b(0, 70), e(0, 128), f(0, 1), e(70, 128), f(1, 1), b(0, 128), dw, db, act)
+        assert (dw == 0).all() and (db == 0).all()
+    dx = G.full((9, 128), 5.0, dtype=torch.bfloat16)
+    fq.fp8q_linear_act_backward(b(9, 0), b(9, 0), e(9, 128), f(9, 1), e(0, 128), f(0, 1), dx, b(0, 128), None, act)
+    assert (dx == 0).all()
+    # no contraction: dbias is still the sum of dz
+    dy, z = rand(gen_of("k0"), 70, 200).bfloat16(), rand(gen_of("k1"), 70, 200).bfloat16()
+    db = G.empty(200, dtype=torch.float32)
+    ws = G.empty(fq.fp8q_linear_act_backward_workspace_bytes(70, 200, 0), dtype=torch.uint8)
+    fq.fp8q_linear_act_backward(up(dy), up(z), e(70, 0), f(70, 0), e(200, 0), f(2, 0), None, None, db, act, ws)
+    dz = dy.to(D) * (1 if act is None else unary64(act, z.to(D))[1])
+    near(db, dz.sum(0), dy.to(D).abs().sum(0) * (2.0 ** -19 * 4 + 2.0 ** -20), "dbias")
+
+
+def test_backward_nan_stays_in_its_row_and_column():
+    g = gen_of("bn")
+    M, K, N = 70, 256, 96
     args = [up(t) for t in operands(g, M, K, N)]
-    b, r = up(rand(g, N)), up(rand(g, M, N).bfloat16())
+    dy, z = (1e-6 * rand(g, M, N)).bfloat16(), rand(g, M, N).bfloat16()
+    for act in (None, "gelu"):
+        keep = dy.clone()
+        keep[5] = 0.0
+        want = fq.linear_act_fp8_backward(up(keep), up(z), *args, act)
+        for bad in (float("nan"), float("inf")):
+            d = keep.clone()
+            d[5, 7] = bad
+            dx, dw, db = fq.linear_act_fp8_backward(up(d), up(z), *args, act)
+            rows, cols = torch.arange(M) != 5, torch.arange(N) != 7
+            assert not torch.isfinite(dx[5]).any() and torch.equal(dx.cpu()[rows], want[0].cpu()[rows])
+            assert not torch.isfinite(dw[7]).all() and torch.equal(dw.cpu()[cols], want[1].cpu()[cols])
+            assert not torch.isfinite(db[7]) and torch.equal(db.cpu()[cols], want[2].cpu()[cols])
+
+
+# ---------------------------------------------------------------------------
+# together, on streams and in graphs
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [1, 40, 200])
+def test_block_on_streams_in_graphs_and_two_at_once(M):
+    """The whole block twice, two at once on two streams, and replayed from a
+    graph with eager calls between: the same bits every time."""
+    g = gen_of("lasg", M)
+    K, N = 512, 384
+    x, r = up(rand(g, M, K).bfloat16()), up(rand(g, M, K).bfloat16())
+    nw, nb, b1, b2 = (up(t.bfloat16()) for t in (1 + 0.1 * rand(g, K), rand(g, K), rand(g, N), rand(g, K)))
+    w1, w2 = [up(t) for t in operands(g, 1, K, N)[2:]], [up(t) for t in operands(g, 1, N, K)[2:]]
+    w1[1] *= 0.05
+    w2[1] *= 0.05
 
     def step():
-        y, z = fq.linear_act_fp8(*args, b, "gelu", r, keep=torch.bfloat16)
-        q, s, _ = fq.linear_act_fp8_cast(*args, b, "silu")
-        return y, z, q, s
+        q, s, h, mean, rstd = fq.layernorm_cast(x, nw, nb, r)
+        p, ps, z = fq.linear_act_fp8_cast(q, s, *w1, b1, "gelu", keep=torch.bfloat16)
+        y, _ = fq.linear_act_fp8(p, ps, *w2, b2, residual=h)
+        dp, dw2, db2 = fq.linear_act_fp8_backward(y, None, p, ps, *w2)
+        dn, dw1, db1 = fq.linear_act_fp8_backward(dp, z, q, s, *w1, "gelu")
+        dx, dnw, dnb = fq.layernorm_backward(dn, h, nw, mean, rstd, y)
+        return q, s, h, mean, rstd, p, ps, z, y, dp, dw2, db2, dn, dw1, db1, dx, dnw, dnb
 
     want = [t.clone() for t in step()]
     same = lambda out: all(torch.equal(a.view(torch.uint8), c.view(torch.uint8)) for a, c in zip(out, want))
+    assert all(torch.isfinite(t.float()).all() for t in want)
     assert same(step())
     torch.cuda.synchronize()
     streams, outs = [torch.cuda.Stream() for _ in range(2)], []
@@ -229,3 +373,18 @@ def test_streams_graphs_and_two_at_once(M):
         torch.cuda.synchronize()
         assert same(out)
         assert same(step())
+
+
+def test_example_block_runs():
+    """examples/mlp_block.py: the operators together, as a training step and a
+    decode step.  Casts to e4m3fn (2^-4 at most, about 2^-5 in root mean square,
+    an element) leave the block's own part of the output within a tenth of its
+    norm."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(fq.__file__), "examples", "mlp_block.py")
+    spec = importlib.util.spec_from_file_location("mlp_block_example", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    err, same = mod.main(200, 512, 640)
+    assert err < 0.1 and same

@@ -165,6 +165,42 @@ def test_linear_act_errors(cast):
     assert L.fp8q_linear_act_workspace_bytes(-1, 128, 128, 0) == 0
 
 
+def _act_bwd(**k):
+    a = dict(dy=at(1), z=at(9), dt=BF16, x=at(2), xf=E4, xs=at(3), w=at(4), wf=E4, wsc=at(5), M=300, N=200, K=256, act=1,
+             dx=at(6), dw=at(7), db=at(10), gdt=BF16, ws=at(8), st=None)
+    a.update(k)
+    return L.fp8q_linear_act_backward(*a.values())
+
+
+def test_linear_act_backward_errors():
+    f = _act_bwd
+    assert f(dt=F32, gdt=F32) == fq.EDTYPE                 # gradients are 16-bit
+    assert f(gdt=F16) == fq.EDTYPE
+    assert f(xf=2) == fq.EDTYPE
+    assert f(act=5) == fq.EDTYPE
+    assert f(K=100) == fq.ESHAPE
+    assert f(M=-1) == fq.EINVAL
+    assert f(M=4194241) == fq.EINVAL
+    assert f(N=2 ** 21 + 1) == fq.EINVAL
+    assert f(N=2 ** 21, K=2 ** 21) == fq.EINVAL
+    for k in ("dy", "z", "x", "xs", "w", "wsc", "ws"):
+        assert f(**{k: None}) == fq.EINVAL, k
+    assert f(x=P(A + 8)) == fq.EALIGN
+    for k in ("dy", "z", "dx", "dw", "db"):
+        assert f(**{k: P(A + 1)}) == fq.EALIGN, k
+    assert f(ws=P(A + 128)) == fq.EALIGN
+    assert f(dx=at(7)) == fq.EINVAL                        # dx = dw
+    assert f(dx=at(1)) == fq.EINVAL
+    assert f(db=at(9)) == fq.EINVAL
+    assert f(db=at(7, 64)) == fq.EINVAL                    # dbias within dw
+    assert f(dx=None, dw=None, db=None) == fq.OK
+    assert f(K=0, db=None) == fq.OK
+    assert f(M=0, dw=None, db=None) == fq.OK
+    assert f(N=0, dx=None) == fq.OK
+    w = L.fp8q_linear_act_backward_workspace_bytes
+    assert w(0, 200, 256) == 0 and w(300, 200, 256) > w(300, 200, 0) > 0 and w(1, 1, 100) == 0
+
+
 def test_python_linear_act_refuses():
     E = torch.float8_e4m3fn
     x, xs = torch.zeros(4, 256).to(E), torch.zeros(4, 2)
@@ -185,6 +221,14 @@ def test_python_linear_act_refuses():
         fq.linear_act_fp8(x, xs, w, ws, residual=torch.zeros(4, 200), out=(torch.zeros(4, 200).half(), None))
     with pytest.raises((ValueError, TypeError)):
         fq.linear_act_fp8_cast(x, xs, w, ws)               # 200 columns are no groups
+    dy = torch.zeros(4, 200).bfloat16()
+    with pytest.raises(ValueError):                        # no z
+        fq.linear_act_fp8_backward(dy, None, x, xs, w, ws, "gelu")
+    with pytest.raises(ValueError):                        # z of another type
+        fq.linear_act_fp8_backward(dy, dy.half(), x, xs, w, ws, "gelu")
+    with pytest.raises(TypeError):                         # weight gradients of two types
+        fq.linear_act_fp8_backward(dy, None, x, xs, w, ws, out=(torch.zeros(4, 256).bfloat16(), torch.zeros(200, 256),
+                                                                torch.zeros(200).bfloat16()))
 
 
 def test_python_layernorm_refuses():
