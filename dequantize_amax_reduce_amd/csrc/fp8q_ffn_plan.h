@@ -152,6 +152,24 @@ inline NormPlan norm_plan(int64_t rows, int64_t nv) {
     return NormPlan{false, 0, 1024, g, g};
 }
 
+// Layer norm: one vector a thread up to 1024 vectors, whose rows' next loads
+// are in flight beside at most 64 registers, so that 32 waves fit a CU (16384 x
+// 7168 bf16: 155 us against 161 with two vectors and half the threads); two
+// vectors up to 2048 (20 waves), four up to 4096 (16; 512 x 32768 bf16 36 us,
+// 43 in passes).  As many workgroups as fit (1999 x 5001 f32: 17.1 us with the two
+// of 10 waves that fit, 18.4 with three).  tiny: rows shorter than a vector.
+inline NormPlan layernorm_plan(int64_t rows, int64_t nv, bool tiny) {
+    if (nv > 4096 || tiny) {
+        const int64_t g = std::min<int64_t>(rows, int64_t(1) << 20);
+        return NormPlan{false, 0, 1024, g, g};
+    }
+    if (nv <= 128 && rows > 256) return norm_plan(rows, nv);
+    const int V = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4, T = threads_for(nv, V);
+    const int64_t fit = std::max(1, (V == 1 ? 32 : V == 2 ? 20 : 16) / (T / 64));
+    const int64_t g = std::min<int64_t>(rows, 256 * fit);
+    return NormPlan{false, V, T, g, g};
+}
+
 inline int64_t norm_bwd_parts(int64_t rows) { return std::min<int64_t>(rows < 1 ? 1 : rows, kBwdParts); }
 inline NormPlan norm_bwd_plan(int64_t rows, int64_t nv) {
     const int64_t g = norm_bwd_parts(rows);

@@ -21,23 +21,49 @@ namespace fp8q {
 
 namespace {
 
-// sums of two values over the lanes of a row, as row_sum; lds: 32 words
-template <bool WAVE> __device__ __forceinline__ void row_sum2(float& a, float& b, float* lds) {
-    a = wave_sum(a);
-    b = wave_sum(b);
-    if constexpr (WAVE) return;
-    const int nw = (int)blockDim.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
-        lds[threadIdx.x >> 6] = a;
-        lds[16 + (threadIdx.x >> 6)] = b;
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// The sum over a wave's lanes, in every lane: within rows of 16 lanes and then
+// across rows by DPP, which needs no LDS access as shuffles do.
+__device__ __forceinline__ float lane_sum(float v) {
+    auto dpp = [](float x, auto ctrl, auto rows) {          // x of another lane; 0 in rows left out
+        return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::value,
+                                                                     decltype(rows)::value, 0xF, false));
+    };
+    v += dpp(v, KC<0xB1>{}, KC<0xF>{});                     // quad_perm [1,0,3,2]
+    v += dpp(v, KC<0x4E>{}, KC<0xF>{});                     // quad_perm [2,3,0,1]
+    v += dpp(v, KC<0x141>{}, KC<0xF>{});                    // row_half_mirror
+    v += dpp(v, KC<0x140>{}, KC<0xF>{});                    // row_mirror
+    v += dpp(v, KC<0x142>{}, KC<0xA>{});                    // row_bcast:15 into rows 1 and 3
+    v += dpp(v, KC<0x143>{}, KC<0xC>{});                    // row_bcast:31 into rows 2 and 3
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// Sums of N values over the lanes of a row: one wave (NW = 0), or a workgroup of
+// up to NW waves through lds, N x NW words of which those of waves that are not
+// there are zero (clear_sums).  The words may be written again after the
+// workgroup's next barrier.
+template <int NW, int N> __device__ __forceinline__ void row_sums(float (&v)[N], float* lds) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lane_sum(v[i]);
+    if constexpr (NW > 0) {
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) lds[i * NW + (threadIdx.x >> 6)] = v[i];
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v4f s = *(const v4f*)(lds + i * NW);
+#pragma unroll
+            for (int j = 4; j < NW; j += 4) s += *(const v4f*)(lds + i * NW + j);
+            v[i] = (s.x + s.y) + (s.z + s.w);
+        }
     }
-    lds_barrier();
-    a = lds[0];
-    b = lds[16];
-    for (int i = 1; i < nw; ++i) {
-        a += lds[i];
-        b += lds[16 + i];
-    }
+}
+// before the first of them, by every thread
+template <int WORDS> __device__ __forceinline__ void clear_sums(float* lds) {
+    for (int i = (int)threadIdx.x; i < WORDS; i += (int)blockDim.x) lds[i] = 0.0f;
+    __syncthreads();
 }
 
 // rstd from the mean of d^2 and that of d (a NaN passes the clamp)
@@ -104,15 +130,19 @@ template <int DT, bool NT> __device__ __forceinline__ void st_at(void* row, int 
 }
 
 // One row per workgroup (or, WAVE, per wave) at a time, V lane vectors a
-// thread.  A workgroup takes several rows, so that weight and bias are read
-// once and the next row's loads are in flight through the reductions and stores
-// of this one (TB, the most threads: up to 512 leave the registers for that).
-// A reduction's LDS words are written again after another reduction's barrier.
-template <int DT, bool WF32, int FMT, int TO, bool WAVE, int V, int TB>
-__global__ void __launch_bounds__(TB) k_ln_rows(LayerNorm a) {
-    constexpr bool PF = TB <= 512, NT = TO == kToGroup;
+// thread.  A workgroup takes several rows, so that the next row's loads are in
+// flight through the reductions and stores of this one, where V and the threads
+// leave registers for that.  WHOLE: rows of whole 128-byte lines, streamed past
+// the caches, and without a mask on every element (16384 x 7168 bf16 with
+// residual and group cast: 155 us with masks, 149 without, 5.5 TB/s; 1999 x 5001
+// f32 17.1 us).  A reduction's LDS words are written again after another
+// reduction's barrier.
+template <int DT, bool WF32, int FMT, int TO, bool WHOLE, bool WAVE, int V, int TB>
+__global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
+    constexpr bool PF = V == 1 || (V == 2 && TB <= 768), NT = WHOLE;
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
-    __shared__ float lds_s[16], lds_d[32];
+    constexpr int NW = WAVE ? 0 : TB / 64;
+    __shared__ __attribute__((aligned(16))) float lds_s[3 * (NW ? NW : 1)];
     __shared__ uint32_t lds_m[16];
     const int cols = (int)a.cols;
     const float fc = (float)cols;
@@ -133,7 +163,8 @@ __global__ void __launch_bounds__(TB) k_ln_rows(LayerNorm a) {
         }
     };
     load(first);
-    constexpr bool HOLD = V <= 2;                           // four vectors leave no registers for them
+    if (NW) clear_sums<3 * NW>(lds_s);
+    constexpr bool HOLD = V <= 1;                           // four vectors leave no registers for them
     Affine<DT, WF32> w[V], b[V];
     auto load_wb = [&](int v) {
         w[v].load(a.w, place(v).c);
@@ -145,7 +176,7 @@ __global__ void __launch_bounds__(TB) k_ln_rows(LayerNorm a) {
         for (int v = 0; v < V; ++v) load_wb(v);
     for (int64_t row = first; row < a.rows; row += next) {
         float h[V][VE];
-        float s = 0.0f;
+        float s[1] = {0.0f};
         // the asm keeps the compiler from holding a mask for every element across the rows
         int dup[V];
 #pragma unroll
@@ -153,29 +184,36 @@ __global__ void __launch_bounds__(TB) k_ln_rows(LayerNorm a) {
             dup[v] = place(v).dup;
             asm volatile("" : "+v"(dup[v]));
             sum_h<DT>(xv[v], rv[v], a.res != nullptr, h[v]);
+            float p = 0.0f;
 #pragma unroll
-            for (int k = 0; k < VE; ++k) s += k >= dup[v] ? h[v][k] : 0.0f;
+            for (int k = 0; k < VE; ++k) p += WHOLE || k >= dup[v] ? h[v][k] : 0.0f;
+            s[0] += WHOLE && dup[v] ? 0.0f : p;
         }
         if (PF && row + next < a.rows) load(row + next);
-        const float m0 = row_sum<WAVE>(s, lds_s) / fc;
+        row_sums<NW>(s, lds_s);
+        const float m0 = s[0] / fc;
         if (a.h) {
             void* hr = (char*)a.h + row * a.cols * ES;
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (place(v).in()) st_at<DT, NT>(hr, place(v).c, h[v]);
         }
-        float s1 = 0.0f, s2 = 0.0f;
+        float d2[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            float p = 0.0f, q = 0.0f;
 #pragma unroll
             for (int k = 0; k < VE; ++k) {
                 h[v][k] -= m0;
-                const float d = k >= dup[v] ? h[v][k] : 0.0f;
-                s1 += d;
-                s2 = __builtin_fmaf(d, d, s2);
+                const float d = WHOLE || k >= dup[v] ? h[v][k] : 0.0f;
+                p += d;
+                q = __builtin_fmaf(d, d, q);
             }
-        row_sum2<WAVE>(s1, s2, lds_d);
-        const float m1 = s1 / fc, rs = rstd_of(s2, m1, fc, a.eps);
+            d2[0] += WHOLE && dup[v] ? 0.0f : p;
+            d2[1] += WHOLE && dup[v] ? 0.0f : q;
+        }
+        row_sums<NW>(d2, lds_s + NW);
+        const float m1 = d2[0] / fc, rs = rstd_of(d2[1], m1, fc, a.eps);
         if (t == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;
@@ -232,40 +270,42 @@ __device__ __forceinline__ void put_y(const LayerNorm& a, int64_t row, int c, co
 // same columns, so that they may be x or the residual itself.
 template <int DT, bool WF32, int FMT, int TO> __global__ void __launch_bounds__(1024) k_ln_long(LayerNorm a) {
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
-    __shared__ float lds_s[16], lds_d[32];
+    __shared__ __attribute__((aligned(16))) float lds_s[48];
     __shared__ uint32_t lds_m[16];
+    clear_sums<48>(lds_s);
     const int cols = (int)a.cols, step = (int)blockDim.x * VE, c0 = (int)threadIdx.x * VE;
     const float fc = (float)cols;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t off = row * a.cols * ES;
         const void* xr = (const char*)a.x + off;
         const void* rr = a.res ? (const char*)a.res + off : nullptr;
-        float s = 0.0f;
+        float s[1] = {0.0f};
         for (int64_t c = c0; c < cols; c += step) {
             float h[VE];
             load_h<DT>(xr, rr, (int)c, cols, h);
 #pragma unroll
-            for (int k = 0; k < VE; ++k) s += h[k];
+            for (int k = 0; k < VE; ++k) s[0] += h[k];
         }
-        const float m0 = row_sum<false>(s, lds_s) / fc;
+        row_sums<16>(s, lds_s);
+        const float m0 = s[0] / fc;
         // d of the columns from c on, zero past the row's end
         auto diff = [&](int64_t c, float* d) {
             load_h<DT>(xr, rr, (int)c, cols, d);
 #pragma unroll
             for (int k = 0; k < VE; ++k) d[k] = c + k < cols ? d[k] - m0 : 0.0f;
         };
-        float s1 = 0.0f, s2 = 0.0f;
+        float d2[2] = {0.0f, 0.0f};
         for (int64_t c = c0; c < cols; c += step) {
             float d[VE];
             diff(c, d);
 #pragma unroll
             for (int k = 0; k < VE; ++k) {
-                s1 += d[k];
-                s2 = __builtin_fmaf(d[k], d[k], s2);
+                d2[0] += d[k];
+                d2[1] = __builtin_fmaf(d[k], d[k], d2[1]);
             }
         }
-        row_sum2<false>(s1, s2, lds_d);
-        const float m1 = s1 / fc, rs = rstd_of(s2, m1, fc, a.eps);
+        row_sums<16>(d2, lds_s + 16);
+        const float m1 = d2[0] / fc, rs = rstd_of(d2[1], m1, fc, a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;
@@ -319,23 +359,28 @@ struct LnBwdArgs {
     float* pb;             // the same of dbias
 };
 
-// dy and h stay as loaded and are widened again after the reduction: that holds
-// half the registers, which the next row's loads take.
+// dy and h stay as loaded and are widened again after the reduction, and the
+// sums over the rows live in LDS, in words that one thread alone touches: that
+// leaves the registers for the next row's loads.  (Sums in registers spilled 30
+// of them: 8192 x 7168 bf16 with dh 148 us; 100 us so, of which 7 are the column
+// sums; 104 with one vector a thread and twice the threads.)
 template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB, 4) k_ln_bwd(LnBwdArgs g) {
     const LayerNormBwd& a = g.f;
     constexpr bool PF = TB <= 512;
-    constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
-    __shared__ float lds[2][32];
+    constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value, Q = VE / 4;
+    extern __shared__ v4f sums[];                           // [2][V][Q][T]: 4 columns each of dweight, then of dbias
+    constexpr int NW = TB / 64;
+    __shared__ __attribute__((aligned(16))) float lds[2][2 * NW];
     const int T = (int)blockDim.x, t = (int)threadIdx.x, cols = (int)a.cols;
     const float fc = (float)cols;
     auto place = [&](int v) { return Place<VE>((v * T + t) * VE, cols); };
+    auto sum = [&](int which, int v, int q) -> v4f& { return sums[((which * V + v) * Q + q) * T + t]; };
     Affine<DT, WF32> w[V];
-    float aw[V][VE], ab[V][VE];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         w[v].load(a.w, place(v).c);
 #pragma unroll
-        for (int k = 0; k < VE; ++k) aw[v][k] = ab[v][k] = 0.0f;
+        for (int q = 0; q < Q; ++q) sum(0, v, q) = sum(1, v, q) = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
     int flip = 0;
     v4u dyr[V], hr[V], dyn[V], hn[V], dhr[V];
@@ -359,6 +404,7 @@ template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB
         for (int k = 0; k < VE; ++k) n[k] = (n[k] - mu) * rs;
     };
     if ((int64_t)blockIdx.x < a.rows) load(blockIdx.x);
+    clear_sums<4 * NW>(lds[0]);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
         const int64_t off = row * a.cols * ES;
         rs = rsn;
@@ -368,7 +414,11 @@ template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB
             dyr[v] = dyn[v];
             hr[v] = hn[v];
         }
-        float s1 = 0.0f, s2 = 0.0f;
+        if (a.dh)
+#pragma unroll
+            for (int v = 0; v < V; ++v) dhr[v] = ld_at<DT, true>((const char*)a.dh + off, place(v).c);
+        if (PF && row + gridDim.x < a.rows) load(row + gridDim.x);   // in flight through the reduction and the stores
+        float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float wv[VE], n[VE], dy[VE];
@@ -377,26 +427,37 @@ template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB
             widen(v, n, dy);
             w[v].widen(wv);
 #pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                if (g.pw) {
+                    v4f& p = sum(0, v, q);
+                    v4f x = p;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = __builtin_fmaf(dy[4 * q + k], n[4 * q + k], x[k]);
+                    p = x;
+                }
+                if (g.pb) {
+                    v4f& p = sum(1, v, q);
+                    v4f x = p;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] += dy[4 * q + k];
+                    p = x;
+                }
+            }
+#pragma unroll
             for (int k = 0; k < VE; ++k) {
-                aw[v][k] = __builtin_fmaf(dy[k], n[k], aw[v][k]);
-                ab[v][k] += dy[k];
                 const float dn = k >= dup ? dy[k] * wv[k] : 0.0f, nk = k >= dup ? n[k] : 0.0f;
-                s1 += dn;
-                s2 = __builtin_fmaf(dn, nk, s2);
+                s[0] += dn;
+                s[1] = __builtin_fmaf(dn, nk, s[1]);
             }
             __builtin_amdgcn_sched_barrier(0);              // one vector widened at a time
         }
-        if (a.dh)
-#pragma unroll
-            for (int v = 0; v < V; ++v) dhr[v] = ld_at<DT, true>((const char*)a.dh + off, place(v).c);
-        if (PF && row + gridDim.x < a.rows) load(row + gridDim.x);   // in flight through the reduction and the stores
         // dx over dh: elements that two lanes hold are loaded by both before either stores them
         // (dy and h have been used, so their loads are done)
         if (a.dx == a.dh)
 #pragma unroll
             for (int v = 0; v < V; ++v) asm volatile("" : "+v"(dhr[v]));
-        row_sum2<false>(s1, s2, lds[flip]);
-        const float m1 = s1 / fc, m2 = s2 / fc;
+        row_sums<NW>(s, lds[flip]);
+        const float m1 = s[0] / fc, m2 = s[1] / fc;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float wv[VE], n[VE], dy[VE], o[VE];
@@ -415,17 +476,20 @@ template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB
         }
         if (!PF && row + gridDim.x < a.rows) load(row + gridDim.x);
     }
-    auto put = [&](float* part, const float (&s)[V][VE]) {
-        if (!part) return;
-        float* p = part + (int64_t)blockIdx.x * a.cols;
+    for (int which = 0; which < 2; ++which) {
+        float* p = which ? g.pb : g.pw;
+        if (!p) continue;
+        p += (int64_t)blockIdx.x * a.cols;
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int k = 0; k < VE; ++k)
-                if (k >= place(v).dup) p[place(v).c + k] = s[v][k];
-    };
-    put(g.pw, aw);
-    put(g.pb, ab);
+            for (int q = 0; q < Q; ++q) {
+                const v4f x = sum(which, v, q);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (4 * q + k >= place(v).dup) p[place(v).c + 4 * q + k] = x[k];
+            }
+    }
 }
 
 // Rows too long for registers, or shorter than a vector: the row is read twice, and the sums over the
@@ -434,7 +498,8 @@ template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB
 template <int DT, bool WF32> __global__ void __launch_bounds__(1024) k_ln_bwd_long(LnBwdArgs g) {
     const LayerNormBwd& a = g.f;
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
-    __shared__ float lds[2][32];
+    __shared__ __attribute__((aligned(16))) float lds[2][32];
+    clear_sums<64>(lds[0]);
     const int cols = (int)a.cols, step = (int)blockDim.x * VE, c0 = (int)threadIdx.x * VE;
     const float fc = (float)cols;
     float* pw = g.pw ? g.pw + (int64_t)blockIdx.x * a.cols : nullptr;
@@ -456,20 +521,20 @@ template <int DT, bool WF32> __global__ void __launch_bounds__(1024) k_ln_bwd_lo
 #pragma unroll
             for (int k = 0; k < VE; ++k) n[k] = (n[k] - mu) * rs;
         };
-        float s1 = 0.0f, s2 = 0.0f;
+        float s[2] = {0.0f, 0.0f};
         for (int64_t c = c0; c < cols; c += step) {
             float dy[VE], w[VE], n[VE];
             load(c, dy, w, n);
 #pragma unroll
             for (int k = 0; k < VE; ++k) {
-                s1 += dy[k] * w[k];
-                s2 = __builtin_fmaf(dy[k] * w[k], n[k], s2);
+                s[0] += dy[k] * w[k];
+                s[1] = __builtin_fmaf(dy[k] * w[k], n[k], s[1]);
                 if (pw && c + k < cols) pw[c + k] = __builtin_fmaf(dy[k], n[k], pw[c + k]);
                 if (pb && c + k < cols) pb[c + k] += dy[k];
             }
         }
-        row_sum2<false>(s1, s2, lds[flip]);
-        const float m1 = s1 / fc, m2 = s2 / fc;
+        row_sums<16>(s, lds[flip]);
+        const float m1 = s[0] / fc, m2 = s[1] / fc;
         for (int64_t c = c0; c < cols; c += step) {
             float dy[VE], w[VE], n[VE], o[VE];
             load(c, dy, w, n);
@@ -500,6 +565,7 @@ template <int DT> __global__ void __launch_bounds__(1024) k_column_sums(const fl
         const int64_t c = c0 + cl;
         float s = 0.0f;
         if (c < cols)
+#pragma unroll 8
             for (int64_t p = rl; p < parts; p += 32) s += part[p * cols + c];
         lds[rl][cl] = s;
         __syncthreads();
@@ -511,26 +577,32 @@ template <int DT> __global__ void __launch_bounds__(1024) k_column_sums(const fl
     }
 }
 
-template <int DT, bool WF, int FMT, int TO> void ln_rows(const LayerNorm& a, hipStream_t st) {
-    constexpr int VE = LaneVE<DT>::value;
-    const NormPlan p = norm_plan(a.rows, (a.cols + VE - 1) / VE);
+template <int DT, bool WF, int FMT, int TO, bool WHOLE> void ln_rows(const LayerNorm& a, const NormPlan& p, hipStream_t st) {
     const unsigned g = (unsigned)p.groups;
     const int T = p.threads;
-    if (p.V == 0 || a.cols < VE) k_ln_long<DT, WF, FMT, TO><<<g, T, 0, st>>>(a);
-    else if (p.wave && p.V == 1) k_ln_rows<DT, WF, FMT, TO, true, 1, 256><<<g, T, 0, st>>>(a);
-    else if (p.wave) k_ln_rows<DT, WF, FMT, TO, true, 2, 256><<<g, T, 0, st>>>(a);
-    else if (p.V == 1) k_ln_rows<DT, WF, FMT, TO, false, 1, 256><<<g, T, 0, st>>>(a);
-    else if (p.V == 2 && T <= 512) k_ln_rows<DT, WF, FMT, TO, false, 2, 512><<<g, T, 0, st>>>(a);
-    else if (p.V == 2) k_ln_rows<DT, WF, FMT, TO, false, 2, 1024><<<g, T, 0, st>>>(a);
-    else k_ln_rows<DT, WF, FMT, TO, false, 4, 1024><<<g, T, 0, st>>>(a);
+    if (p.wave && p.V == 1) k_ln_rows<DT, WF, FMT, TO, WHOLE, true, 1, 256><<<g, T, 0, st>>>(a);
+    else if (p.wave) k_ln_rows<DT, WF, FMT, TO, WHOLE, true, 2, 256><<<g, T, 0, st>>>(a);
+    else if (p.V == 1 && T <= 256) k_ln_rows<DT, WF, FMT, TO, WHOLE, false, 1, 256><<<g, T, 0, st>>>(a);
+    else if (p.V == 1) k_ln_rows<DT, WF, FMT, TO, WHOLE, false, 1, 1024><<<g, T, 0, st>>>(a);
+    else if (p.V == 2 && T <= 768) k_ln_rows<DT, WF, FMT, TO, WHOLE, false, 2, 768><<<g, T, 0, st>>>(a);
+    else if (p.V == 2) k_ln_rows<DT, WF, FMT, TO, WHOLE, false, 2, 1024><<<g, T, 0, st>>>(a);
+    else k_ln_rows<DT, WF, FMT, TO, WHOLE, false, 4, 1024><<<g, T, 0, st>>>(a);
 }
 
 template <int DT, bool WF> void ln_to(const LayerNorm& a, hipStream_t st) {
-    if (a.to == kToPlain) return ln_rows<DT, WF, kE4M3, kToPlain>(a, st);
+    constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
+    const NormPlan p = layernorm_plan(a.rows, (a.cols + VE - 1) / VE, a.cols < VE);
+    const bool whole = a.cols * ES % 128 == 0;
+    auto run = [&](auto F, auto TOc) {
+        constexpr int FMT = decltype(F)::value ? kE5M2 : kE4M3, TO = decltype(TOc)::value;
+        if (p.V == 0) k_ln_long<DT, WF, FMT, TO><<<(unsigned)p.groups, p.threads, 0, st>>>(a);
+        else if (TO == kToGroup || whole) ln_rows<DT, WF, FMT, TO, true>(a, p, st);
+        else if constexpr (TO != kToGroup) ln_rows<DT, WF, FMT, TO, false>(a, p, st);
+    };
+    if (a.to == kToPlain) return run(std::false_type{}, KC<kToPlain>{});
     with_bool(a.fmt == kE5M2, [&](auto F) {
-        constexpr int FMT = decltype(F)::value ? kE5M2 : kE4M3;
-        if (a.to == kToGroup) ln_rows<DT, WF, FMT, kToGroup>(a, st);
-        else ln_rows<DT, WF, FMT, kToRow>(a, st);
+        if (a.to == kToGroup) run(F, KC<kToGroup>{});
+        else run(F, KC<kToRow>{});
     });
 }
 
@@ -539,10 +611,11 @@ template <int DT, bool WF> void ln_bwd(const LnBwdArgs& a, hipStream_t st) {
     const NormPlan p = norm_bwd_plan(a.f.rows, (a.f.cols + VE - 1) / VE);
     const unsigned g = (unsigned)p.groups;
     const int T = p.threads;
+    const unsigned lds = (unsigned)(2 * p.V * VE * T * 4);  // the sums: at most 128 KB
     if (p.V == 0 || a.f.cols < VE) k_ln_bwd_long<DT, WF><<<g, T, 0, st>>>(a);
-    else if (p.V == 1) k_ln_bwd<DT, WF, 1, 256><<<g, T, 0, st>>>(a);
-    else if (T <= 512) k_ln_bwd<DT, WF, 2, 512><<<g, T, 0, st>>>(a);
-    else k_ln_bwd<DT, WF, 2, 1024><<<g, T, 0, st>>>(a);
+    else if (p.V == 1) k_ln_bwd<DT, WF, 1, 256><<<g, T, lds, st>>>(a);
+    else if (T <= 512) k_ln_bwd<DT, WF, 2, 512><<<g, T, lds, st>>>(a);
+    else k_ln_bwd<DT, WF, 2, 1024><<<g, T, lds, st>>>(a);
 }
 
 // go(DT, WF32) over the types of the activations and of the weight

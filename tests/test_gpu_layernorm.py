@@ -14,6 +14,7 @@ import torch
 
 import dequantize_amax_reduce_amd as fq
 from gpu_util import G, TORCH_HP
+from mlp_plans import LAYERNORM
 from test_gpu_ffn import D, FP8, HALF_ULP, TINY, cast_close, gen_of, near, out_tol, rand, up
 
 pytestmark = pytest.mark.gpu
@@ -118,6 +119,14 @@ def test_cast_per_row(rows, cols, dt, res, fmt, wf32, bias):
 @pytest.mark.parametrize("wf32,bias", [(True, True), (False, True), (False, False)])
 def test_plain(rows, cols, dt, res, wf32, bias):
     forward_case(rows, cols, dt, res, bias, "plain", "e4m3fn", wf32)
+
+
+@pytest.mark.parametrize("rows,cols,dt", list(LAYERNORM))
+@pytest.mark.parametrize("wf32", [False, True])
+def test_every_variant(rows, cols, dt, wf32):
+    """each kernel past the rows its grid takes at once"""
+    for to in ("plain", "row") + (("group",) if cols % 128 == 0 else ()):
+        forward_case(rows, cols, dt, rows % 200 == 0, True, to, "e5m2", wf32)
 
 
 @pytest.mark.parametrize("cols", [200, 4099, 20000, 33333])

@@ -1,11 +1,12 @@
 """CPU: the sizes of tests/mlp_plans.py reach the kernels they are meant to, and
-together every variant of the products that begin with the rest's steps."""
+together every variant of layer norm and of the products that begin with the
+rest's steps."""
 import shutil
 
 import pytest
 
 from ffn_plans import Plans
-from mlp_plans import BACKWARD_REST
+from mlp_plans import BACKWARD_REST, LAYERNORM, LayerNormPlan
 
 
 @pytest.fixture(scope="module")
@@ -31,3 +32,27 @@ def test_every_variant_is_reached():
                 first, end = i * kper, min((i + 1) * kper, C // 64 + C // 128)
                 kinds.add("rest" if end <= C // 128 else "f16" if first >= C // 128 else "both")
     assert kinds == {"rest", "both", "f16"}
+
+
+def test_layernorm_variants(plans, tmp_path):
+    plan = LayerNormPlan(tmp_path)
+    for key, want in LAYERNORM.items():
+        assert plan(*key) == want, key
+        assert key[0] > want[3], key                       # more rows than the grid takes at once
+    # wave or workgroup, vectors, size of the workgroup, and rows of whole lines or not
+    kind = lambda k, p: (p[0], p[1], p[2] > (256 if p[1] == 1 else 768), k[1] * (4 if k[2] == "f32" else 2) % 128 == 0)
+    got = {kind(k, p) for k, p in LAYERNORM.items()}
+    assert got == {(w, v, big, whole) for whole in (False, True)
+                   for w, v, big in ((True, 1, False), (True, 2, False), (False, 1, False), (False, 1, True),
+                                     (False, 2, False), (False, 2, True), (False, 4, big4(whole)))}
+    assert plan(10, 3, "f32")[1] == 0 and plan(10, 7, "bf16")[1] == 0 and plan(10, 40000, "bf16")[1] == 0
+    # never more vectors than its threads hold
+    for nv in range(1, 4097):
+        for rows in (1, 300):
+            _, v, t, _ = plan(rows, nv * 8, "bf16")
+            assert (v * (64 if plan(rows, nv * 8, "bf16")[0] else t)) >= nv, (rows, nv)
+
+
+def big4(whole):
+    """the two sizes of four vectors a thread: 1024 threads and 576"""
+    return whole
