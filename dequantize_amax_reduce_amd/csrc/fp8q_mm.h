@@ -260,10 +260,81 @@ template <int ACT> __device__ __forceinline__ float gated_value(float g, float u
     return r.a * u * r.e;
 }
 
-// act(g)
-template <int ACT> __device__ __forceinline__ float unary_value(float g) {
-    const Act r = act_at<ACT, false>(g);
-    return r.a * r.e;
+// The activations of a projection without a gate.  GELU is evaluated many times
+// an output tile and so has a form of its own, of 20 instructions and two
+// transcendental ones without a branch (erfc and exp above are over 100: 4096 x
+// 18432 values in an epilogue took 65 us more):
+//   Phi(-x) = exp(-x^2 / 2) R(x),  R(x) = erfcx(x / sqrt 2) / 2 for x = |z|,
+// where R = t P(t) with t = 1 / (1 + 0.27 x), P the polynomial of degree 8 of
+// least relative error over 0 <= x <= 20 (2.5e-8; beyond, exp is 0).  exp is a
+// square, multiplied in two steps, so that a gradient times a slope is lost only
+// where it leaves binary32 itself.  exp's argument has one rounding, which costs
+// x^2 2^-25 of the value: what z's own last bit moves it by.
+struct Gelu {
+    float x, r, e;         // x = |z| (at most 40), R(x), exp(-x^2 / 4)
+    __device__ __forceinline__ explicit Gelu(float z) {
+        x = fabsf(z) > 40.0f ? 40.0f : fabsf(z);            // a NaN passes
+        const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.27f, x, 1.0f));
+        float p = 0.029064410970260385f;
+        p = __builtin_fmaf(p, t, -0.12700376572081296f);
+        p = __builtin_fmaf(p, t, 0.1708924787429539f);
+        p = __builtin_fmaf(p, t, -0.07052281498096842f);
+        p = __builtin_fmaf(p, t, 0.10876799243307479f);
+        p = __builtin_fmaf(p, t, 0.07163105169286166f);
+        p = __builtin_fmaf(p, t, 0.10192255230202073f);
+        p = __builtin_fmaf(p, t, 0.10752643850546949f);
+        p = __builtin_fmaf(p, t, 0.10772166824843142f);
+        r = t * p;
+        e = __builtin_amdgcn_exp2f(x * x * -0.36067376022224085f);
+    }
+};
+
+// act(z)
+template <int ACT> __device__ __forceinline__ float unary_value(float z) {
+    if constexpr (ACT == kGelu) {
+        const Gelu g(z);
+        return (z < 0.0f ? 0.0f : z) - g.x * g.r * g.e * g.e;
+    } else {
+        const Act r = act_at<ACT, false>(z);
+        return r.a * r.e;
+    }
+}
+
+// dy act'(z)
+template <int ACT> __device__ __forceinline__ float unary_grad(float dy, float z) {
+    if constexpr (ACT == kGelu) {
+        const Gelu g(z);
+        const float q = (0.39894228040143268f * g.x - g.r) * g.e;   // x phi(x) - Phi(-x), over e
+        return z < 0.0f ? dy * -q * g.e : dy * __builtin_fmaf(q, g.e, 1.0f);
+    } else {
+        const Act r = act_at<ACT, true>(z);
+        return dy * r.d * r.e;
+    }
+}
+
+// A bound on |dy act'(z)|, for its exponent: from 0 up a constant above the
+// slope's maximum (1.129 at most); below, what multiplies exp there: (1 + |z|)
+// e^z of SiLU, e^w (1 + |z| w') of the tanh form, and max(1/2, 0.4 |z|) exp(-z^2 / 2)
+// of GELU.  It exceeds the value by no more than a few binary orders but near a
+// slope's zero, which costs nothing: f16 has 29 of them with all its bits.
+template <int ACT> __device__ __forceinline__ float unary_bound(float dy, float z) {
+    if constexpr (ACT == kIdentity) return dy;
+    if constexpr (ACT == kRelu) return z <= 0.0f ? 0.0f : dy;
+    const float x = z < -64.0f ? 64.0f : -z;
+    float c, y;                                             // z < 0: c e^(2 y), x = -z
+    if constexpr (ACT == kGelu) {
+        c = fmaxf(0.5f, 0.4f * x);
+        y = -0.25f * x * x;
+    } else if constexpr (ACT == kGeluTanh) {
+        const float k = 1.5957691216057308f;
+        c = 1.0f + x * k * (1.0f + 0.134145f * x * x);
+        y = -0.5f * k * (x + 0.044715f * x * x * x);
+    } else {
+        c = 1.0f + x;
+        y = -0.5f * x;
+    }
+    const float e = fmaxf(__expf(y), 0x1p-126f);            // __expf has no subnormal values
+    return z < 0.0f ? dy * c * e * e : z >= 0.0f ? 1.14f * dy : z;
 }
 
 // f(integral_constant) over a runtime activation; with_unary: those of a

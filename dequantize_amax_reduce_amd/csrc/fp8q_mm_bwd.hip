@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(256) k_scales(ScaleArgs a) {
 }
 
 // 8 columns of dg (dz without a gate) and du from column c of row m < M;
-// zero from column N on (FULL: there are none); QUICK as in act_at
+// zero from column N on (FULL: there are none); QUICK, for exponents: as in
+// act_at, and without a gate bounds in place of the values
 template <int DT, int MODE, bool FULL, bool QUICK>
 __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z, int64_t m, int c, int N, int act,
                                           float* g, float* u) {
@@ -367,8 +368,8 @@ __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z,
         with_unary(act, [&](auto A) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const Act r = act_at<decltype(A)::value, true, QUICK>(zv[k]);
-                g[k] = FULL || c + k < N ? g[k] * r.d * r.e : 0.0f;
+                const float d = QUICK ? unary_bound<decltype(A)::value>(g[k], zv[k]) : unary_grad<decltype(A)::value>(g[k], zv[k]);
+                g[k] = FULL || c + k < N ? d : 0.0f;
             }
         });
     }
@@ -389,6 +390,8 @@ __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z,
 }
 
 // The keys of dz's rows and columns, and of X' and W' per 128 columns of K.
+// (4096 x 18432 bf16 through GELU: 157 us with the slope itself, whose erfc and exp
+// bound it, and 58 with a bound on it.)
 // Workgroups [0, e0) take 128 x 128 of dz, 16 lanes a row and 8 columns a lane;
 // [e0, e1) 32 rows of X's scales, the rest as many block rows of W's.  The
 // maxima of integers do not depend on the order of the atomics.  A key of dz is of
