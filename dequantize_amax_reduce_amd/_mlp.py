@@ -19,7 +19,7 @@ import re
 import torch
 
 from . import _ffn
-from ._ffn import _AUTO, _CODES, _f32, _flat, _formats, _hp_dtype, _opt, _ptr, _same, _stream, _w_codes, _ws, _x_codes
+from ._ffn import _AUTO, _CODES, _flat, _formats, _hp_dtype, _raw_stream, _same, _ws
 
 MLP_HEADER_PATH = os.path.join(os.path.dirname(_ffn.FFN_HEADER_PATH), "fp8q_mlp.h")
 
@@ -59,33 +59,57 @@ def mlp_header_functions() -> list:
 
 
 # set by the package once its own marshalling helpers exist
-lib = _check = _fmt = _fp8 = _FP8_DTYPE = None
+lib = _check = _dev = _fmt = _fp8 = _FP8_DTYPE = None
 
 
 def _bind(package_lib, helpers):
     global lib
     lib = load_mlp(package_lib)
-    globals().update({k: helpers[k] for k in ("_check", "_fmt", "_fp8", "_FP8_DTYPE")})
+    globals().update(helpers)
+
+
+# As in _ffn.py, a call on one token is bound by its host time.  `d` is the
+# device of the call's first tensor (-1: the host), which every tensor has to be on.
+
+def _at(t, name, d) -> int:
+    """the address of a contiguous tensor on device d (0 of an empty one)"""
+    try:
+        if t.get_device() == d and d >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _dev(t, name)                                   # raises, or 0 for an empty tensor
+    if p and t.get_device() != d:
+        raise ValueError(f"{name} is on another device than the other tensors")
+    return p
+
+
+def _opt(t, name, d) -> int:
+    return 0 if t is None else _at(t, name, d)
+
+
+def _f32(t, numel, name, d) -> int:
+    if t.dtype != torch.float32 or t.numel() != numel:
+        raise ValueError(f"{name} must be float32 with {numel} elements")
+    return _at(t, name, d)
+
+
+def _stream(stream, d):
+    if stream is None:
+        return _raw_stream(d) if d >= 0 else None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 _current = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-def _call(name, like, tensors, *args):
-    """The C call on `like`'s device (every tensor's), which a launch needs as
-    the thread's current one."""
-    if like.is_cuda:
-        d = like.get_device()
-        for t in tensors:
-            if t is not None and t.get_device() != d:
-                raise ValueError(f"{name}: tensors on different devices")
-        if d != _current():
-            with torch.cuda.device(d):
-                st = getattr(lib, name)(*args)
-                if st:
-                    _check(st, name)
-                return
-    st = getattr(lib, name)(*args)
+def _call(name, d, *args):
+    """The C call with device d as the thread's current one, which a launch needs."""
+    if d >= 0 and d != _current():
+        with torch.cuda.device(d):
+            st = getattr(lib, name)(*args)
+    else:
+        st = getattr(lib, name)(*args)
     if st:
         _check(st, name)
 
@@ -94,34 +118,29 @@ def _call(name, like, tensors, *args):
 # one function per C entry point
 # ---------------------------------------------------------------------------
 
-def _affine(name, x, weight, bias, dtype_of):
-    cols = x.shape[-1]
+def _norm(name, x, weight, bias, y, scale_inv, residual, h, mean, rstd, eps, fmt, stream):
+    rows, cols = shape = _flat(x, "x")
+    dt, wdt, d = _hp_dtype(x, "x"), _hp_dtype(weight, "weight"), x.get_device()
     if weight.numel() != cols:
-        raise ValueError(f"{name}: weight must have {dtype_of}'s last dimension")
+        raise ValueError(f"{name}: weight must have x's last dimension")
     if bias is not None and (bias.numel() != cols or bias.dtype != weight.dtype):
         raise ValueError(f"{name}: bias must match weight")
-
-
-def _norm(name, x, weight, bias, y, scale_inv, residual, h, mean, rstd, eps, fmt, stream):
-    rows, cols = _flat(x, "x")
-    dt = _hp_dtype(x, "x")
-    _affine(name, x, weight, bias, "x")
-    _same(residual, (rows, cols), x.dtype, "residual")
-    _same(h, (rows, cols), x.dtype, "h")
-    out = []
+    if residual is not None:
+        _same(residual, shape, x.dtype, "residual")
+    if h is not None:
+        _same(h, shape, x.dtype, "h")
     if name == "fp8q_layernorm":
-        _same(y, (rows, cols), x.dtype, "y")
-        out = [_ptr(y, "y")]
+        _same(y, shape, x.dtype, "y")
+        out = (_at(y, "y", d),)
     else:
         f = _fp8(y, fmt, "q")
         if y.numel() != rows * cols:
             raise ValueError(f"{name}: q must match x")
         scales = rows if name == "fp8q_layernorm_cast_per_channel" else rows * (cols // 128)
-        out = [f, _ptr(y, "q"), _f32(scale_inv, scales, "scale_inv")]
-    _call(name, x, (weight, bias, y, scale_inv, residual, h, mean, rstd), _ptr(x, "x"), dt, _opt(residual, "residual"),
-          _ptr(weight, "weight"), _opt(bias, "bias"), _hp_dtype(weight, "weight"), rows, cols, eps, *out, _opt(h, "h"),
-          0 if mean is None else _f32(mean, rows, "mean"), 0 if rstd is None else _f32(rstd, rows, "rstd"),
-          _stream(x, stream))
+        out = (f, _at(y, "q", d), _f32(scale_inv, scales, "scale_inv", d))
+    _call(name, d, _at(x, "x", d), dt, _opt(residual, "residual", d), _at(weight, "weight", d), _opt(bias, "bias", d), wdt,
+          rows, cols, eps, *out, _opt(h, "h", d), 0 if mean is None else _f32(mean, rows, "mean", d),
+          0 if rstd is None else _f32(rstd, rows, "rstd", d), _stream(stream, d))
 
 
 def fp8q_layernorm(x, weight, bias, y, residual=None, h=None, mean=None, rstd=None, eps=1e-5, stream=None) -> None:
@@ -145,20 +164,20 @@ def fp8q_layernorm_backward_workspace_bytes(rows: int, cols: int) -> int:
 def fp8q_layernorm_backward(dy, h, weight, mean, rstd, dx, dweight=None, dbias=None, dh=None, workspace=None,
                             stream=None) -> None:
     name = "fp8q_layernorm_backward"
-    rows, cols = _flat(h, "h")
-    dt = _hp_dtype(h, "h")
+    rows, cols = shape = _flat(h, "h")
+    dt, wdt, d = _hp_dtype(h, "h"), _hp_dtype(weight, "weight"), h.get_device()
     for t, n in ((dy, "dy"), (dx, "dx"), (dh, "dh")):
-        _same(t, (rows, cols), h.dtype, n)
-    _affine(name, h, weight, None, "h")
+        _same(t, shape, h.dtype, n)
+    if weight.numel() != cols:
+        raise ValueError(f"{name}: weight must have h's last dimension")
     for t, n in ((dweight, "dweight"), (dbias, "dbias")):
         if t is not None and (t.numel() != cols or t.dtype != weight.dtype):
             raise ValueError(f"{name}: {n} must match weight")
     need = lib.fp8q_layernorm_backward_workspace_bytes(rows, cols) if dweight is not None or dbias is not None else 0
     ws = _ws(workspace, need, h, name)
-    _call(name, h, (dy, weight, mean, rstd, dx, dweight, dbias, dh, ws), _ptr(dy, "dy"), _ptr(h, "h"), dt,
-          _ptr(weight, "weight"), _hp_dtype(weight, "weight"), _f32(mean, rows, "mean"), _f32(rstd, rows, "rstd"),
-          _opt(dh, "dh"), rows, cols, _ptr(dx, "dx"), _opt(dweight, "dweight"), _opt(dbias, "dbias"),
-          _opt(ws, "workspace"), _stream(h, stream))
+    _call(name, d, _at(dy, "dy", d), _at(h, "h", d), dt, _at(weight, "weight", d), wdt, _f32(mean, rows, "mean", d),
+          _f32(rstd, rows, "rstd", d), _opt(dh, "dh", d), rows, cols, _at(dx, "dx", d), _opt(dweight, "dweight", d),
+          _opt(dbias, "dbias", d), _opt(ws, "workspace", d), _stream(stream, d))
 
 
 def _activation(name) -> int:
@@ -167,23 +186,32 @@ def _activation(name) -> int:
     return _ACT[name]
 
 
-def _typed(t, shape, name):
+def _typed(t, shape, name, d):
     """pointer and type of an optional [M, N] tensor of any element type"""
     if t is None:
         return 0, 0
     _same(t, shape, t.dtype, name)
-    return _ptr(t, name), _hp_dtype(t, name)
+    return _at(t, name, d), _hp_dtype(t, name)
 
 
-def _projection(name, x, xs, w, ws, bias, x_fmt, w_fmt):
-    """the arguments that the entry points have in common, M, N, K"""
+def _codes(x, xs, w, ws, x_fmt, w_fmt):
+    """the operands' arguments with the sizes, and M, N, K and the device"""
     xf, wf = _formats(x, x_fmt, w_fmt, w)
-    xa, M, K = _x_codes(x, xs, xf)
-    wp, wsp, N = _w_codes(w, ws, K, "w")
-    if bias is not None and bias.numel() != N:
+    M, K = _flat(x, "x")
+    d = x.get_device()
+    if w.dim() != 2 or w.shape[1] != K:
+        raise ValueError(f"w must be 2-D with {K} columns")
+    N, KB = w.shape[0], K // 128
+    return (_at(x, "x", d), xf, _f32(xs, M * KB, "x_scale_inv", d), _at(w, "w", d), wf,
+            _f32(ws, ((N + 127) // 128) * KB, "the weight's scale_inv", d), M, N, K), M, N, K, d
+
+
+def _bias(name, bias, N, d):
+    if bias is None:
+        return 0, 0
+    if bias.numel() != N:
         raise ValueError(f"{name}: bias must have w's rows")
-    b = (0, 0) if bias is None else (_ptr(bias, "bias"), _hp_dtype(bias, "bias"))
-    return (*xa, wp, wf, wsp, M, N, K, *b), M, N, K
+    return _at(bias, "bias", d), _hp_dtype(bias, "bias")
 
 
 def fp8q_linear_act_workspace_bytes(M: int, N: int, K: int, cast: bool) -> int:
@@ -194,26 +222,27 @@ def fp8q_linear_act(x, x_scale_inv, w, w_scale_inv, bias, y, residual=None, z=No
                     stream=None, x_fmt=None, w_fmt=None) -> None:
     name = "fp8q_linear_act"
     act = _activation(activation)
-    args, M, N, K = _projection(name, x, x_scale_inv, w, w_scale_inv, bias, x_fmt, w_fmt)
-    _same(residual, (M, N), y.dtype, "residual")
+    args, M, N, K, d = _codes(x, x_scale_inv, w, w_scale_inv, x_fmt, w_fmt)
+    if residual is not None:
+        _same(residual, (M, N), y.dtype, "residual")
     scratch = _ws(workspace, lib.fp8q_linear_act_workspace_bytes(M, N, K, 0), x, name)
-    _call(name, x, (x_scale_inv, w, w_scale_inv, bias, residual, y, z, scratch), *args, act, _opt(residual, "residual"),
-          *_typed(y, (M, N), "y"), *_typed(z, (M, N), "z"), _opt(scratch, "workspace"), _stream(x, stream))
+    _call(name, d, *args, *_bias(name, bias, N, d), act, _opt(residual, "residual", d), *_typed(y, (M, N), "y", d),
+          *_typed(z, (M, N), "z", d), _opt(scratch, "workspace", d), _stream(stream, d))
 
 
 def fp8q_linear_act_cast(x, x_scale_inv, w, w_scale_inv, bias, q, scale_inv, z=None, activation=None, fmt=None,
                          workspace=None, stream=None, x_fmt=None, w_fmt=None) -> None:
     name = "fp8q_linear_act_cast"
     act = _activation(activation)
-    args, M, N, K = _projection(name, x, x_scale_inv, w, w_scale_inv, bias, x_fmt, w_fmt)
+    args, M, N, K, d = _codes(x, x_scale_inv, w, w_scale_inv, x_fmt, w_fmt)
     f = _fp8(q, fmt, "q")
     if q.numel() != M * N:
         raise ValueError(f"{name}: q must have M x N elements")
-    if N % 128 == 0:
-        _f32(scale_inv, M * (N // 128), "scale_inv")
+    if N % 128 == 0 and (scale_inv.dtype != torch.float32 or scale_inv.numel() != M * (N // 128)):
+        raise ValueError(f"scale_inv must be float32 with {M * (N // 128)} elements")
     scratch = _ws(workspace, lib.fp8q_linear_act_workspace_bytes(M, N, K, 1), x, name)
-    _call(name, x, (x_scale_inv, w, w_scale_inv, bias, q, scale_inv, z, scratch), *args, act, f, _ptr(q, "q"),
-          _ptr(scale_inv, "scale_inv"), *_typed(z, (M, N), "z"), _opt(scratch, "workspace"), _stream(x, stream))
+    _call(name, d, *args, *_bias(name, bias, N, d), act, f, _at(q, "q", d), _at(scale_inv, "scale_inv", d),
+          *_typed(z, (M, N), "z", d), _opt(scratch, "workspace", d), _stream(stream, d))
 
 
 def fp8q_linear_act_backward_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -224,9 +253,7 @@ def fp8q_linear_act_backward(dy, z, x, x_scale_inv, w, w_scale_inv, dx=None, dw=
                              workspace=None, stream=None, x_fmt=None, w_fmt=None) -> None:
     name = "fp8q_linear_act_backward"
     act, g = _activation(activation), _ffn._grad_dtype((dw, dbias))
-    xf, wf = _formats(x, x_fmt, w_fmt, w)
-    xa, M, K = _x_codes(x, x_scale_inv, xf)
-    wp, wsp, N = _w_codes(w, w_scale_inv, K, "w")
+    args, M, N, K, d = _codes(x, x_scale_inv, w, w_scale_inv, x_fmt, w_fmt)
     dt = _hp_dtype(dy, "dy")
     _same(dy, (M, N), dy.dtype, "dy")
     _same(dx, (M, K), dy.dtype, "dx")
@@ -241,9 +268,8 @@ def fp8q_linear_act_backward(dy, z, x, x_scale_inv, w, w_scale_inv, dx=None, dw=
         raise ValueError(f"{name}: dbias must have w's rows")
     gdt = dt if g is None else _hp_dtype(dw if dw is not None else dbias, "dw")
     scratch = _ws(workspace, lib.fp8q_linear_act_backward_workspace_bytes(M, N, K), x, name)
-    _call(name, x, (dy, z, x_scale_inv, w, w_scale_inv, dx, dw, dbias, scratch), _ptr(dy, "dy"), _opt(z, "z"), dt, *xa, wp,
-          wf, wsp, M, N, K, act, _opt(dx, "dx"), _opt(dw, "dw"), _opt(dbias, "dbias"), gdt, _opt(scratch, "workspace"),
-          _stream(x, stream))
+    _call(name, d, _at(dy, "dy", d), _opt(z, "z", d), dt, *args, act, _opt(dx, "dx", d), _opt(dw, "dw", d),
+          _opt(dbias, "dbias", d), gdt, _opt(scratch, "workspace", d), _stream(stream, d))
 
 
 # ---------------------------------------------------------------------------

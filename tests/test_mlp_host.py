@@ -264,13 +264,17 @@ def test_calls_run_on_the_tensors_device(monkeypatch):
     from dequantize_amax_reduce_amd import _mlp
 
     class T:
-        is_cuda = True
-
         def __init__(self, d):
             self.d = d
 
         def get_device(self):
             return self.d
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 7
 
     log = []
 
@@ -293,13 +297,15 @@ def test_calls_run_on_the_tensors_device(monkeypatch):
     monkeypatch.setattr(_mlp, "_current", lambda: 0)
     monkeypatch.setattr(torch.cuda, "device", Dev)
     monkeypatch.setattr(_mlp, "lib", Lib)
-    _mlp._call("f", T(0), (T(0), None), 1)
+    monkeypatch.setattr(_mlp, "_dev", lambda t, name: t.data_ptr())
+    _mlp._call("f", 0, 1)
     assert log == [(1,)]
     log.clear()
-    _mlp._call("f", T(1), (T(1),), 2)
+    _mlp._call("f", 1, 2)
     assert log == [("enter", 1), (2,), ("exit", 1)]
+    assert _mlp._at(T(1), "t", 1) == 7
     with pytest.raises(ValueError):
-        _mlp._call("f", T(0), (T(1),), 3)
+        _mlp._at(T(1), "t", 0)
 
 
 @pytest.mark.skipif(not STUBS, reason="needs the launcher-stub build of the ABI layer (test_mlp_abi_under_asan_ubsan)")
