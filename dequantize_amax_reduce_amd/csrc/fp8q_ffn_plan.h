@@ -62,6 +62,21 @@ inline int64_t part_bytes(const Plan& p, int64_t M, int64_t N, bool gated) {
     return p.splits > 1 ? p.splits * M * N * (gated ? 8 : 4) : 0;
 }
 
+// Few rows through a projection with an epilogue: two MFMA tiles a workgroup
+// tile where that leaves 144 workgroups or more, which draw from memory what 256
+// draw, each the same number of tiles.  (Weights that no cache holds, one token:
+// 7168 -> 18432 26.4 us with one MFMA tile and 256 workgroups, 28.4 with two and
+// 256, 25.7 with two and 192; 12 tokens 18432 -> 7168 33.7 with one, 27.1 with
+// two; one token 7168 -> 2048 6.7 with one, 7.2 with two and 64 workgroups.  A
+// cast within the kernel, by workgroups that take whole groups of 128 columns,
+// was slower than its own launch of 2 us but from 200 to 256 groups: 30.0 against
+// 27.7 at 144, 43.5 against 50.4 at 224.)
+inline bool wide_rows(int64_t N) { return (N + 31) / 32 >= 144; }
+inline int64_t even_groups(int64_t tiles) {
+    const int64_t rounds = (tiles + 255) / 256;
+    return (tiles + rounds - 1) / rounds;
+}
+
 // ---------------------------------------------------------------------------
 // backward products
 // ---------------------------------------------------------------------------

@@ -67,7 +67,7 @@ fp8q_status_t linear_act(fp8q::MmAct& e, int64_t M, int64_t N, int64_t K, void* 
     if (!aligned(f.y, ye) || !aligned(e.res, ye) || (f.z && !aligned(f.z, esize(f.zdt))) || !aligned(f.sinv, 4) ||
         (e.bias && !aligned(e.bias, esize(e.bdt))))
         return FP8Q_EALIGN;
-    const int64_t wsb = fp8q::mm_fwd_workspace(M, N, K, false, f.q != nullptr);
+    const int64_t wsb = fp8q::mm_act_workspace(M, N, K, f.q != nullptr);
     st = check_ws(f.ws, wsb);
     if (st != FP8Q_OK) return st;
     const int64_t KB = K / 128;
@@ -155,7 +155,7 @@ fp8q_status_t fp8q_layernorm_backward(const void* dy, const void* h, fp8q_dtype_
 
 size_t fp8q_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K, int cast) {
     if (!sizes_ok(M, N, K, kMaxFwdRows)) return 0;
-    return (size_t)fp8q::mm_fwd_workspace(M, N, K, false, cast != 0);
+    return (size_t)fp8q::mm_act_workspace(M, N, K, cast != 0);
 }
 
 fp8q_status_t fp8q_linear_act(const uint8_t* x, fp8q_fmt_t xfmt, const float* x_scale_inv, const uint8_t* w,

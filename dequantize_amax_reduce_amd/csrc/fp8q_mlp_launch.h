@@ -52,14 +52,14 @@ void launch_column_sums(const float* part, int64_t parts, int64_t cols, void* ou
 
 // One projection with an epilogue: z = X W^T + bias (kept in f.z [M, N] where
 // asked), then act(z) + res to f.y, or the group cast of act(z) to f.q.  f.w1,
-// f.ws1 and f.gated are unused; the workspace is mm_fwd_workspace's of a
-// projection.
+// f.ws1 and f.gated are unused.
 struct MmAct {
     MmFwd f;
     const void* bias;    // [N] of bdt, or nullptr
     int bdt;
     const void* res;     // [M, N] of f.ydt, or nullptr; may be f.y
 };
+int64_t mm_act_workspace(int64_t M, int64_t N, int64_t K, bool cast);
 void launch_mm_act(const MmAct& a, hipStream_t st);
 
 // Its backward: dz = dy act'(z), f.dx, f.dw0 and db, each or null (not all

@@ -513,6 +513,28 @@ template <int V, bool CAST, bool ACT = false> __global__ void __launch_bounds__(
         float g[V], u[V], v[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) g[k] = u[k] = 0.0f;
+        // four splits' loads in flight at once; past the last they are the last again
+        if constexpr (ACT)
+            for (int s = 0; s < a.splits; s += 4) {
+                float t[4][V];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float* q = p + min(s + j, a.splits - 1) * a.M * W;
+                    if constexpr (V == 4) {
+                        const v4f x = *(const v4f*)q;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) t[j][k] = x[k];
+                    } else {
+                        t[j][0] = q[0];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        if (s + j < a.splits) g[k] += t[j][k];
+            }
+        else
         for (int s = 0; s < a.splits; ++s, p += a.M * W) {
             if constexpr (V == 4) {
                 const v4f x = *(const v4f*)p;
@@ -750,11 +772,13 @@ template <int XF, int WF, int KIND> void run_rows(const FwdArgs& a, float* pbuf,
     auto rounds = [&](int bt) { return (((a.N + per * bt - 1) / (per * bt) + 255) / 256) * bt; };
     auto go = [&](auto MPc, auto BTc) {
         constexpr int MP = decltype(MPc)::value, BT = decltype(BTc)::value;
-        const unsigned g = (unsigned)std::min((a.N + per * BT - 1) / (per * BT), 256);
+        const int tiles = (a.N + per * BT - 1) / (per * BT);
+        unsigned g = (unsigned)std::min(tiles, 256);
+        if (KIND == kOutAct) g = (unsigned)even_groups(tiles);
         k_mm_rows<XF, WF, MP, BT, KIND><<<g, 512, 0, st>>>(a, pbuf);
     };
     auto rows = [&](auto MPc) {
-        if (rounds(1) < rounds(2)) go(MPc, KC<1>{});
+        if (KIND == kOutAct ? !wide_rows(a.N) : rounds(1) < rounds(2)) go(MPc, KC<1>{});
         else go(MPc, KC<2>{});
     };
     if (a.M <= 8) rows(KC<1>{});
