@@ -35,7 +35,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8q.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("fp8q_kernels.hip", "fp8q_shift.hip", "fp8q_abi.cpp",
                                            "fp8q_norm.hip", "fp8q_mm_fwd.hip", "fp8q_mm_bwd.hip", "fp8q_ffn_abi.cpp",
-                                           "fp8q_layernorm.hip", "fp8q_mm_act.hip", "fp8q_mlp_abi.cpp")]
+                                           "fp8q_layernorm.hip", "fp8q_mm_act.hip", "fp8q_mm_act_e5m2.hip", "fp8q_mlp_abi.cpp")]
 ARCH = "gfx950"
 
 

@@ -62,6 +62,85 @@ inline int64_t part_bytes(const Plan& p, int64_t M, int64_t N, bool gated) {
     return p.splits > 1 ? p.splits * M * N * (gated ? 8 : 4) : 0;
 }
 
+// A projection with an epilogue: as plan(), and two more kinds of tiles.
+// Where 64 x 256 tiles are few, 64 x 128, of which two fit a CU; they take 0.44
+// us (binary32 sums: 0.67) a block of K, as many at once or in turn.  In us,
+// 16-bit output with residual / group cast: 1003 x 4096 -> 2048 26.7 and 31.4 with
+// 64 x 256, 18.7 and 25.3 with 64 x 128; 100 x 512 -> 512 8.0 and 12.3, 5.9 and 8.1;
+// the other way 300 x 7168 -> 2048 21.4 and 25.2 (split), 26.0 and 37.7.
+// And where 256 x 256 tiles do not fill their last round of 256 workgroups, the
+// last columns in tiles of 192, of which a workgroup takes one after its whole
+// tiles: 8192 x 2048 -> 4608 137.4 us with one width, 113.8 with two; 4096 x 4096
+// -> 5120 135.3 and 122.9; 4096 x 18432 -> 7168 528.0 and 513.7.
+struct PlanAct {
+    Plan p;                // p.tn: column tiles of 256
+    int64_t tn2;           // then those of 64 nt2
+    int nt2;               // 4: none
+};
+
+// The rounds (in whole tiles' time) after which 256 workgroups have taken
+// `whole` tiles and then `part` tiles of r rounds each
+inline double mixed_rounds(int64_t whole, int64_t part, double r) {
+    const int64_t q = whole / 256, rem = whole % 256;      // rem workgroups have taken q + 1
+    const double least = (double)(q + (rem > 0));
+    if (part == 0) return least;
+    double best = 1e30;
+    for (int late = 0; late < 2; ++late)
+        for (int64_t k = 1 - late;; ++k) {                  // ends at a multiple of r after q, or after q + 1
+            const double t = (double)(q + late) + (double)k * r;
+            if (t >= best) break;
+            const int64_t first = (int64_t)((t - (double)q) / r + 1e-6);
+            const int64_t second = t > (double)(q + 1) ? (int64_t)((t - (double)(q + 1)) / r + 1e-6) : 0;
+            if ((256 - rem) * first + rem * second < part) continue;
+            best = t;
+            break;
+        }
+    return std::max(best, least);
+}
+
+inline PlanAct plan_act(int64_t M, int64_t N, int64_t K, bool ex) {
+    PlanAct r{plan(M, N, K, false, ex), 0, 4};
+    if (r.p.rows || K == 0) return r;
+    const double KB = (double)(K / 128);
+    const double each = ex ? (r.p.bm == 128 ? 1.84 : 1.10) : (r.p.bm == 256 ? 2.30 : r.p.bm == 128 ? 1.26 : 0.78);
+    const int64_t tiles = r.p.tm * r.p.tn;
+    double best = (double)((tiles * r.p.splits + 255) / 256) * ((double)r.p.kper * each + 6.0) +
+                  (r.p.splits > 1 ? 5.0 + (double)(r.p.splits * M * N * 8) / 5e6 : 0.0);
+    // 64 x 128
+    const int64_t tm = (M + 63) / 64, tn = (N + 127) / 128, rounds = (tm * tn + 255) / 256;
+    const double t = (double)rounds * KB * (ex ? 0.67 : 0.44) + 4.5 * (double)((rounds + 1) / 2);
+    if (t < best) {
+        best = t;
+        r.p.bm = 64;
+        r.p.splits = 1;
+        r.p.kper = (int)(K / 128);
+        r.p.tm = tm;
+        r.p.tn = 0;
+        r.tn2 = tn;
+        r.nt2 = 2;
+    }
+    // 256 x 256 and 256 x 192
+    const int64_t th = (M + 255) / 256, whole = (N + 255) / 256;
+    if (!ex && th * whole > 128 && th * whole <= 2048) {
+        const double w = KB * 2.30 + 6.0, part = (KB * 1.80 + 5.0) / w;
+        for (int64_t b = 1; b <= 32 && 192 * b < N + 192; ++b) {
+            const int64_t a = std::max<int64_t>(0, (N - 192 * b + 255) / 256);
+            if (256 * a + 192 * (b - 1) >= N) continue;     // the last would begin past the end
+            const double u = mixed_rounds(th * a, th * b, part) * w;
+            if (u >= best) continue;
+            best = u;
+            r.p.bm = 256;
+            r.p.splits = 1;
+            r.p.kper = (int)(K / 128);
+            r.p.tm = th;
+            r.p.tn = a;
+            r.tn2 = b;
+            r.nt2 = 3;
+        }
+    }
+    return r;
+}
+
 // Few rows through a projection with an epilogue: two MFMA tiles a workgroup
 // tile where that leaves 144 workgroups or more, which draw from memory what 256
 // draw, each the same number of tiles.  (Weights that no cache holds, one token:

@@ -106,8 +106,10 @@ __device__ __forceinline__ int b_row_of(int p) {
 // Tile loader: the rows of one stage, [BM rows of A][256 rows of B], 128 bytes
 // each.  Every wave loads 8 rows per instruction; offsets within a row do not
 // change from step to step, only the three bases move.
-template <int BM> struct TileLoad {
-    static constexpr int JA = BM / 64, JB = 4;
+// NT: 64 rows of B each; PLAIN: they stand in LDS as they stand in B (else in
+// two halves of 128, each in the order of b_row_of).
+template <int BM, int NT = 4, bool PLAIN = false> struct TileLoad {
+    static constexpr int JA = BM / 64, JB = NT;
     const char* a;
     const char* b0;
     const char* b1;
@@ -133,8 +135,8 @@ template <int BM> struct TileLoad {
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
             const int p = (j * 64 + wave * 8 + sub) & 127;
-            int64_t r = b_row_of(p);
-            const int64_t last = j < 2 ? N0 - 1 - n0 : N1 - 1 - n1;
+            int64_t r = PLAIN ? j * 64 + wave * 8 + sub : b_row_of(p);
+            const int64_t last = PLAIN || j < 2 ? N0 - 1 - n0 : N1 - 1 - n1;
             if (r > last) r = last;
             // a half that lies wholly past the end reads the last row before its base
             vb[j] = (uint32_t)((r < 0 ? 0 : r) * row_bytes) + off;
@@ -149,7 +151,7 @@ template <int BM> struct TileLoad {
 #pragma unroll
         for (int j = 0; j < JA; ++j) lds_dma16(stage_lds + lds + j * 8192, va[j], ak);
 #pragma unroll
-        for (int j = 0; j < JB; ++j) lds_dma16(stage_lds + lds + (JA + j) * 8192, vb[j], j < 2 ? b0k : b1k);
+        for (int j = 0; j < JB; ++j) lds_dma16(stage_lds + lds + (JA + j) * 8192, vb[j], PLAIN || j < 2 ? b0k : b1k);
     }
 };
 

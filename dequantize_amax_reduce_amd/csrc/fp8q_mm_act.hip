@@ -7,9 +7,11 @@
 // in registers (k_mm), where the splits of a contraction are joined
 // (k_mm_join), or where the waves' sums of few rows meet (k_mm_rows).
 #include "fp8q_mlp_launch.h"
-#include "fp8q_mm_fwd.h"
+#include "fp8q_mm_act.h"
 
 namespace fp8q {
+
+template void launch_mm_act_whole<kE4M3>(const FwdArgs&, float*, int, const PlanAct&, bool, hipStream_t);
 
 namespace {
 
@@ -26,7 +28,7 @@ bool exact_sums(const MmFwd& f) { return f.q || (f.y && f.ydt == kF32) || (f.z &
 int64_t mm_act_workspace(int64_t M, int64_t N, int64_t K, bool cast) {
     int64_t most = 0;
     for (int ex = cast ? 1 : 0; ex < 2; ++ex) {
-        const Plan p = plan(M, N, K, false, ex);
+        const Plan p = plan_act(M, N, K, ex).p;
         most = std::max(most, p.rows ? (cast ? M * N * 4 : 0) : up256(part_bytes(p, M, N, false)));
     }
     return most;
@@ -35,24 +37,17 @@ int64_t mm_act_workspace(int64_t M, int64_t N, int64_t K, bool cast) {
 void launch_mm_act(const MmAct& e, hipStream_t st) {
     const MmFwd& f = e.f;
     const bool ex = exact_sums(f);
-    const Plan p = plan(f.M, f.N, f.K, false, ex);
+    const PlanAct pa = plan_act(f.M, f.N, f.K, ex);
+    const Plan& p = pa.p;
     // a cast of up to 16 rows goes through binary32 values in the workspace: a
     // workgroup of k_mm_rows has no whole group of 128 columns
     float* pbuf = f.q && p.rows ? (float*)f.ws : nullptr;
     const FwdArgs a{f.x, f.xs, f.w0, f.ws0, nullptr, nullptr, f.M, f.N, f.K / 128, (uint32_t)p.tm, (uint32_t)p.tn, f.act,
                     f.y, f.ydt, f.q, f.qfmt, f.sinv, f.z, f.zdt, f.N % 8 == 0, 0, 0, p.kper, (float*)f.ws,
-                    e.bias, e.bdt, e.res};
-    if (p.splits > 1)
-        launch_mm_partial(a, f.xfmt, f.wfmt, p, ex, st);
-    else
-        with_formats(f.xfmt, f.wfmt, [&](auto X, auto W) {
-            constexpr int XF = decltype(X)::value, WF = decltype(W)::value;
-            if (p.rows) return run_rows<XF, WF, kOutAct>(a, pbuf, st);
-            with_tile(p, ex, [&](auto BM, auto EX) {
-                k_mm<XF, WF, decltype(BM)::value, kOutAct, decltype(EX)::value>
-                    <<<(unsigned)(p.tm * p.tn), kMmThreads, 0, st>>>(a);
-            });
-        });
+                    e.bias, e.bdt, e.res, (uint32_t)pa.tn2};
+    if (p.splits > 1) launch_mm_partial(a, f.xfmt, f.wfmt, p, ex, st);
+    else if (f.xfmt == kE4M3) launch_mm_act_whole<kE4M3>(a, pbuf, f.wfmt, pa, ex, st);
+    else launch_mm_act_whole<kE5M2>(a, pbuf, f.wfmt, pa, ex, st);
     if (p.splits > 1) {
         const JoinArgs j{a.part, p.splits, f.M, f.N, 0, f.act, f.y, f.ydt, f.z, f.zdt, f.q, f.qfmt, f.sinv, e.bias, e.bdt, e.res};
         const int V = f.N % 4 == 0 ? 4 : 1;

@@ -41,6 +41,7 @@ struct FwdArgs {
     const void* bias;      // [N] of bdt, or nullptr
     int bdt;
     const void* res;       // [M, N] of ydt, or nullptr; may be y
+    uint32_t tn2;          // narrower column tiles, after tn of 256
 };
 
 // element e of a tensor of a runtime type
@@ -121,12 +122,13 @@ template <bool WIDE> __device__ __forceinline__ void store8(void* p, int dt, int
 }
 
 // LDS of one step: the tiles, then 64 floats a wave: the scales of BM / 8
-// rows of A and, in the last two, of the halves of B
-template <int BM> struct FwdLds {
-    static constexpr int kS = (BM + kMmBN) * 128;
+// rows of A and, in the last two, of the halves (or the two blocks) of B.  NT: 64
+// columns each.
+template <int BM, int NT = 4> struct FwdLds {
+    static constexpr int kS = (BM + 64 * NT) * 128;
     static constexpr int kStage = kS + 8 * 256;
-    static constexpr int kStages = BM == 256 ? 2 : 3;
-    static constexpr int kPer = BM / 64 + 4 + 1;            // loads a wave issues for a step
+    static constexpr int kStages = BM == 256 && NT > 2 ? 2 : 3;
+    static constexpr int kPer = BM / 64 + NT + 1;           // loads a wave issues for a step
 };
 
 // group-cast epilogue: the amax of a token's 128 columns is over a lane's 8
@@ -171,19 +173,22 @@ template <int BM, int MT> __device__ __forceinline__ void cast_tile(const FwdArg
 // The epilogue of a projection: z = acc + bias (kept where asked), act(z), then
 // the residual and one rounding, or the group cast of each 128 columns.
 //
-// The sums go through LDS (64 or 128 rows of the tile at a time), so that half
-// a wave has 256 columns of a row: stores and residual loads are whole lines, a
-// 128-group is 16 lanes, and the activation's code runs in a loop.  (Where the
-// sums are, in registers that only unrolled code can index, 128 elements a lane
-// of each activation spilled 2263 registers.)  16-byte chunk c of LDS row r is
-// at c ^ (r & 15): writes of 16 rows and reads of 16 chunks spread over the banks.
+// The sums go through LDS (64 or 128 rows of the tile at a time), so that 16,
+// 24 or 32 lanes have the tile's columns of a row: stores and residual loads are
+// whole lines, a 128-group is 16 lanes, and the activation's code runs in a loop.
+// (Where the sums are, in registers that only unrolled code can index, 128 elements
+// a lane of each activation spilled 2263 registers.)  16-byte chunk c of LDS row r
+// is at c ^ (r & 15): writes of 16 rows and reads of 16 chunks spread over the banks.
 typedef unsigned int v2u_b __attribute__((ext_vector_type(2), aligned(1)));
-template <int BM, int MT, bool EX, int ACT>
-__device__ __forceinline__ void act_rows(const FwdArgs& a, v4f (&acc)[MT][4], char* smem, int64_t m0, int n0, int wm, int wn,
-                                         int lane) {
-    constexpr int RT = MT < 4 ? MT : 4, U = ACT == kIdentity ? 4 : 2;   // row tiles a pass; rows a lane has in flight
-    const int col = lane & 15, lr = lane >> 4, ch = lane & 31, wave = wm * 4 + wn;
+template <int BM, int NT, bool EX, int ACT>
+__device__ __forceinline__ void act_rows(const FwdArgs& a, v4f (&acc)[BM / 32][NT], char* smem, int64_t m0, int n0, int wm,
+                                         int wn, int lane) {
+    constexpr int MT = BM / 32, RT = MT < 4 ? MT : 4;      // row tiles a pass
+    constexpr int PITCH = 256 * NT, LPR = 8 * NT, RPI = 64 / LPR, ITER = 4 * RT / RPI;   // bytes and lanes a row; rows at once
+    constexpr int U = ACT == kIdentity && ITER >= 4 ? 4 : 2;                             // rows a lane has in flight
+    const int col = lane & 15, lr = lane >> 4, ch = lane % LPR, wave = wm * 4 + wn;
     const int n = n0 + ch * 8;                             // this lane's columns of a row
+    const bool idle = LPR * RPI < 64 && lane >= LPR * RPI;
     float b[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) b[k] = a.bias ? load1(a.bias, a.bdt, min(n + k, a.N - 1)) : 0.0f;
@@ -194,13 +199,13 @@ __device__ __forceinline__ void act_rows(const FwdArgs& a, v4f (&acc)[MT][4], ch
         for (int t = 0; t < RT; ++t) {
             const int r = (wm * RT + t) * 16 + col;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *(v4f*)(smem + r * 1024 + (((j >> 1) * 32 + wn * 8 + lr * 2 + (j & 1)) ^ col) * 16) = acc[pass * RT + t][j];
+            for (int j = 0; j < NT; ++j)
+                *(v4f*)(smem + r * PITCH + (((wn * NT + j) * 4 + lr) ^ col) * 16) = acc[pass * RT + t][j];
         }
-        // LDS rows wave * 4 RT + 2 i + (lane >> 5), i < 2 RT, are this lane's
-        auto at = [&](int i) { return wave * 4 * RT + 2 * i + (lane >> 5); };
+        // LDS rows wave * 4 RT + RPI i + lane / LPR, i < ITER, are this lane's
+        auto at = [&](int i) { return wave * 4 * RT + RPI * i + (idle ? 0 : lane / LPR); };
         auto row_of = [&](int r) {
-            return m0 + (r / (16 * RT)) * (BM / 2) + pass * RT * 16 + r % (16 * RT);
+            return idle ? a.M : m0 + (r / (16 * RT)) * (BM / 2) + pass * RT * 16 + r % (16 * RT);
         };
         Raw8<EX> res[U], next[U];                           // binary32 outputs have binary32 sums
         auto fetch = [&](Raw8<EX> (&d)[U], int i0) {
@@ -213,15 +218,15 @@ __device__ __forceinline__ void act_rows(const FwdArgs& a, v4f (&acc)[MT][4], ch
         fetch(res, 0);
         __syncthreads();
 #pragma unroll 1
-        for (int i0 = 0; i0 < 2 * RT; i0 += U) {
-            if (i0 + U < 2 * RT) fetch(next, i0 + U);
+        for (int i0 = 0; i0 < ITER; i0 += U) {
+            if (i0 + U < ITER) fetch(next, i0 + U);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int r = at(i0 + u);
                 const int64_t row = row_of(r);
                 const bool in = row < a.M && n < a.N;
-                const v4f lo = *(const v4f*)(smem + r * 1024 + ((2 * ch) ^ (r & 15)) * 16);
-                const v4f hi = *(const v4f*)(smem + r * 1024 + ((2 * ch + 1) ^ (r & 15)) * 16);
+                const v4f lo = *(const v4f*)(smem + r * PITCH + ((2 * ch) ^ (r & 15)) * 16);
+                const v4f hi = *(const v4f*)(smem + r * PITCH + ((2 * ch + 1) ^ (r & 15)) * 16);
                 float v[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = (k < 4 ? lo : hi)[k & 3] + b[k];
@@ -259,30 +264,32 @@ __device__ __forceinline__ void act_rows(const FwdArgs& a, v4f (&acc)[MT][4], ch
     }
 }
 
-// EX: binary32 sums of the codes as bf16; else the fp8 instruction
-template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bounds__(kMmThreads, 2) k_mm(FwdArgs a) {
-    using L = FwdLds<BM>;
+// One tile: rows from m0, 64 NT columns from n0 (of each projection of a gated
+// pair half as many).  EX: binary32 sums of the codes as bf16; else the fp8
+// instruction.  With an epilogue (kOutAct) wave (wm, wn) has 16 NT consecutive
+// columns, since the epilogue deals them out again.
+template <int XF, int WF, int BM, int NT, int OUT, bool EX>
+__device__ __forceinline__ void mm_tile(const FwdArgs& a, char* smem, int64_t m0, int n0) {
+    using L = FwdLds<BM, NT>;
     constexpr int MT = BM / 32;
-    __shared__ __attribute__((aligned(1024))) char smem[L::kStages * L::kStage];
+    constexpr bool ACT = OUT == kOutAct;
+    static_assert(ACT || NT == 4, "halves of 128 columns");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    uint32_t im, in;
-    tile_of(blockIdx.x, a.tm, a.tn, &im, &in);
-    const int64_t m0 = (int64_t)im * BM;
     const bool gated = OUT == kOutGated || (OUT == kOutPartial && a.gated);
-    const int n0 = (int)in * (gated ? 128 : 256);
-    const int n1 = gated ? n0 : n0 + 128;
+    const int n1 = gated ? n0 : ACT ? n0 + 64 * NT - 1 : n0 + 128;
 
     const int kb0 = OUT == kOutPartial ? (int)blockIdx.y * a.kper : 0;
     const int kb1 = OUT == kOutPartial ? min(a.KB, kb0 + a.kper) : a.KB;
 
-    TileLoad<BM> ld;
+    TileLoad<BM, NT, ACT> ld;
     ld.init(a.x, m0, a.M, a.w0, gated ? a.w1 : a.w0, n0, n1, a.N, a.N, (int64_t)a.KB * 128, wave, lane);
     const uint32_t lds0 = lds_offset(smem);
     // Scales through LDS like the tiles (a load into a register inside the
     // loop would wait for every tile load issued before it): lanes below BM / 8
-    // bring the wave's rows of A, the last two the halves of B.
+    // bring the wave's rows of A, the last two the halves of B (with an epilogue
+    // the blocks of the first and of the last column).
     const float* sp;
     if (lane < 62) {
         int64_t r = wave * (BM / 8) + (lane < BM / 8 ? lane : 0);
@@ -298,15 +305,15 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
         lds_dma4_at(s + L::kS + wave * 256, sp + kb);
     };
 
-    v4f acc[MT][4];
+    v4f acc[MT][NT];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) acc[t][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int n = 0; n < NT; ++n) acc[t][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
     const int col = lane & 15, lr = lane >> 4;
     const uint32_t c0 = (uint32_t)((lr ^ (col & 7)) * 16), c1 = (uint32_t)(((lr + 4) ^ (col & 7)) * 16);
-    const uint32_t ra = (uint32_t)((wm * (BM / 2) + col) * 128), rb = (uint32_t)((BM + wn * 32 + col) * 128);
+    const uint32_t ra = (uint32_t)((wm * (BM / 2) + col) * 128), rb = (uint32_t)((BM + wn * (ACT ? 16 * NT : 32) + col) * 128);
     // row r of A: scale r % (BM / 8) of wave r / (BM / 8)
     const uint32_t rs = (uint32_t)(L::kS + wm * 1024 + (BM == 64 ? (col >> 3) * 256 + (col & 7) * 4 : col * 4));
     auto scale_at = [&](int t) { return rs + (BM == 256 ? (t >> 1) * 256 + (t & 1) * 64 : t * (BM == 128 ? 256 : 512)); };
@@ -319,11 +326,11 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
     // it after the step's last MFMA.
     constexpr int ST = L::kStages, PF = MT >= 4 ? 2 : 1;
     constexpr bool BLATE = BM == 256;
-    v8i b[4], bn[4], x[MT + PF];                            // x[MT ..): the next step's first
-    auto read_b = [&](v8i (&d)[4], const char* s) {
+    v8i b[NT], bn[NT], x[MT + PF];                            // x[MT ..): the next step's first
+    auto read_b = [&](v8i (&d)[NT], const char* s) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const char* p = s + rb + (n >> 1) * (128 * 128) + (n & 1) * (16 * 128);
+        for (int n = 0; n < NT; ++n) {
+            const char* p = s + rb + (ACT ? n * (16 * 128) : (n >> 1) * (128 * 128) + (n & 1) * (16 * 128));
             d[n] = frag(p + c0, p + c1);
         }
     };
@@ -336,7 +343,13 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
 #pragma unroll
         for (int t = 0; t < MT; ++t) sx[t] = *(const float*)(s + scale_at(t));
         const float s0 = *(const float*)(s + L::kS + 62 * 4), s1 = *(const float*)(s + L::kS + 63 * 4);
-        v4i bw[4][4];
+        // with an epilogue: a wave's columns are of one block of 128 but for 48, which
+        // may lie in two
+        float sn[ACT ? NT : 1];
+        if constexpr (ACT)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sn[n] = (n0 + (wn * NT + (NT == 3 ? n : 0)) * 16) >> 7 == n0 >> 7 ? s0 : s1;
+        v4i bw[NT][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             if (t + PF < MT) x[t + PF] = read_x(s, t + PF);
@@ -350,9 +363,10 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
             if constexpr (decltype(NEXT)::value)
                 if (t >= MT - PF) x[t + PF] = read_x(smem + nbuf * L::kStage, t + PF - MT);
             const float f0 = sx[t] * s0, f1 = sx[t] * s1;
-            v4f r[4];
+            v4f r[NT];
             auto add = [&](int n) {
-                const float f = n < 2 ? f0 : f1;
+                float f = n < 2 ? f0 : f1;
+                if constexpr (ACT) f = sx[t] * sn[n];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[t][n][i] = __builtin_fmaf(r[n][i], f, acc[t][n][i]);
             };
@@ -360,12 +374,12 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
                 v4i xw[4];
                 widen_codes<XF>(x[t], xw);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) r[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int n = 0; n < NT; ++n) r[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
                 if (t == 0) {
                     // each column tile is widened when its MFMAs come, so that
                     // they start before all four are
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
+                    for (int n = 0; n < NT; ++n) {
                         widen_codes<WF>(b[n], bw[n]);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) r[n] = mfma_bf16(bw[n][k], xw[k], r[n]);
@@ -375,21 +389,21 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) r[n] = mfma_bf16(bw[n][k], xw[k], r[n]);
+                        for (int n = 0; n < NT; ++n) r[n] = mfma_bf16(bw[n][k], xw[k], r[n]);
                 }
             } else {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) r[n] = mfma_fp8<WF, XF>(b[n], x[t]);
+                for (int n = 0; n < NT; ++n) r[n] = mfma_fp8<WF, XF>(b[n], x[t]);
             }
             if constexpr (decltype(NEXT)::value && BLATE)
                 if (t == MT - 1) read_b(b, smem + nbuf * L::kStage);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) add(n);
+            for (int n = 0; n < NT; ++n) add(n);
         }
         if constexpr (decltype(NEXT)::value) {
             if constexpr (!BLATE)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) b[n] = bn[n];
+                for (int n = 0; n < NT; ++n) b[n] = bn[n];
 #pragma unroll
             for (int t = 0; t < PF; ++t) x[t] = x[MT + t];
         }
@@ -412,7 +426,7 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
 
     const int nc = n0 + wn * 32 + lr * 8;                  // this lane's 8 columns of the first half
     if constexpr (OUT == kOutAct) {
-        with_unary(a.act, [&](auto A) { act_rows<BM, MT, EX, decltype(A)::value>(a, acc, smem, m0, n0, wm, wn, lane); });
+        with_unary(a.act, [&](auto A) { act_rows<BM, NT, EX, decltype(A)::value>(a, acc, smem, m0, n0, wm, wn, lane); });
     } else if constexpr (OUT == kOutGated) {
         if (a.z) {
 #pragma unroll
@@ -482,6 +496,35 @@ template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bou
             }
         }
     }
+}
+
+template <int XF, int WF, int BM, int OUT, bool EX> __global__ void __launch_bounds__(kMmThreads, 2) k_mm(FwdArgs a) {
+    using L = FwdLds<BM>;
+    __shared__ __attribute__((aligned(1024))) char smem[L::kStages * L::kStage];
+    uint32_t im, in;
+    tile_of(blockIdx.x, a.tm, a.tn, &im, &in);
+    const bool gated = OUT == kOutGated || (OUT == kOutPartial && a.gated);
+    mm_tile<XF, WF, BM, 4, OUT, EX>(a, smem, (int64_t)im * BM, (int)in * (gated ? 128 : 256));
+}
+
+// A projection with an epilogue: tn column tiles of 256, then tn2 of 64 NT2
+// (whole rounds of workgroups need not be whole tiles of one width); NT2 = 4: none
+// of another width, NT2 = 2 below 256 rows: all of 128.
+template <int XF, int WF, int BM, int NT2, bool EX> __global__ void __launch_bounds__(kMmThreads, 2) k_mm_act(FwdArgs a) {
+    constexpr bool WIDE = NT2 != 2, NARROW = NT2 != 4;
+    using L = FwdLds<BM, WIDE ? 4 : NT2>;
+    __shared__ __attribute__((aligned(1024))) char smem[L::kStages * L::kStage];
+    uint32_t im, in;
+    const uint32_t wide = WIDE ? a.tm * a.tn : 0;
+    const bool second = NARROW && (!WIDE || blockIdx.x >= wide);
+    tile_of(second ? blockIdx.x - wide : blockIdx.x, a.tm, second ? a.tn2 : a.tn, &im, &in);
+    // (wave-uniform as they are; the compiler loses it across the branch)
+    im = __builtin_amdgcn_readfirstlane(im);
+    in = __builtin_amdgcn_readfirstlane(in);
+    if constexpr (WIDE)
+        if (!second) return mm_tile<XF, WF, BM, 4, kOutAct, EX>(a, smem, (int64_t)im * BM, (int)in * 256);
+    if constexpr (NARROW)
+        mm_tile<XF, WF, BM, NT2, kOutAct, EX>(a, smem, (int64_t)im * BM, (int)(WIDE ? a.tn * 256 : 0) + (int)in * 64 * NT2);
 }
 
 // The end of a split product: the partial sums of every output, in order,

@@ -38,7 +38,7 @@ void launch_mm_fwd(const MmFwd& f, hipStream_t st) {
     const bool ex = f.M <= kExactMax || f.q || (f.y && f.ydt == kF32) || (f.z && f.zdt == kF32);
     const Plan p = plan(f.M, f.N, f.K, gated, ex);
     FwdArgs a{f.x, f.xs, f.w0, f.ws0, f.w1, f.ws1, f.M, f.N, f.K / 128, (uint32_t)p.tm, (uint32_t)p.tn, f.act,
-              f.y, f.ydt, f.q, f.qfmt, f.sinv, f.z, f.zdt, 0, 0, gated, p.kper, nullptr, nullptr, 0, nullptr};
+              f.y, f.ydt, f.q, f.qfmt, f.sinv, f.z, f.zdt, 0, 0, gated, p.kper, nullptr, nullptr, 0, nullptr, 0};
     a.vec_y = f.N % 8 == 0 && (p.splits > 1 || al(f.y, 16));
     a.vec_z = f.N % 8 == 0 && al(f.z, 16);
     char* ws = (char*)f.ws;

@@ -1,4 +1,4 @@
-// C entry point over csrc/fp8q_ffn_plan.h, for tests/mlp_plans.py.
+// C entry points over csrc/fp8q_ffn_plan.h, for tests/mlp_plans.py.
 #include "fp8q_ffn_plan.h"
 
 extern "C" void shim_layernorm(int64_t rows, int64_t nv, int tiny, int64_t* o) {
@@ -8,3 +8,16 @@ extern "C" void shim_layernorm(int64_t rows, int64_t nv, int tiny, int64_t* o) {
     o[2] = p.threads;
     o[3] = p.at_once;
 }
+
+// rows a tile (0: few rows), splits, blocks of 128 a split, row tiles, column tiles of 256, of 64 nt2, nt2
+extern "C" void shim_act(int64_t M, int64_t N, int64_t K, int ex, int64_t* o) {
+    const fp8q::PlanAct a = fp8q::plan_act(M, N, K, ex != 0);
+    o[0] = a.p.rows ? 0 : a.p.bm;
+    o[1] = a.p.splits;
+    o[2] = a.p.kper;
+    o[3] = a.p.tm;
+    o[4] = a.p.tn;
+    o[5] = a.tn2;
+    o[6] = a.nt2;
+}
+extern "C" double shim_mixed_rounds(int64_t whole, int64_t part, double r) { return fp8q::mixed_rounds(whole, part, r); }

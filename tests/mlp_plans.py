@@ -1,6 +1,6 @@
-"""Sizes of layer norm, and of a projection's backward pass through an
-activation with f16 gradients, at which every kernel variant runs past its first
-row or steps.  As in ffn_plans.py, the host's choice is asked of
+"""Sizes of layer norm, of a projection with an epilogue, and of its backward
+pass through an activation with f16 gradients, at which every kernel variant runs
+past its first row or steps.  As in ffn_plans.py, the host's choice is asked of
 csrc/fp8q_ffn_plan.h: test_mlp_plans.py checks the tables on the CPU,
 test_gpu_layernorm.py and test_gpu_linear_act.py run them."""
 import ctypes
@@ -43,15 +43,45 @@ BACKWARD_REST = {
 }
 
 
-class LayerNormPlan:
+# (M, K, N, binary32 sums): (rows a tile, splits, blocks a split, column tiles of
+# 256, narrower ones, their width / 64) of a projection with an epilogue; a
+# pipeline has 3 stages (2 of 256 rows), and one block more is its steady step
+ACT = {
+    (70, 640, 72, True): (64, 1, 5, 0, 1, 2),
+    (300, 640, 8200, True): (64, 1, 5, 0, 65, 2),
+    (200, 640, 300, False): (64, 1, 5, 0, 3, 2),
+    (1003, 1024, 1501, False): (64, 1, 8, 0, 12, 2),
+    (400, 1280, 7168, True): (64, 1, 10, 28, 0, 4),
+    (500, 7168, 4104, False): (64, 1, 56, 17, 0, 4),
+    (1900, 1024, 4224, False): (128, 1, 8, 17, 0, 4),
+    (1900, 1024, 4224, True): (128, 1, 8, 17, 0, 4),
+    (4000, 640, 4096, False): (256, 1, 5, 16, 0, 4),
+    (4096, 640, 5120, False): (256, 1, 5, 8, 16, 3),
+    (2050, 512, 8300, False): (256, 1, 4, 19, 18, 3),
+    (65, 7168, 300, False): (64, 14, 4, 2, 0, 4),
+    (70, 7168, 128, True): (64, 14, 4, 1, 0, 4),
+}
+
+
+class MlpPlans:
     def __init__(self, folder):
         lib = os.path.join(str(folder), "libmlp_plan_shim.so")
         subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-fPIC", "-shared", "-I", CSRC,
                         os.path.join(ROOT, "tests", "mlp_plan_shim.cpp"), "-o", lib], check=True)
         self.lib = ctypes.CDLL(lib)
 
-    def __call__(self, rows, cols, dt):
+        self.lib.shim_mixed_rounds.restype = ctypes.c_double
+
+    def layernorm(self, rows, cols, dt):
         out = (ctypes.c_int64 * 4)()
         self.lib.shim_layernorm(ctypes.c_int64(rows), ctypes.c_int64(vectors(cols, dt)),
                                 ctypes.c_int(cols < (4 if dt == "f32" else 8)), out)
         return (bool(out[0]), *tuple(out)[1:])
+
+    def act(self, M, K, N, exact):
+        out = (ctypes.c_int64 * 7)()
+        self.lib.shim_act(*(ctypes.c_int64(v) for v in (M, N, K)), ctypes.c_int(exact), out)
+        return tuple(out)
+
+    def mixed_rounds(self, whole, part, r):
+        return self.lib.shim_mixed_rounds(ctypes.c_int64(whole), ctypes.c_int64(part), ctypes.c_double(r))

@@ -9,7 +9,7 @@ import torch
 
 import dequantize_amax_reduce_amd as fq
 from ffn_plans import BACKWARD, FORWARD
-from mlp_plans import BACKWARD_REST
+from mlp_plans import ACT, BACKWARD_REST
 from gpu_util import G, TORCH_HP
 from test_gpu_ffn import BWD, D, FP8, act64, bwd_err, cast_close, codes, gen_of, near, out_tol, rand, sum_err, up, w64, x64
 
@@ -99,6 +99,14 @@ def test_every_tiling(M, K, N, act):
     """every tile height, whole and split, of both kinds of sum, past its first steps"""
     exact = {k[:3]: k[4] for k in FORWARD if not k[3]}[(M, K, N)]
     linear_case(M, K, N, "f32" if exact else "bf16", act, True, True, None)
+
+
+@pytest.mark.parametrize("M,K,N,exact", list(ACT))
+@pytest.mark.parametrize("act,res,keep", [(None, True, False), ("gelu", False, True), ("silu", True, True)])
+def test_every_epilogue(M, K, N, exact, act, res, keep):
+    """each kind of tile, with and without a residual and kept pre-activations"""
+    dt = "f32" if exact else "f16"
+    linear_case(M, K, N, dt, act, True, res, dt if keep else None)
 
 
 @pytest.mark.parametrize("bt", ["f32", "bf16", "f16"])

@@ -1,12 +1,14 @@
 """CPU: the sizes of tests/mlp_plans.py reach the kernels they are meant to, and
 together every variant of layer norm and of the products that begin with the
 rest's steps."""
+import heapq
+import random
 import shutil
 
 import pytest
 
 from ffn_plans import Plans
-from mlp_plans import BACKWARD_REST, LAYERNORM, LayerNormPlan
+from mlp_plans import ACT, BACKWARD_REST, LAYERNORM, MlpPlans
 
 
 @pytest.fixture(scope="module")
@@ -35,7 +37,7 @@ def test_every_variant_is_reached():
 
 
 def test_layernorm_variants(plans, tmp_path):
-    plan = LayerNormPlan(tmp_path)
+    plan = MlpPlans(tmp_path).layernorm
     for key, want in LAYERNORM.items():
         assert plan(*key) == want, key
         assert key[0] > want[3], key                       # more rows than the grid takes at once
@@ -56,3 +58,54 @@ def test_layernorm_variants(plans, tmp_path):
 def big4(whole):
     """the two sizes of four vectors a thread: 1024 threads and 576"""
     return whole
+
+
+def test_projection_tiles_cover_every_output_once(plans, tmp_path):
+    """random sizes: the tiles of both widths cover the outputs, none begins past
+    the end, and a split's blocks cover the contraction"""
+    P = MlpPlans(tmp_path)
+    rng = random.Random(5)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))
+    seen = set()
+    for _ in range(20000):
+        M, N, K, ex = log(1, 20000), log(1, 40000), 128 * log(1, 200), rng.random() < 0.4
+        bm, splits, kper, tm, tn, tn2, nt2 = P.act(M, K, N, ex)
+        if M <= 16:
+            assert bm == 0 and splits == 1
+            continue
+        key = (M, N, K, ex)
+        assert bm in ((64, 128) if ex else (64, 128, 256)), key
+        assert (tm - 1) * bm < M <= tm * bm, key
+        last = 256 * tn if tn2 == 0 else 256 * tn + 64 * nt2 * (tn2 - 1)
+        assert (last - 256 if tn2 == 0 else last) < N <= 256 * tn + 64 * nt2 * tn2, key
+        assert splits == 1 or (tn2 == 0 and nt2 == 4), key
+        assert (splits - 1) * kper < K // 128 <= splits * kper, key
+        assert nt2 == 4 and tn2 == 0 or nt2 == 2 and bm == 64 and tn == 0 or nt2 == 3 and bm == 256 and not ex, key
+        seen.add((bm, nt2, ex, splits > 1))
+    assert {(bm, nt2, ex) for bm, nt2, ex, _ in seen} == {(64, 4, True), (128, 4, True), (64, 2, True), (64, 4, False),
+                                                         (128, 4, False), (256, 4, False), (64, 2, False), (256, 3, False)}
+
+
+def test_projection_variants(plans, tmp_path):
+    P = MlpPlans(tmp_path)
+    for key, want in ACT.items():
+        bm, splits, kper, _, tn, tn2, nt2 = P.act(*key)
+        assert (bm, splits, kper, tn, tn2, nt2) == want, key
+        assert kper > (2 if bm == 256 else 3)
+    whole = {(bm, nt2, key[3]) for key, (bm, splits, _, _, _, nt2) in ACT.items() if splits == 1}
+    assert whole == {(64, 2, True), (64, 2, False), (64, 4, True), (64, 4, False), (128, 4, True), (128, 4, False),
+                     (256, 4, False), (256, 3, False)}
+    # casts of every kind with binary32 sums: whole groups
+    assert {v[0] for k, v in ACT.items() if k[3] and k[2] % 128 == 0} == {64, 128}
+
+
+def test_mixed_rounds(plans, tmp_path):
+    """against workgroups that take the next tile as they end"""
+    P = MlpPlans(tmp_path)
+    rng = random.Random(6)
+    for _ in range(300):
+        whole, part, r = rng.randrange(0, 1500), rng.randrange(0, 1500), rng.uniform(0.6, 0.95)
+        ends = [0.0] * 256
+        for t in [1.0] * whole + [r] * part:
+            heapq.heappush(ends, heapq.heappop(ends) + t)
+        assert abs(P.mixed_rounds(whole, part, r) - max(ends)) < 1e-4 * (1 + max(ends)), (whole, part, r)
