@@ -206,6 +206,46 @@ inline Plan16 plan_dw(int64_t M, int64_t N, int64_t K, bool gated, bool rest) {
     return plan16(gated ? up64(N) + N : N, K, rest ? C + C / 2 : C);
 }
 
+// The backward pass of a projection with an epilogue: a height of 192 besides
+// (1.21 us a step), and both products in one launch, the longer tiles first, where
+// that takes less.  3001 x 4096 -> 4096 has 192 tiles of 256 rows for dx and 256 for
+// dw, which are two rounds in any order, and 256 and 256 with tiles of 192 rows for
+// dx: 223.5 -> 214.4 us.  4096 x 7168 -> 18432 has 448 tiles of 288 steps and 2016
+// of 64: 2028 -> 1990 in one launch; 2048 x 4096 -> 4096 154.3 -> 146.4; 4096 x 2048
+// -> 5120 241.5 -> 225.2.
+struct PlanBwd {
+    Plan16 dx, dw;
+    bool both;
+};
+inline double each16(int bm) { return bm == 256 ? 1.56 : bm == 192 ? 1.21 : bm == 128 ? 0.90 : 0.50; }
+inline double time16(const Plan16& p, int64_t M, int64_t N) {
+    const int64_t tiles = (M + p.bm - 1) / p.bm * ((N + 255) / 256) * p.splits;
+    return (double)((tiles + 255) / 256) * ((double)p.kper * each16(p.bm) + 4.0) +
+           (p.splits > 1 ? 3.0 + (double)(p.splits * M * N * 8) / 5e6 : 0.0);
+}
+inline PlanBwd plan_bwd_act(int64_t M, int64_t N, int64_t K, bool rest) {
+    const int64_t C = dz_columns(N, false, rest), R = rows_padded(M, rest);
+    const int64_t s1 = (rest ? C + C / 2 : C) / 64, s2 = (rest ? R + R / 2 : R) / 64;   // steps
+    PlanBwd p{plan_dx(M, N, K, false, rest), plan_dw(M, N, K, false, rest), false};
+    auto taller = [&](Plan16& q, int64_t rows, int64_t steps) {
+        const Plan16 alt{192, 1, (int)steps, 0};
+        if (time16(alt, rows, K) < time16(q, rows, K)) q = alt;
+    };
+    taller(p.dx, M, s1);
+    taller(p.dw, N, s2);
+    double best = time16(p.dx, M, K) + time16(p.dw, N, K);
+    for (int h : {256, 192, 128}) {
+        const int64_t tn = (K + 255) / 256, t1 = (M + h - 1) / h * tn, t2 = (N + h - 1) / h * tn;
+        if (t1 + t2 > 8192) continue;                       // the last round is little of so many
+        const double d1 = (double)s1 * each16(h) + 4.0, d2 = (double)s2 * each16(h) + 4.0;
+        const double t = d1 >= d2 ? mixed_rounds(t1, t2, d2 / d1) * d1 : mixed_rounds(t2, t1, d1 / d2) * d2;
+        if (t >= best) continue;
+        best = t;
+        p = PlanBwd{Plan16{h, 1, (int)s1, 0}, Plan16{h, 1, (int)s2, 0}, true};
+    }
+    return p;
+}
+
 // ---------------------------------------------------------------------------
 // norms
 // ---------------------------------------------------------------------------

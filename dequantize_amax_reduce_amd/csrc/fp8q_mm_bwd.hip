@@ -103,14 +103,12 @@ __device__ __forceinline__ bool out_row(const Mm16Args& a, int64_t row, void** c
     return row >= a.gap && row < a.M;
 }
 
-template <int BM, bool PART, bool REST> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Args a) {
+template <int BM, bool PART, bool REST>
+__device__ __forceinline__ void mm16_tile(const Mm16Args& a, char* smem, uint32_t im, uint32_t in) {
     constexpr int MT = BM / 32, kStage = (BM + kMmBN) * 128;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    uint32_t im, in;
-    tile_of(blockIdx.x, a.tm, a.tn, &im, &in);
     const int64_t m0 = (int64_t)im * BM;
     const int n0 = (int)in * 256;
     TileLoad<BM> ld;
@@ -224,6 +222,26 @@ template <int BM, bool PART, bool REST> __global__ void __launch_bounds__(kMmThr
             put8(c, a.cdt, r, a.N, nc + half * 128, a.N, a.vec, v);
         }
     }
+}
+
+template <int BM, bool PART, bool REST> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16(Mm16Args a) {
+    __shared__ __attribute__((aligned(1024))) char smem[2 * (BM + kMmBN) * 128];
+    uint32_t im, in;
+    tile_of(blockIdx.x, a.tm, a.tn, &im, &in);
+    mm16_tile<BM, PART, REST>(a, smem, im, in);
+}
+
+// two whole products in one launch: the first's tiles, then the second's
+template <int BM, bool REST> __global__ void __launch_bounds__(kMmThreads, 2) k_mm16_two(Mm16Args a, Mm16Args b) {
+    __shared__ __attribute__((aligned(1024))) char smem[2 * (BM + kMmBN) * 128];
+    const uint32_t first = a.tm * a.tn;
+    const bool second = blockIdx.x >= first;
+    Mm16Args g = a;
+    if (second) g = b;
+    uint32_t im, in;
+    tile_of(second ? blockIdx.x - first : blockIdx.x, g.tm, g.tn, &im, &in);
+    // (wave-uniform as they are; the compiler loses it across the choice)
+    mm16_tile<BM, false, REST>(g, smem, __builtin_amdgcn_readfirstlane(im), __builtin_amdgcn_readfirstlane(in));
 }
 
 // the end of a split product: the partial sums in order; a thread takes 8
@@ -710,28 +728,52 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 // c[m, n] = sum_k a[m, k] b[n, k]; rows [0, split) to c0, rows from gap to c1;
 // N % 128 == 0; rest: each row's first K bytes are the rest; p: the plan of the
 // product
-void mm16(const void* A, const void* B, int64_t M, int64_t N, int64_t K, bool rest, void* c0, void* c1, int64_t split,
-          int64_t gap, int cdt, const Plan16& p, const uint32_t* ka, const uint32_t* kb, int qb, float* part, hipStream_t st) {
+Mm16Args mm16_args(const void* A, const void* B, int64_t M, int64_t N, int64_t K, bool rest, void* c0, void* c1,
+                   int64_t split, int64_t gap, int cdt, const Plan16& p, const uint32_t* ka, const uint32_t* kb, int qb,
+                   float* part) {
     const int K8 = rest ? (int)(K / 128) : 0;
     Mm16Args a{A, B, M, (int)N, (int)(K / 64) + K8, K8, 0, 0, c0, c1, split, gap, cdt, 0, ka, kb, qb, p.kper, p.splits, part};
     a.vec = al(c0, 16) && (!c1 || al(c1, 16));
     a.tn = (uint32_t)((N + 255) / 256);
     a.tm = (uint32_t)((M + p.bm - 1) / p.bm);
-    const dim3 g(a.tm * a.tn, (unsigned)p.splits);
-    auto go = [&](auto BMc, auto RESTc) {
+    return a;
+}
+
+template <typename F> void with_bool(bool b, F&& f) {
+    if (b) f(std::true_type{});
+    else f(std::false_type{});
+}
+
+// go(BM, REST)
+template <typename F> void with_height(int bm, bool rest, F&& go) {
+    with_bool(rest, [&](auto R) {
+        if (bm == 256) go(KC<256>{}, R);
+        else if (bm == 192) go(KC<192>{}, R);
+        else if (bm == 128) go(KC<128>{}, R);
+        else go(KC<64>{}, R);
+    });
+}
+
+void mm16(const Mm16Args& a, int bm, bool rest, hipStream_t st) {
+    const dim3 g(a.tm * a.tn, (unsigned)a.splits);
+    with_height(bm, rest, [&](auto BMc, auto R) {
         constexpr int BM = decltype(BMc)::value;
-        constexpr bool REST = decltype(RESTc)::value;
-        if (p.splits > 1) k_mm16<BM, true, REST><<<g, kMmThreads, 0, st>>>(a);
-        else k_mm16<BM, false, REST><<<g, kMmThreads, 0, st>>>(a);
-    };
-    auto tall = [&](auto RESTc) {
-        if (p.bm == 256) go(KC<256>{}, RESTc);
-        else if (p.bm == 128) go(KC<128>{}, RESTc);
-        else go(KC<64>{}, RESTc);
-    };
-    if (rest) tall(std::true_type{});
-    else tall(std::false_type{});
-    if (p.splits > 1) k_mm16_join<<<(unsigned)std::min<int64_t>((M * (N / 8) + 255) / 256, 4096), 256, 0, st>>>(a);
+        constexpr bool REST = decltype(R)::value;
+        if (a.splits == 1) k_mm16<BM, false, REST><<<g, kMmThreads, 0, st>>>(a);
+        else if constexpr (BM != 192) k_mm16<BM, true, REST><<<g, kMmThreads, 0, st>>>(a);   // 192 is never split
+    });
+    if (a.splits > 1)
+        k_mm16_join<<<(unsigned)std::min<int64_t>((a.M * (a.N / 8) + 255) / 256, 4096), 256, 0, st>>>(a);
+}
+
+// both, the longer tiles first
+void mm16_two(const Mm16Args& a, const Mm16Args& b, int bm, bool rest, hipStream_t st) {
+    if (a.KB < b.KB) return mm16_two(b, a, bm, rest, st);
+    const unsigned g = a.tm * a.tn + b.tm * b.tn;
+    with_height(bm, rest, [&](auto BMc, auto R) {
+        constexpr int BM = decltype(BMc)::value;
+        if constexpr (BM != 64) k_mm16_two<BM, decltype(R)::value><<<g, kMmThreads, 0, st>>>(a, b);
+    });
 }
 
 template <typename F> void with_fmt(int f, F&& go) {
@@ -758,7 +800,7 @@ struct BwdLayout {
     int64_t part;          // the products' partial sums
     int64_t bytes;
 };
-BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated, bool rest) {
+BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated, bool rest, const PlanBwd& p) {
     BwdLayout l;
     l.Mp = rows_padded(M, rest);
     l.C = dz_columns(N, gated, rest);
@@ -777,7 +819,7 @@ BwdLayout layout(int64_t M, int64_t N, int64_t K, bool gated, bool rest) {
     l.kcol = l.krow + 4 * M;
     l.kx = l.kcol + 4 * l.C;
     l.kw = l.kx + 4 * (K / 128);
-    l.part = take(std::max(plan_dx(M, N, K, gated, rest).part, plan_dw(M, N, K, gated, rest).part));
+    l.part = take(std::max(p.dx.part, p.dw.part));
     l.bytes = at;
     return l;
 }
@@ -790,13 +832,22 @@ void launch_zero16(void* p, int64_t n, hipStream_t st) {
 
 namespace {
 
+PlanBwd plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool rest, bool act) {
+    if (act) return plan_bwd_act(M, N, K, rest);
+    return PlanBwd{plan_dx(M, N, K, gated, rest), plan_dw(M, N, K, gated, rest), false};
+}
+int64_t layout_bytes(int64_t M, int64_t N, int64_t K, bool gated, bool rest, bool act) {
+    return layout(M, N, K, gated, rest, plan_of(M, N, K, gated, rest, act)).bytes;
+}
+
 int64_t bias_rows(int64_t M) { return (M + 127) / 128 * 2; }  // sums of 64 rows, padded as M is with a rest
 
-// dx, the weight gradients and, of a projection, the partial sums of dbias
-// (bias: [bias_rows(M)][N] floats, or nullptr); sizes > 0
-void run_bwd(const MmBwd& f, int mode, float* bias, hipStream_t st) {
+// dx, the weight gradients and, of a projection with an epilogue (act), the
+// partial sums of dbias (bias: [bias_rows(M)][N] floats, or nullptr); sizes > 0
+void run_bwd(const MmBwd& f, int mode, bool act, float* bias, hipStream_t st) {
     const bool gated = mode == kOfGated, rest = has_rest(f.dt, mode);
-    const BwdLayout l = layout(f.M, f.N, f.K, gated, rest);
+    const PlanBwd plan = plan_of(f.M, f.N, f.K, gated, rest, act);
+    const BwdLayout l = layout(f.M, f.N, f.K, gated, rest, plan);
     char* ws = (char*)f.ws;
     char *dz = ws + l.dz, *dzt = ws + l.dzt, *wt = ws + l.wt, *xt = ws + l.xt;
     float* part = (float*)(ws + l.part);
@@ -840,12 +891,12 @@ void run_bwd(const MmBwd& f, int mode, float* bias, hipStream_t st) {
             });
         });
     });
-    if (wdx)
-        mm16(dz, wt, f.M, f.K, l.C, rest, f.dx, nullptr, f.M, f.M, f.dt, plan_dx(f.M, f.N, f.K, gated, rest), krow, kw, qw,
-             part, st);
-    if (wdw)
-        mm16(dzt, xt, gated ? l.Np + f.N : f.N, f.K, l.Mp, rest, f.dw0, gated ? f.dw1 : nullptr, f.N, gated ? l.Np : f.N,
-             f.dwdt, plan_dw(f.M, f.N, f.K, gated, rest), kcol, kx, qx, part, st);
+    const Mm16Args ax = mm16_args(dz, wt, f.M, f.K, l.C, rest, f.dx, nullptr, f.M, f.M, f.dt, plan.dx, krow, kw, qw, part);
+    const Mm16Args aw = mm16_args(dzt, xt, gated ? l.Np + f.N : f.N, f.K, l.Mp, rest, f.dw0, gated ? f.dw1 : nullptr, f.N,
+                                  gated ? l.Np : f.N, f.dwdt, plan.dw, kcol, kx, qx, part);
+    if (plan.both && wdx && wdw) return mm16_two(ax, aw, plan.dx.bm, rest, st);
+    if (wdx) mm16(ax, plan.dx.bm, rest, st);
+    if (wdw) mm16(aw, plan.dw.bm, rest, st);
 }
 
 }  // namespace
@@ -853,7 +904,7 @@ void run_bwd(const MmBwd& f, int mode, float* bias, hipStream_t st) {
 int64_t mm_bwd_workspace(int64_t M, int64_t N, int64_t K, bool gated) {
     if (M == 0 || N == 0 || K == 0) return 0;
     // enough for either type of gradient, which is not known here
-    return std::max(layout(M, N, K, gated, false).bytes, layout(M, N, K, gated, gated).bytes);
+    return std::max(layout_bytes(M, N, K, gated, false, false), layout_bytes(M, N, K, gated, gated, false));
 }
 
 void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
@@ -863,12 +914,12 @@ void launch_mm_bwd(const MmBwd& f, hipStream_t st) {
         zero(f.dw1, (int64_t)f.N * f.K, f.dwdt, st);
         return;
     }
-    run_bwd(f, f.gated ? kOfGated : kOfLinear, nullptr, st);
+    run_bwd(f, f.gated ? kOfGated : kOfLinear, false, nullptr, st);
 }
 
 int64_t mm_act_bwd_workspace(int64_t M, int64_t N, int64_t K) {
     if (M == 0 || N == 0) return 0;
-    const int64_t products = K == 0 ? 0 : std::max(layout(M, N, K, false, false).bytes, layout(M, N, K, false, true).bytes);
+    const int64_t products = K == 0 ? 0 : std::max(layout_bytes(M, N, K, false, false, true), layout_bytes(M, N, K, false, true, true));
     return products + bias_rows(M) * N * 4;
 }
 
@@ -882,10 +933,10 @@ void launch_mm_act_bwd(const MmActBwd& e, hipStream_t st) {
     }
     const int mode = f.act == kIdentity ? kOfLinear : kOfUnary;
     const bool products = f.K > 0 && (f.dx || f.dw0), rest = has_rest(f.dt, mode);
-    float* bias = e.db ? (float*)((char*)f.ws + (products ? layout(f.M, f.N, f.K, false, rest).bytes : 0)) : nullptr;
+    float* bias = e.db ? (float*)((char*)f.ws + (products ? layout_bytes(f.M, f.N, f.K, false, rest, true) : 0)) : nullptr;
     const int64_t tiles = (products ? rows_padded(f.M, rest) : up64(f.M)) / 64;
     if (products) {
-        run_bwd(f, mode, bias, st);
+        run_bwd(f, mode, true, bias, st);
     } else {                                                // dbias alone: the tiles of dz, none laid out
         PrepArgs p{};
         p.dz.dy = (const uint16_t*)f.dy;

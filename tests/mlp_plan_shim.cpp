@@ -21,3 +21,14 @@ extern "C" void shim_act(int64_t M, int64_t N, int64_t K, int ex, int64_t* o) {
     o[6] = a.nt2;
 }
 extern "C" double shim_mixed_rounds(int64_t whole, int64_t part, double r) { return fp8q::mixed_rounds(whole, part, r); }
+
+// of dx, then of dw: rows a tile, splits, steps a split; then whether one launch has both
+extern "C" void shim_bwd_act(int64_t M, int64_t N, int64_t K, int rest, int64_t* o) {
+    const fp8q::PlanBwd p = fp8q::plan_bwd_act(M, N, K, rest != 0);
+    for (const fp8q::Plan16* q : {&p.dx, &p.dw}) {
+        *o++ = q->bm;
+        *o++ = q->splits;
+        *o++ = q->kper;
+    }
+    *o = p.both;
+}

@@ -1,6 +1,5 @@
 """Sizes of layer norm, of a projection with an epilogue, and of its backward
-pass through an activation with f16 gradients, at which every kernel variant runs
-past its first row or steps.  As in ffn_plans.py, the host's choice is asked of
+pass, at which every kernel variant runs past its first row or steps.  As in ffn_plans.py, the host's choice is asked of
 csrc/fp8q_ffn_plan.h: test_mlp_plans.py checks the tables on the CPU,
 test_gpu_layernorm.py and test_gpu_linear_act.py run them."""
 import ctypes
@@ -27,21 +26,48 @@ LAYERNORM = {
     (300, 17001, "bf16"): (False, 4, 576, 256),
 }
 
-# (M, K, N): (rows a tile, splits, steps of 64 a split) of dx and of dw; a split
-# may hold steps of the rest alone, of both, or of neither
-BACKWARD_REST = {
-    (17, 128, 72): ((64, 1, 3), (64, 1, 3)),
-    (17, 128, 640): ((64, 2, 8), (64, 1, 3)),
-    (513, 128, 64): ((64, 1, 3), (64, 2, 8)),
-    (200, 384, 8200): ((64, 28, 7), (128, 1, 6)),
-    (2100, 128, 4104): ((128, 15, 7), (64, 2, 26)),
-    (3000, 128, 4104): ((64, 4, 25), (128, 4, 18)),
-    (4100, 128, 4104): ((256, 15, 7), (256, 15, 7)),
-    (4100, 1024, 256): ((128, 1, 6), (64, 15, 7)),
-    (4100, 2048, 130): ((256, 1, 6), (64, 8, 13)),
-    (200, 640, 12300): ((64, 16, 19), (256, 1, 6)),
+# (M, K, N): (rows a tile, splits, steps of 64 a split) of dx and of dw, and whether
+# one launch has both
+BACKWARD = {
+    (200, 128, 1280): ((64, 4, 5), (64, 1, 4), False),
+    (1000, 128, 72): ((64, 1, 2), (64, 4, 4), False),
+    (200, 384, 8200): ((64, 26, 5), (128, 1, 4), False),
+    (130, 128, 130): ((128, 1, 3), (128, 1, 3), True),
+    (4100, 128, 2053): ((64, 2, 17), (128, 13, 5), False),
+    (200, 640, 12300): ((64, 15, 13), (192, 1, 4), False),
+    (200, 1024, 12300): ((64, 15, 13), (256, 1, 4), False),
+    (17, 128, 1280): ((64, 4, 5), (64, 1, 1), False),
+    (6000, 640, 130): ((128, 1, 3), (64, 16, 6), False),
+    (2100, 128, 4104): ((128, 13, 5), (64, 2, 17), False),
+    (4100, 2048, 130): ((192, 1, 3), (64, 8, 9), False),
+    (4100, 2048, 250): ((192, 1, 4), (64, 8, 9), False),
+    (8192, 128, 4104): ((64, 2, 33), (256, 8, 16), False),
+    (4100, 128, 8192): ((256, 8, 16), (64, 2, 33), False),
+    (1000, 5120, 640): ((192, 1, 10), (192, 1, 16), True),
+    (1000, 5120, 1280): ((256, 1, 20), (256, 1, 16), True),
+    (1000, 128, 130): ((64, 1, 3), (64, 4, 4), False),
+    (4100, 3584, 130): ((256, 1, 3), (64, 4, 17), False),
 }
 
+# the same of f16 gradients through an activation, whose contractions begin with the
+# rest's steps: a split may hold steps of the rest alone, of both, or of neither
+BACKWARD_REST = {
+    (17, 128, 640): ((64, 2, 8), (64, 1, 3), False),
+    (513, 128, 72): ((64, 1, 3), (64, 2, 8), False),
+    (200, 384, 8200): ((64, 28, 7), (128, 1, 6), False),
+    (130, 128, 130): ((128, 1, 6), (128, 1, 6), True),
+    (4100, 128, 2053): ((64, 2, 26), (128, 15, 7), False),
+    (200, 640, 12300): ((64, 16, 19), (192, 1, 6), False),
+    (200, 1024, 12300): ((64, 16, 19), (256, 1, 6), False),
+    (2100, 128, 4104): ((128, 15, 7), (64, 2, 26), False),
+    (6000, 640, 72): ((128, 1, 3), (64, 29, 5), False),
+    (4100, 2048, 72): ((192, 1, 3), (64, 15, 7), False),
+    (4100, 3584, 72): ((256, 1, 3), (64, 8, 13), False),
+    (4100, 128, 4104): ((256, 15, 7), (256, 15, 7), False),
+    (1000, 5120, 640): ((192, 1, 15), (192, 1, 24), True),
+    (1000, 5120, 1280): ((256, 1, 30), (256, 1, 24), True),
+    (3000, 128, 4104): ((64, 4, 25), (128, 4, 18), False),
+}
 
 # (M, K, N, binary32 sums): (rows a tile, splits, blocks a split, column tiles of
 # 256, narrower ones, their width / 64) of a projection with an epilogue; a
@@ -85,3 +111,8 @@ class MlpPlans:
 
     def mixed_rounds(self, whole, part, r):
         return self.lib.shim_mixed_rounds(ctypes.c_int64(whole), ctypes.c_int64(part), ctypes.c_double(r))
+
+    def backward(self, M, K, N, rest):
+        out = (ctypes.c_int64 * 7)()
+        self.lib.shim_bwd_act(*(ctypes.c_int64(v) for v in (M, N, K)), ctypes.c_int(rest), out)
+        return tuple(out)[:3], tuple(out)[3:6], bool(out[6])

@@ -8,7 +8,7 @@ import shutil
 import pytest
 
 from ffn_plans import Plans
-from mlp_plans import ACT, BACKWARD_REST, LAYERNORM, MlpPlans
+from mlp_plans import ACT, BACKWARD, BACKWARD_REST, LAYERNORM, MlpPlans
 
 
 @pytest.fixture(scope="module")
@@ -18,15 +18,16 @@ def plans(tmp_path_factory):
     return Plans(tmp_path_factory.mktemp("plan"))
 
 
-def test_sizes_reach_their_kernels(plans):
-    for key, want in BACKWARD_REST.items():
-        assert plans.backward(*key, False, True) == want, key
-
-
-def test_every_variant_is_reached():
-    for product in (0, 1):
-        got = {(p[product][0], p[product][1] > 1) for p in BACKWARD_REST.values() if p[product][2] > 2}
-        assert got == {(bm, s) for bm in (64, 128, 256) for s in (False, True)}, product
+def test_backward_variants(plans, tmp_path):
+    P = MlpPlans(tmp_path)
+    for rest, table in ((False, BACKWARD), (True, BACKWARD_REST)):
+        for key, want in table.items():
+            assert P.backward(*key, rest) == want, key
+        for product in (0, 1):
+            got = {(p[product][0], p[product][1] > 1) for p in table.values() if p[product][2] > 2 and not p[2]}
+            assert got == {(bm, s) for bm in (64, 128, 256) for s in (False, True)} | {(192, False)}, (rest, product)
+        both = {p[0][0] for p in table.values() if p[2] and p[0][2] > 2 and p[1][2] > 2}
+        assert both == {128, 192, 256}
     kinds = set()
     for (M, _, N), plan in BACKWARD_REST.items():
         for (_, splits, kper), C in zip(plan, ((N + 127) // 128 * 128, (M + 127) // 128 * 128)):
