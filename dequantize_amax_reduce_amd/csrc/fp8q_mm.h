@@ -314,29 +314,28 @@ template <int ACT> __device__ __forceinline__ float unary_grad(float dy, float z
     }
 }
 
-// A bound on |dy act'(z)|, for its exponent: from 0 up a constant above the
-// slope's maximum (1.129 at most); below, what multiplies exp there: (1 + |z|)
-// e^z of SiLU, e^w (1 + |z| w') of the tanh form, and max(1/2, 0.4 |z|) exp(-z^2 / 2)
-// of GELU.  It exceeds the value by no more than a few binary orders but near a
-// slope's zero, which costs nothing: f16 has 29 of them with all its bits.
-template <int ACT> __device__ __forceinline__ float unary_bound(float dy, float z) {
-    if constexpr (ACT == kIdentity) return dy;
-    if constexpr (ACT == kRelu) return z <= 0.0f ? 0.0f : dy;
-    const float x = z < -64.0f ? 64.0f : -z;
-    float c, y;                                             // z < 0: c e^(2 y), x = -z
+// An e with |act'(z)| < 2^e, for the exponent of a gradient.  From 0 up the slope
+// is at most 1.13; below, x = -z, it is at most c 2^t: (1 + x) e^-x of SiLU, (1 + x
+// w') e^w of the tanh form, max(1/2, 0.4 x) exp(-x^2 / 2) of GELU (whose c here is at
+// least the slope's maximum, so that x = 0 serves z > 0).  It exceeds the slope by
+// no more than a few binary orders but near its zeros, which costs nothing: f16 has
+// 29 of them with all its bits.
+template <int ACT> __device__ __forceinline__ int slope_exponent(float z) {
+    static_assert(ACT != kIdentity && ACT != kRelu, "their slopes are 0 and 1");
+    const float x = __builtin_amdgcn_fmed3f(-z, 0.0f, ACT == kGelu ? 30.0f : ACT == kGeluTanh ? 10.0f : 200.0f);
+    float c, t;
     if constexpr (ACT == kGelu) {
-        c = fmaxf(0.5f, 0.4f * x);
-        y = -0.25f * x * x;
+        c = fmaxf(1.14f, 0.4f * x);
+        t = -0.72134752f * x * x;
     } else if constexpr (ACT == kGeluTanh) {
         const float k = 1.5957691216057308f;
-        c = 1.0f + x * k * (1.0f + 0.134145f * x * x);
-        y = -0.5f * k * (x + 0.044715f * x * x * x);
+        c = 1.14f + x * k * (1.0f + 0.134145f * x * x);
+        t = -1.44269504f * k * (x + 0.044715f * x * x * x);
     } else {
-        c = 1.0f + x;
-        y = -0.5f * x;
+        c = 1.14f + x;
+        t = -1.44269504f * x;
     }
-    const float e = fmaxf(__expf(y), 0x1p-126f);            // __expf has no subnormal values
-    return z < 0.0f ? dy * c * e * e : z >= 0.0f ? 1.14f * dy : z;
+    return (int)t + (int)(__float_as_uint(c) >> 23) - 126;  // t <= 0 is rounded up
 }
 
 // f(integral_constant) over a runtime activation; with_unary: those of a

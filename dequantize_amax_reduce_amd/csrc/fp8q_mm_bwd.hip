@@ -374,8 +374,7 @@ __global__ void __launch_bounds__(256) k_scales(ScaleArgs a) {
 }
 
 // 8 columns of dg (dz without a gate) and du from column c of row m < M;
-// zero from column N on (FULL: there are none); QUICK, for exponents: as in
-// act_at, and without a gate bounds in place of the values
+// zero from column N on (FULL: there are none); QUICK as in act_at
 template <int DT, int MODE, bool FULL, bool QUICK>
 __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z, int64_t m, int c, int N, int act,
                                           float* g, float* u) {
@@ -386,7 +385,7 @@ __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z,
         with_unary(act, [&](auto A) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float d = QUICK ? unary_bound<decltype(A)::value>(g[k], zv[k]) : unary_grad<decltype(A)::value>(g[k], zv[k]);
+                const float d = unary_grad<decltype(A)::value>(g[k], zv[k]);
                 g[k] = FULL || c + k < N ? d : 0.0f;
             }
         });
@@ -408,8 +407,10 @@ __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z,
 }
 
 // The keys of dz's rows and columns, and of X' and W' per 128 columns of K.
-// (4096 x 18432 bf16 through GELU: 157 us with the slope itself, whose erfc and exp
-// bound it, and 58 with a bound on it.)
+// Of a dz that is dy times one activation's slope they come from dy's exponents and
+// bounds on the slopes' (4096 x 18432 bf16 through GELU: 157 us with the slope
+// itself, 94 with a binary32 bound on it, 81 with the integer one; each bound by its
+// instructions, 32 an element in the second.)
 // Workgroups [0, e0) take 128 x 128 of dz, 16 lanes a row and 8 columns a lane;
 // [e0, e1) 32 rows of X's scales, the rest as many block rows of W's.  The
 // maxima of integers do not depend on the order of the atomics.  A key of dz is of
@@ -483,12 +484,46 @@ template <int DT, int MODE> __global__ void __launch_bounds__(256) k_keys(KeyArg
     // atomics on one word take 8 ns each: only a row's own lanes make them).
     // The loads of R rows are in flight at once.
     auto rows = [&](auto FULL) {
-        constexpr int R = MODE == kOfLinear ? 4 : 2;
+        constexpr int R = MODE == kOfGated ? 2 : 4;
 #pragma unroll 1
         for (int i = 0; i < 8; i += R) {
             float d[R][H][8];
             int64_t m[R];
             int ex[R];
+            if constexpr (MODE == kOfUnary) {
+                float z[R][8];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    m[r] = m0 + (i + r) * 16 + rl;
+                    if (m[r] > a.M - 1) m[r] = a.M - 1;
+                    ex[r] = exponent_of(a.sx[m[r]]);
+                    ld8<DT, decltype(FULL)::value>(a.dy + m[r] * a.N, c, a.N, d[r][0]);
+                    ld8<DT, decltype(FULL)::value>(a.z + m[r] * a.N, c, a.N, z[r]);
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    // the keys of |dy| 2^e, none of zero and non-finite values (nor of those whose slope is 0)
+                    int key[8], top = 0;
+                    auto of = [&](int k, int e, bool ok) {
+                        const uint32_t b = __float_as_uint(d[r][0][k]) & 0x7FFFFFFFu;
+                        key[k] = ok && b - 1u < 0x7F7FFFFFu ? (int)(b >> 23) + e + kKeyBias : -(1 << 20);
+                        top = max(top, key[k]);
+                    };
+                    if (a.act == kRelu)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) of(k, 0, !(z[r][k] <= 0.0f));
+                    else
+                        with_act(a.act, [&](auto A) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) of(k, slope_exponent<decltype(A)::value>(z[r][k]), true);
+                        });
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) kc[0][k] = (uint32_t)max((int)kc[0][k], key[k] + ex[r]);
+                    const uint32_t kr = max_lanes<16>(top > 0 ? (uint32_t)max(top + ew[0], 0) : 0u);
+                    if (v == 0 && a.krow && kr && m0 + (i + r) * 16 + rl < a.M) atomicMax(a.krow + m[r], kr);
+                }
+                continue;
+            }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 m[r] = m0 + (i + r) * 16 + rl;
