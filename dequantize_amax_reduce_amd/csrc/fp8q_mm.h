@@ -291,25 +291,26 @@ struct Gelu {
     }
 };
 
-// act(z)
+// act(z); 0 at -infinity but of the identity
 template <int ACT> __device__ __forceinline__ float unary_value(float z) {
     if constexpr (ACT == kGelu) {
         const Gelu g(z);
         return (z < 0.0f ? 0.0f : z) - g.x * g.r * g.e * g.e;
     } else {
-        const Act r = act_at<ACT, false>(z);
+        const Act r = act_at<ACT, false>(ACT != kIdentity && z < -0x1p100f ? -0x1p100f : z);
         return r.a * r.e;
     }
 }
 
-// dy act'(z)
+// dy act'(z); the slope is 0 at -infinity and 1 at infinity
 template <int ACT> __device__ __forceinline__ float unary_grad(float dy, float z) {
     if constexpr (ACT == kGelu) {
         const Gelu g(z);
         const float q = (0.39894228040143268f * g.x - g.r) * g.e;   // x phi(x) - Phi(-x), over e
         return z < 0.0f ? dy * -q * g.e : dy * __builtin_fmaf(q, g.e, 1.0f);
     } else {
-        const Act r = act_at<ACT, true>(z);
+        // past 256 the logistic function is 0 or 1 (a NaN passes)
+        const Act r = act_at<ACT, true>(z > 256.0f ? 256.0f : z < -256.0f ? -256.0f : z);
         return dy * r.d * r.e;
     }
 }
@@ -319,10 +320,10 @@ template <int ACT> __device__ __forceinline__ float unary_grad(float dy, float z
 // w') e^w of the tanh form, max(1/2, 0.4 x) exp(-x^2 / 2) of GELU (whose c here is at
 // least the slope's maximum, so that x = 0 serves z > 0).  It exceeds the slope by
 // no more than a few binary orders but near its zeros, which costs nothing: f16 has
-// 29 of them with all its bits.
+// 29 of them with all its bits.  (Past the largest x a gradient of any size gives 0.)
 template <int ACT> __device__ __forceinline__ int slope_exponent(float z) {
     static_assert(ACT != kIdentity && ACT != kRelu, "their slopes are 0 and 1");
-    const float x = __builtin_amdgcn_fmed3f(-z, 0.0f, ACT == kGelu ? 30.0f : ACT == kGeluTanh ? 10.0f : 200.0f);
+    const float x = __builtin_amdgcn_fmed3f(-z, 0.0f, ACT == kGelu ? 30.0f : ACT == kGeluTanh ? 16.0f : 200.0f);
     float c, t;
     if constexpr (ACT == kGelu) {
         c = fmaxf(1.14f, 0.4f * x);
