@@ -285,14 +285,15 @@ def layernorm(x, weight, bias=None, residual=None, eps=1e-5, out=None):
     """(y, h, mean, rstd): h = x + residual, y = (h - mean) / sqrt(var + eps) *
     weight + bias over the last dimension, in x's dtype.  h is x itself without
     a residual; h, mean and rstd are what layernorm_backward reads.  `out`:
-    those four tensors, caller-allocated (without a residual, x itself may
-    stand for h; another tensor gets a copy of x)."""
+    those four tensors, caller-allocated.  h may be x there: without a residual
+    it is left as it is, with one h is written over x (another tensor gets a copy
+    of x without a residual)."""
     if out is not None:
         y, h, mean, rstd = out
     else:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
         h, mean, rstd = _stats(x, _flat(x, "x")[0], residual)
-    _norm("fp8q_layernorm", x, weight, bias, y, None, residual, None if h is x else h, mean, rstd, eps, None, None)
+    _norm("fp8q_layernorm", x, weight, bias, y, None, residual, None if h is x and residual is None else h, mean, rstd, eps, None, None)
     return y, h, mean, rstd
 
 
@@ -309,7 +310,7 @@ def layernorm_cast(x, weight, bias=None, residual=None, eps=1e-5, fp8_format="e4
         s = torch.empty((rows,) if per_channel_scale else (rows, cols // 128), dtype=torch.float32, device=x.device)
         h, mean, rstd = _stats(x, rows, residual)
     name = "fp8q_layernorm_cast_per_channel" if per_channel_scale else "fp8q_layernorm_cast_group128"
-    _norm(name, x, weight, bias, q, s, residual, None if h is x else h, mean, rstd, eps, fp8_format, None)
+    _norm(name, x, weight, bias, q, s, residual, None if h is x and residual is None else h, mean, rstd, eps, fp8_format, None)
     return q, s, h, mean, rstd
 
 

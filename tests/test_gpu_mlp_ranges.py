@@ -206,6 +206,19 @@ def test_codes_without_a_type_and_workspaces_of_their_size(M, xf, wf):
     assert all(torch.equal(a, c) for a, c in zip(want, got))
 
 
+@pytest.mark.parametrize("rows,cols", [(5, 7168), (300, 200), (3, 1003), (2, 33333)])
+def test_one_tensor_as_x_and_residual(rows, cols):
+    g = gen_of("twice", cols)
+    x, w, b = rand(g, rows, cols).bfloat16(), (1 + rand(g, cols)).bfloat16(), rand(g, cols).bfloat16()
+    want = fq.layernorm(up(x), up(w), up(b), up(x))
+    xd = up(x)
+    new = lambda: G.empty(rows, dtype=torch.float32)
+    y = G.empty((rows, cols), dtype=torch.bfloat16)
+    got = fq.layernorm(xd, up(w), up(b), xd, out=(y, xd, new(), new()))
+    assert all(torch.equal(a, c) for a, c in zip(want, got))
+    assert torch.equal(xd.cpu(), (x.float() * 2).bfloat16())
+
+
 @pytest.mark.parametrize("cols", [7168, 7171])
 def test_layernorm_offsets_past_32_bits(cols):
     """rows at the far end are what a call on them alone gives; dweight and dbias
