@@ -553,5 +553,5 @@ globals().update({_n: getattr(_ffn, _n) for _n in _ffn.FFN_NAMES})
 
 from . import _mlp  # noqa: E402
 
-_mlp._bind(lib, dict(_check=_check, _dev=_dev, _fmt=_fmt, _fp8=_fp8, _FP8_DTYPE=_FP8_DTYPE))
+_mlp._bind(lib, dict(_check=_check, _dev=_dev, _fmt=_fmt, _fp8=_fp8, _FP8_DTYPE=_FP8_DTYPE, _FMT=_FMT))
 globals().update({_n: getattr(_mlp, _n) for _n in _mlp.MLP_NAMES})

@@ -15,11 +15,12 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from functools import lru_cache
 
 import torch
 
 from . import _ffn
-from ._ffn import _AUTO, _CODES, _flat, _formats, _hp_dtype, _raw_stream, _same, _ws
+from ._ffn import _AUTO, _CODES, _flat, _hp_dtype, _raw_stream, _ws
 
 MLP_HEADER_PATH = os.path.join(os.path.dirname(_ffn.FFN_HEADER_PATH), "fp8q_mlp.h")
 
@@ -59,7 +60,7 @@ def mlp_header_functions() -> list:
 
 
 # set by the package once its own marshalling helpers exist
-lib = _check = _dev = _fmt = _fp8 = _FP8_DTYPE = None
+lib = _check = _dev = _fmt = _fp8 = _FP8_DTYPE = _FMT = None
 
 
 def _bind(package_lib, helpers):
@@ -68,8 +69,48 @@ def _bind(package_lib, helpers):
     globals().update(helpers)
 
 
-# As in _ffn.py, a call on one token is bound by its host time.  `d` is the
+# As in _ffn.py, a call on one token is bound by its host time, so each tensor is
+# asked what it is in one go, and again only to say what is wrong.  `d` is the
 # device of the call's first tensor (-1: the host), which every tensor has to be on.
+
+_F32 = torch.float32
+
+
+def _ten(t, n, dtype, name, d) -> int:
+    """the address of n contiguous elements of dtype on device d (0 without a tensor)"""
+    if t is None:
+        return 0
+    try:
+        if t.dtype is dtype and t.numel() == n and t.get_device() == d and t.is_contiguous() and d >= 0:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor) and (t.dtype != dtype or t.numel() != n):
+        raise ValueError(f"{name} must be {dtype} with {n} elements")
+    return _at(t, name, d)
+
+
+def _format(t, fmt, name) -> int:
+    """the format of fp8 codes; fmt names that of uint8 ones"""
+    f = _FMT.get(t.dtype)
+    return f if f is not None and (fmt is None or _FMT.get(fmt) == f) else _fp8(t, fmt, name)
+
+
+# sizes alone decide a workspace's bytes
+@lru_cache(maxsize=4096)
+def _norm_ws_bytes(rows, cols):
+    return lib.fp8q_layernorm_backward_workspace_bytes(rows, cols)
+
+
+@lru_cache(maxsize=4096)
+def _act_ws_bytes(M, N, K, cast):
+    return lib.fp8q_linear_act_workspace_bytes(M, N, K, cast)
+
+
+@lru_cache(maxsize=4096)
+def _bwd_ws_bytes(M, N, K):
+    return lib.fp8q_linear_act_backward_workspace_bytes(M, N, K)
+
 
 def _at(t, name, d) -> int:
     """the address of a contiguous tensor on device d (0 of an empty one)"""
@@ -86,12 +127,6 @@ def _at(t, name, d) -> int:
 
 def _opt(t, name, d) -> int:
     return 0 if t is None else _at(t, name, d)
-
-
-def _f32(t, numel, name, d) -> int:
-    if t.dtype != torch.float32 or t.numel() != numel:
-        raise ValueError(f"{name} must be float32 with {numel} elements")
-    return _at(t, name, d)
 
 
 def _stream(stream, d):
@@ -119,28 +154,18 @@ def _call(name, d, *args):
 # ---------------------------------------------------------------------------
 
 def _norm(name, x, weight, bias, y, scale_inv, residual, h, mean, rstd, eps, fmt, stream):
-    rows, cols = shape = _flat(x, "x")
-    dt, wdt, d = _hp_dtype(x, "x"), _hp_dtype(weight, "weight"), x.get_device()
-    if weight.numel() != cols:
-        raise ValueError(f"{name}: weight must have x's last dimension")
-    if bias is not None and (bias.numel() != cols or bias.dtype != weight.dtype):
-        raise ValueError(f"{name}: bias must match weight")
-    if residual is not None:
-        _same(residual, shape, x.dtype, "residual")
-    if h is not None:
-        _same(h, shape, x.dtype, "h")
+    rows, cols = _flat(x, "x")
+    n, T, W, d = rows * cols, x.dtype, weight.dtype, x.get_device()
+    dt, wdt = _hp_dtype(x, "x"), _hp_dtype(weight, "weight")
+    w, b = _ten(weight, cols, W, "weight", d), _ten(bias, cols, W, "bias", d)
+    r, ho = _ten(residual, n, T, "residual", d), _ten(h, n, T, "h", d)
     if name == "fp8q_layernorm":
-        _same(y, shape, x.dtype, "y")
-        out = (_at(y, "y", d),)
+        out = (_ten(y, n, T, "y", d),)
     else:
-        f = _fp8(y, fmt, "q")
-        if y.numel() != rows * cols:
-            raise ValueError(f"{name}: q must match x")
         scales = rows if name == "fp8q_layernorm_cast_per_channel" else rows * (cols // 128)
-        out = (f, _at(y, "q", d), _f32(scale_inv, scales, "scale_inv", d))
-    _call(name, d, _at(x, "x", d), dt, _opt(residual, "residual", d), _at(weight, "weight", d), _opt(bias, "bias", d), wdt,
-          rows, cols, eps, *out, _opt(h, "h", d), 0 if mean is None else _f32(mean, rows, "mean", d),
-          0 if rstd is None else _f32(rstd, rows, "rstd", d), _stream(stream, d))
+        out = (_format(y, fmt, "q"), _ten(y, n, y.dtype, "q", d), _ten(scale_inv, scales, _F32, "scale_inv", d))
+    _call(name, d, _at(x, "x", d), dt, r, w, b, wdt, rows, cols, eps, *out, ho, _ten(mean, rows, _F32, "mean", d),
+          _ten(rstd, rows, _F32, "rstd", d), _stream(stream, d))
 
 
 def fp8q_layernorm(x, weight, bias, y, residual=None, h=None, mean=None, rstd=None, eps=1e-5, stream=None) -> None:
@@ -164,20 +189,15 @@ def fp8q_layernorm_backward_workspace_bytes(rows: int, cols: int) -> int:
 def fp8q_layernorm_backward(dy, h, weight, mean, rstd, dx, dweight=None, dbias=None, dh=None, workspace=None,
                             stream=None) -> None:
     name = "fp8q_layernorm_backward"
-    rows, cols = shape = _flat(h, "h")
-    dt, wdt, d = _hp_dtype(h, "h"), _hp_dtype(weight, "weight"), h.get_device()
-    for t, n in ((dy, "dy"), (dx, "dx"), (dh, "dh")):
-        _same(t, shape, h.dtype, n)
-    if weight.numel() != cols:
-        raise ValueError(f"{name}: weight must have h's last dimension")
-    for t, n in ((dweight, "dweight"), (dbias, "dbias")):
-        if t is not None and (t.numel() != cols or t.dtype != weight.dtype):
-            raise ValueError(f"{name}: {n} must match weight")
-    need = lib.fp8q_layernorm_backward_workspace_bytes(rows, cols) if dweight is not None or dbias is not None else 0
+    rows, cols = _flat(h, "h")
+    n, T, W, d = rows * cols, h.dtype, weight.dtype, h.get_device()
+    dt, wdt = _hp_dtype(h, "h"), _hp_dtype(weight, "weight")
+    need = _norm_ws_bytes(rows, cols) if dweight is not None or dbias is not None else 0
     ws = _ws(workspace, need, h, name)
-    _call(name, d, _at(dy, "dy", d), _at(h, "h", d), dt, _at(weight, "weight", d), wdt, _f32(mean, rows, "mean", d),
-          _f32(rstd, rows, "rstd", d), _opt(dh, "dh", d), rows, cols, _at(dx, "dx", d), _opt(dweight, "dweight", d),
-          _opt(dbias, "dbias", d), _opt(ws, "workspace", d), _stream(stream, d))
+    _call(name, d, _ten(dy, n, T, "dy", d), _at(h, "h", d), dt, _ten(weight, cols, W, "weight", d), wdt,
+          _ten(mean, rows, _F32, "mean", d), _ten(rstd, rows, _F32, "rstd", d), _ten(dh, n, T, "dh", d), rows, cols,
+          _ten(dx, n, T, "dx", d), _ten(dweight, cols, W, "dweight", d), _ten(dbias, cols, W, "dbias", d),
+          _opt(ws, "workspace", d), _stream(stream, d))
 
 
 def _activation(name) -> int:
@@ -186,32 +206,21 @@ def _activation(name) -> int:
     return _ACT[name]
 
 
-def _typed(t, shape, name, d):
-    """pointer and type of an optional [M, N] tensor of any element type"""
-    if t is None:
-        return 0, 0
-    _same(t, shape, t.dtype, name)
-    return _at(t, name, d), _hp_dtype(t, name)
+def _typed(t, n, name, d):
+    """pointer and type of an optional tensor of n elements of any element type"""
+    return (0, 0) if t is None else (_ten(t, n, t.dtype, name, d), _hp_dtype(t, name))
 
 
 def _codes(x, xs, w, ws, x_fmt, w_fmt):
     """the operands' arguments with the sizes, and M, N, K and the device"""
-    xf, wf = _formats(x, x_fmt, w_fmt, w)
+    xf, wf = _format(x, x_fmt, "x"), _format(w, w_fmt, "the weight")
     M, K = _flat(x, "x")
     d = x.get_device()
     if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be 2-D with {K} columns")
     N, KB = w.shape[0], K // 128
-    return (_at(x, "x", d), xf, _f32(xs, M * KB, "x_scale_inv", d), _at(w, "w", d), wf,
-            _f32(ws, ((N + 127) // 128) * KB, "the weight's scale_inv", d), M, N, K), M, N, K, d
-
-
-def _bias(name, bias, N, d):
-    if bias is None:
-        return 0, 0
-    if bias.numel() != N:
-        raise ValueError(f"{name}: bias must have w's rows")
-    return _at(bias, "bias", d), _hp_dtype(bias, "bias")
+    return (_at(x, "x", d), xf, _ten(xs, M * KB, _F32, "x_scale_inv", d), _at(w, "w", d), wf,
+            _ten(ws, ((N + 127) // 128) * KB, _F32, "the weight's scale_inv", d), M, N, K), M, N, K, d
 
 
 def fp8q_linear_act_workspace_bytes(M: int, N: int, K: int, cast: bool) -> int:
@@ -223,11 +232,10 @@ def fp8q_linear_act(x, x_scale_inv, w, w_scale_inv, bias, y, residual=None, z=No
     name = "fp8q_linear_act"
     act = _activation(activation)
     args, M, N, K, d = _codes(x, x_scale_inv, w, w_scale_inv, x_fmt, w_fmt)
-    if residual is not None:
-        _same(residual, (M, N), y.dtype, "residual")
-    scratch = _ws(workspace, lib.fp8q_linear_act_workspace_bytes(M, N, K, 0), x, name)
-    _call(name, d, *args, *_bias(name, bias, N, d), act, _opt(residual, "residual", d), *_typed(y, (M, N), "y", d),
-          *_typed(z, (M, N), "z", d), _opt(scratch, "workspace", d), _stream(stream, d))
+    n = M * N
+    scratch = _ws(workspace, _act_ws_bytes(M, N, K, 0), x, name)
+    _call(name, d, *args, *_typed(bias, N, "bias", d), act, _ten(residual, n, y.dtype, "residual", d),
+          *_typed(y, n, "y", d), *_typed(z, n, "z", d), _opt(scratch, "workspace", d), _stream(stream, d))
 
 
 def fp8q_linear_act_cast(x, x_scale_inv, w, w_scale_inv, bias, q, scale_inv, z=None, activation=None, fmt=None,
@@ -235,14 +243,12 @@ def fp8q_linear_act_cast(x, x_scale_inv, w, w_scale_inv, bias, q, scale_inv, z=N
     name = "fp8q_linear_act_cast"
     act = _activation(activation)
     args, M, N, K, d = _codes(x, x_scale_inv, w, w_scale_inv, x_fmt, w_fmt)
-    f = _fp8(q, fmt, "q")
-    if q.numel() != M * N:
-        raise ValueError(f"{name}: q must have M x N elements")
-    if N % 128 == 0 and (scale_inv.dtype != torch.float32 or scale_inv.numel() != M * (N // 128)):
-        raise ValueError(f"scale_inv must be float32 with {M * (N // 128)} elements")
-    scratch = _ws(workspace, lib.fp8q_linear_act_workspace_bytes(M, N, K, 1), x, name)
-    _call(name, d, *args, *_bias(name, bias, N, d), act, f, _at(q, "q", d), _at(scale_inv, "scale_inv", d),
-          *_typed(z, (M, N), "z", d), _opt(scratch, "workspace", d), _stream(stream, d))
+    n = M * N
+    f, codes = _format(q, fmt, "q"), _ten(q, n, q.dtype, "q", d)
+    scales = _ten(scale_inv, n // 128, _F32, "scale_inv", d) if N % 128 == 0 else 0     # else the call is refused
+    scratch = _ws(workspace, _act_ws_bytes(M, N, K, 1), x, name)
+    _call(name, d, *args, *_typed(bias, N, "bias", d), act, f, codes, scales, *_typed(z, n, "z", d),
+          _opt(scratch, "workspace", d), _stream(stream, d))
 
 
 def fp8q_linear_act_backward_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -254,22 +260,16 @@ def fp8q_linear_act_backward(dy, z, x, x_scale_inv, w, w_scale_inv, dx=None, dw=
     name = "fp8q_linear_act_backward"
     act, g = _activation(activation), _ffn._grad_dtype((dw, dbias))
     args, M, N, K, d = _codes(x, x_scale_inv, w, w_scale_inv, x_fmt, w_fmt)
-    dt = _hp_dtype(dy, "dy")
-    _same(dy, (M, N), dy.dtype, "dy")
-    _same(dx, (M, K), dy.dtype, "dx")
+    T, dt, n = dy.dtype, _hp_dtype(dy, "dy"), M * N
     if act == IDENTITY:
         z = None
     elif z is None:
         raise ValueError(f"{name}: an activation's gradient needs z")
-    _same(z, (M, N), dy.dtype, "z")
-    if dw is not None:
-        _same(dw, (N, K), dw.dtype, "dw")
-    if dbias is not None and dbias.numel() != N:
-        raise ValueError(f"{name}: dbias must have w's rows")
-    gdt = dt if g is None else _hp_dtype(dw if dw is not None else dbias, "dw")
-    scratch = _ws(workspace, lib.fp8q_linear_act_backward_workspace_bytes(M, N, K), x, name)
-    _call(name, d, _at(dy, "dy", d), _opt(z, "z", d), dt, *args, act, _opt(dx, "dx", d), _opt(dw, "dw", d),
-          _opt(dbias, "dbias", d), gdt, _opt(scratch, "workspace", d), _stream(stream, d))
+    GT, gdt = (T, dt) if g is None else (g, _hp_dtype(dw if dw is not None else dbias, "dw"))
+    scratch = _ws(workspace, _bwd_ws_bytes(M, N, K), x, name)
+    _call(name, d, _ten(dy, n, T, "dy", d), _ten(z, n, T, "z", d), dt, *args, act, _ten(dx, M * K, T, "dx", d),
+          _ten(dw, N * K, GT, "dw", d), _ten(dbias, N, GT, "dbias", d), gdt, _opt(scratch, "workspace", d),
+          _stream(stream, d))
 
 
 # ---------------------------------------------------------------------------
@@ -277,8 +277,8 @@ def fp8q_linear_act_backward(dy, z, x, x_scale_inv, w, w_scale_inv, dx=None, dw=
 # ---------------------------------------------------------------------------
 
 def _stats(x, rows, residual):
-    f = lambda: torch.empty(rows, dtype=torch.float32, device=x.device)
-    return x if residual is None else torch.empty_like(x, memory_format=torch.contiguous_format), f(), f()
+    mean = torch.empty(rows, dtype=_F32, device=x.device)
+    return x if residual is None else torch.empty_like(x, memory_format=torch.contiguous_format), mean, torch.empty_like(mean)
 
 
 def layernorm(x, weight, bias=None, residual=None, eps=1e-5, out=None):
@@ -306,7 +306,7 @@ def layernorm_cast(x, weight, bias=None, residual=None, eps=1e-5, fp8_format="e4
     if out is not None:
         q, s, h, mean, rstd = out
     else:
-        q = torch.empty(x.shape, dtype=_FP8_DTYPE[_fmt(fp8_format)], device=x.device)
+        q = torch.empty_like(x, dtype=_FP8_DTYPE[_fmt(fp8_format)], memory_format=torch.contiguous_format)
         s = torch.empty((rows,) if per_channel_scale else (rows, cols // 128), dtype=torch.float32, device=x.device)
         h, mean, rstd = _stats(x, rows, residual)
     name = "fp8q_layernorm_cast_per_channel" if per_channel_scale else "fp8q_layernorm_cast_group128"

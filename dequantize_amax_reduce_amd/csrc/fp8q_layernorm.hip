@@ -164,7 +164,10 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
     };
     load(first);
     if (NW) clear_sums<3 * NW>(lds_s);
-    constexpr bool HOLD = V <= 1;                           // four vectors leave no registers for them
+    // Weights are held across the rows where registers are left for them: not beside
+    // four vectors, nor binary32 ones beside 16-bit rows' casts in 64 registers (16384 x
+    // 7168 bf16, group and row cast: 178 and 202 us held, with spills, 166 and 178 not).
+    constexpr bool HOLD = V <= 1 && !(Affine<DT, WF32>::kWide && TO != kToPlain && !WAVE && TB > 256);
     Affine<DT, WF32> w[V], b[V];
     auto load_wb = [&](int v) {
         w[v].load(a.w, place(v).c);

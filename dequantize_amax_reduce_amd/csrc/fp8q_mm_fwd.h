@@ -578,21 +578,21 @@ template <int V, bool CAST, bool ACT = false> __global__ void __launch_bounds__(
                         if (s + j < a.splits) g[k] += t[j][k];
             }
         else
-        for (int s = 0; s < a.splits; ++s, p += a.M * W) {
-            if constexpr (V == 4) {
-                const v4f x = *(const v4f*)p;
+            for (int s = 0; s < a.splits; ++s, p += a.M * W) {
+                if constexpr (V == 4) {
+                    const v4f x = *(const v4f*)p;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) g[k] += x[k];
-                if (a.gated) {
-                    const v4f y = *(const v4f*)(p + a.N);
+                    for (int k = 0; k < 4; ++k) g[k] += x[k];
+                    if (a.gated) {
+                        const v4f y = *(const v4f*)(p + a.N);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) u[k] += y[k];
+                        for (int k = 0; k < 4; ++k) u[k] += y[k];
+                    }
+                } else {
+                    g[0] += p[0];
+                    if (a.gated) u[0] += p[a.N];
                 }
-            } else {
-                g[0] += p[0];
-                if (a.gated) u[0] += p[a.N];
             }
-        }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             if (ACT && a.bias) g[k] += load1(a.bias, a.bdt, n + k);

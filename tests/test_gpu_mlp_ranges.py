@@ -117,6 +117,11 @@ def test_slopes_at_every_argument(act, dt, top):
                                 torch.empty(N, 0, dtype=E, device="cuda"), none, None, None, db, act, ws)
     d = slope64(act, z64)
     near(db, top * d, top * slope_tol(act, z64, d) + TINY, "dbias")
+    if act:
+        far = torch.tensor([[float("-inf"), float("inf")]]).to(b.dtype)
+        fq.fp8q_linear_act_backward(up(dy[:, :2]), up(far), torch.empty(1, 0, dtype=E, device="cuda"), none,
+                                    torch.empty(2, 0, dtype=E, device="cuda"), none, None, None, db[:2], act, ws)
+        assert db[:2].tolist() == [0.0, top]
 
 
 FAR = {"silu": -100.0, "gelu": -13.0, "gelu_tanh": -9.0}
