@@ -23,41 +23,44 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-// The sum over a wave's lanes, in every lane: within rows of 16 lanes and then
-// across rows by DPP, which needs no LDS access as shuffles do.
+// x of another lane by DPP, which needs no LDS access as shuffles do; 0 in rows left out
+template <int CTRL, int ROWS = 0xF> __device__ __forceinline__ float dpp(float x) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, ROWS, 0xF, false));
+}
+// the sum over each 4, 8 or 16 consecutive lanes, in all of them
+template <int LANES> __device__ __forceinline__ float part_sum(float v) {
+    v += dpp<0xB1>(v);                                      // quad_perm [1,0,3,2]
+    v += dpp<0x4E>(v);                                      // quad_perm [2,3,0,1]
+    if constexpr (LANES >= 8) v += dpp<0x141>(v);           // row_half_mirror
+    if constexpr (LANES >= 16) v += dpp<0x140>(v);          // row_mirror
+    return v;
+}
+// the sum over a wave's lanes, in every lane
 __device__ __forceinline__ float lane_sum(float v) {
-    auto dpp = [](float x, auto ctrl, auto rows) {          // x of another lane; 0 in rows left out
-        return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::value,
-                                                                     decltype(rows)::value, 0xF, false));
-    };
-    v += dpp(v, KC<0xB1>{}, KC<0xF>{});                     // quad_perm [1,0,3,2]
-    v += dpp(v, KC<0x4E>{}, KC<0xF>{});                     // quad_perm [2,3,0,1]
-    v += dpp(v, KC<0x141>{}, KC<0xF>{});                    // row_half_mirror
-    v += dpp(v, KC<0x140>{}, KC<0xF>{});                    // row_mirror
-    v += dpp(v, KC<0x142>{}, KC<0xA>{});                    // row_bcast:15 into rows 1 and 3
-    v += dpp(v, KC<0x143>{}, KC<0xC>{});                    // row_bcast:31 into rows 2 and 3
+    v = part_sum<16>(v);
+    v += dpp<0x142, 0xA>(v);                                // row_bcast:15 into rows 1 and 3
+    v += dpp<0x143, 0xC>(v);                                // row_bcast:31 into rows 2 and 3
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
 // Sums of N values over the lanes of a row: one wave (NW = 0), or a workgroup of
-// up to NW waves through lds, N x NW words of which those of waves that are not
-// there are zero (clear_sums).  The words may be written again after the
-// workgroup's next barrier.
+// up to NW waves through lds, N x sum_words(NW) words of which those of waves that
+// are not there are zero (clear_sums).  The words may be written again after the
+// workgroup's next barrier.  Each lane reads one wave's sum and adds by DPP: a sum
+// takes 4 additions, where all of them in every lane took 15, a tenth of the
+// instructions of a row of 7168.
+constexpr int sum_words(int nw) { return nw <= 4 ? 4 : nw <= 8 ? 8 : 16; }
 template <int NW, int N> __device__ __forceinline__ void row_sums(float (&v)[N], float* lds) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = lane_sum(v[i]);
     if constexpr (NW > 0) {
+        constexpr int W = sum_words(NW);
         if ((threadIdx.x & 63) == 0)
 #pragma unroll
-            for (int i = 0; i < N; ++i) lds[i * NW + (threadIdx.x >> 6)] = v[i];
+            for (int i = 0; i < N; ++i) lds[i * W + (threadIdx.x >> 6)] = v[i];
         lds_barrier();
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v4f s = *(const v4f*)(lds + i * NW);
-#pragma unroll
-            for (int j = 4; j < NW; j += 4) s += *(const v4f*)(lds + i * NW + j);
-            v[i] = (s.x + s.y) + (s.z + s.w);
-        }
+        for (int i = 0; i < N; ++i) v[i] = part_sum<W>(lds[i * W + (threadIdx.x & (W - 1))]);
     }
 }
 // before the first of them, by every thread
@@ -66,10 +69,14 @@ template <int WORDS> __device__ __forceinline__ void clear_sums(float* lds) {
     __syncthreads();
 }
 
-// rstd from the mean of d^2 and that of d (a NaN passes the clamp)
-__device__ __forceinline__ float rstd_of(float s2, float m1, float n, float eps) {
-    const float v = s2 / n - m1 * m1;
-    return 1.0f / sqrtf((v < 0.0f ? 0.0f : v) + eps);
+// rstd from the sum of d^2 and the mean of d, rn = 1 / n (a NaN passes the clamp).
+// The instruction is within 2^-23 and takes subnormal values as 0.
+__device__ __forceinline__ float rstd_of(float s2, float m1, float rn, float eps) {
+    float v = s2 * rn - m1 * m1;
+    v = (v < 0.0f ? 0.0f : v) + eps;
+    const bool tiny = v < 0x1p-100f;
+    const float r = __builtin_amdgcn_rsqf(tiny ? v * 0x1p100f : v);
+    return tiny ? r * 0x1p50f : r;
 }
 
 // y of one lane vector from d = h - m0
@@ -141,11 +148,11 @@ template <int DT, bool WF32, int FMT, int TO, bool WHOLE, bool WAVE, int V, int 
 __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
     constexpr bool PF = V == 1 || (V == 2 && TB <= 768), NT = WHOLE;
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
-    constexpr int NW = WAVE ? 0 : TB / 64;
-    __shared__ __attribute__((aligned(16))) float lds_s[3 * (NW ? NW : 1)];
+    constexpr int NW = WAVE ? 0 : TB / 64, SW = NW ? sum_words(NW) : 1;
+    __shared__ float lds_s[3 * SW];
     __shared__ uint32_t lds_m[16];
     const int cols = (int)a.cols;
-    const float fc = (float)cols;
+    const float rn = 1.0f / (float)cols;
     const int lanes = WAVE ? 64 : (int)blockDim.x;
     const int t = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
     const int per = WAVE ? (int)blockDim.x >> 6 : 1;        // rows a workgroup takes at once
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
         }
     };
     load(first);
-    if (NW) clear_sums<3 * NW>(lds_s);
+    if (NW) clear_sums<3 * SW>(lds_s);
     // Weights are held across the rows where registers are left for them: not beside
     // four vectors, nor binary32 ones beside 16-bit rows' casts in 64 registers (16384 x
     // 7168 bf16, group and row cast: 178 and 202 us held, with spills, 166 and 178 not).
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
         }
         if (PF && row + next < a.rows) load(row + next);
         row_sums<NW>(s, lds_s);
-        const float m0 = s[0] / fc;
+        const float m0 = s[0] * rn;
         if (a.h) {
             void* hr = (char*)a.h + row * a.cols * ES;
 #pragma unroll
@@ -215,8 +222,8 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
             d2[0] += WHOLE && dup[v] ? 0.0f : p;
             d2[1] += WHOLE && dup[v] ? 0.0f : q;
         }
-        row_sums<NW>(d2, lds_s + NW);
-        const float m1 = d2[0] / fc, rs = rstd_of(d2[1], m1, fc, a.eps);
+        row_sums<NW>(d2, lds_s + SW);
+        const float m1 = d2[0] * rn, rs = rstd_of(d2[1], m1, rn, a.eps);
         if (t == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;
@@ -273,11 +280,11 @@ __device__ __forceinline__ void put_y(const LayerNorm& a, int64_t row, int c, co
 // same columns, so that they may be x or the residual itself.
 template <int DT, bool WF32, int FMT, int TO> __global__ void __launch_bounds__(1024) k_ln_long(LayerNorm a) {
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
-    __shared__ __attribute__((aligned(16))) float lds_s[48];
+    __shared__ float lds_s[48];
     __shared__ uint32_t lds_m[16];
     clear_sums<48>(lds_s);
     const int cols = (int)a.cols, step = (int)blockDim.x * VE, c0 = (int)threadIdx.x * VE;
-    const float fc = (float)cols;
+    const float rn = 1.0f / (float)cols;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t off = row * a.cols * ES;
         const void* xr = (const char*)a.x + off;
@@ -290,7 +297,7 @@ template <int DT, bool WF32, int FMT, int TO> __global__ void __launch_bounds__(
             for (int k = 0; k < VE; ++k) s[0] += h[k];
         }
         row_sums<16>(s, lds_s);
-        const float m0 = s[0] / fc;
+        const float m0 = s[0] * rn;
         // d of the columns from c on, zero past the row's end
         auto diff = [&](int64_t c, float* d) {
             load_h<DT>(xr, rr, (int)c, cols, d);
@@ -308,7 +315,7 @@ template <int DT, bool WF32, int FMT, int TO> __global__ void __launch_bounds__(
             }
         }
         row_sums<16>(d2, lds_s + 16);
-        const float m1 = d2[0] / fc, rs = rstd_of(d2[1], m1, fc, a.eps);
+        const float m1 = d2[0] * rn, rs = rstd_of(d2[1], m1, rn, a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;
@@ -372,10 +379,10 @@ template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB
     constexpr bool PF = TB <= 512;
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value, Q = VE / 4;
     extern __shared__ v4f sums[];                           // [2][V][Q][T]: 4 columns each of dweight, then of dbias
-    constexpr int NW = TB / 64;
-    __shared__ __attribute__((aligned(16))) float lds[2][2 * NW];
+    constexpr int NW = TB / 64, SW = sum_words(NW);
+    __shared__ float lds[2][2 * SW];
     const int T = (int)blockDim.x, t = (int)threadIdx.x, cols = (int)a.cols;
-    const float fc = (float)cols;
+    const float rn = 1.0f / (float)cols;
     auto place = [&](int v) { return Place<VE>((v * T + t) * VE, cols); };
     auto sum = [&](int which, int v, int q) -> v4f& { return sums[((which * V + v) * Q + q) * T + t]; };
     Affine<DT, WF32> w[V];
@@ -407,7 +414,7 @@ template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB
         for (int k = 0; k < VE; ++k) n[k] = (n[k] - mu) * rs;
     };
     if ((int64_t)blockIdx.x < a.rows) load(blockIdx.x);
-    clear_sums<4 * NW>(lds[0]);
+    clear_sums<4 * SW>(lds[0]);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
         const int64_t off = row * a.cols * ES;
         rs = rsn;
@@ -460,7 +467,7 @@ template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB
 #pragma unroll
             for (int v = 0; v < V; ++v) asm volatile("" : "+v"(dhr[v]));
         row_sums<NW>(s, lds[flip]);
-        const float m1 = s[0] / fc, m2 = s[1] / fc;
+        const float m1 = s[0] * rn, m2 = s[1] * rn;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float wv[VE], n[VE], dy[VE], o[VE];
@@ -501,10 +508,10 @@ template <int DT, bool WF32, int V, int TB> __global__ void __launch_bounds__(TB
 template <int DT, bool WF32> __global__ void __launch_bounds__(1024) k_ln_bwd_long(LnBwdArgs g) {
     const LayerNormBwd& a = g.f;
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
-    __shared__ __attribute__((aligned(16))) float lds[2][32];
+    __shared__ float lds[2][32];
     clear_sums<64>(lds[0]);
     const int cols = (int)a.cols, step = (int)blockDim.x * VE, c0 = (int)threadIdx.x * VE;
-    const float fc = (float)cols;
+    const float rn = 1.0f / (float)cols;
     float* pw = g.pw ? g.pw + (int64_t)blockIdx.x * a.cols : nullptr;
     float* pb = g.pb ? g.pb + (int64_t)blockIdx.x * a.cols : nullptr;
     for (float* p : {pw, pb})
@@ -537,7 +544,7 @@ template <int DT, bool WF32> __global__ void __launch_bounds__(1024) k_ln_bwd_lo
             }
         }
         row_sums<16>(s, lds[flip]);
-        const float m1 = s[0] / fc, m2 = s[1] / fc;
+        const float m1 = s[0] * rn, m2 = s[1] * rn;
         for (int64_t c = c0; c < cols; c += step) {
             float dy[VE], w[VE], n[VE], o[VE];
             load(c, dy, w, n);
