@@ -7,6 +7,9 @@
 //
 // Bound by HBM: x and r are read once, h and y (or its codes and scales)
 // written once.  A row stays in registers between its reductions, as binary32.
+// The instructions are close behind: 41 an element (a quarter of them the three sums
+// over the workgroup and their divisions) took 160 to 180 us for 16384 x 7168 as the
+// clock fell under load, 31 take 149.
 //
 // The mean is m0 + m1: m0 the rounded mean of h, m1 the mean of d = h - m0,
 // which is exact where h is near m0; the variance is mean(d^2) - m1^2.  So a
@@ -140,9 +143,9 @@ template <int DT, bool NT> __device__ __forceinline__ void st_at(void* row, int 
 // thread.  A workgroup takes several rows, so that the next row's loads are in
 // flight through the reductions and stores of this one, where V and the threads
 // leave registers for that.  WHOLE: rows of whole 128-byte lines, streamed past
-// the caches, and without a mask on every element (16384 x 7168 bf16 with
-// residual and group cast: 155 us with masks, 149 without, 5.5 TB/s; 1999 x 5001
-// f32 17.1 us).  A reduction's LDS words are written again after another
+// the caches, and without a mask on every element (6 us more of 16384 x 7168 bf16
+// with residual and group cast, which takes 146, 5.7 TB/s; 1999 x 5001 f32 16.1).
+// A reduction's LDS words are written again after another
 // reduction's barrier.
 template <int DT, bool WF32, int FMT, int TO, bool WHOLE, bool WAVE, int V, int TB>
 __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
@@ -171,10 +174,7 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
     };
     load(first);
     if (NW) clear_sums<3 * SW>(lds_s);
-    // Weights are held across the rows where registers are left for them: not beside
-    // four vectors, nor binary32 ones beside 16-bit rows' casts in 64 registers (16384 x
-    // 7168 bf16, group and row cast: 178 and 202 us held, with spills, 166 and 178 not).
-    constexpr bool HOLD = V <= 1 && !(Affine<DT, WF32>::kWide && TO != kToPlain && !WAVE && TB > 256);
+    constexpr bool HOLD = V <= 1;                           // four vectors leave no registers for them
     Affine<DT, WF32> w[V], b[V];
     auto load_wb = [&](int v) {
         w[v].load(a.w, place(v).c);
