@@ -6,9 +6,15 @@
  * The conventions of fp8q.h and fp8q_ffn.h hold (device pointers, dense
  * row-major tensors, fp8 activations and weights and their scales as there,
  * asynchronous on `stream`, arguments validated on the host before any HIP
- * call, no allocation, no state kept, the same limits, workspaces and
- * numerics; a row's result does not depend on the other rows), and the calling
- * thread's current device is the one that holds the tensors.
+ * call, no allocation, no state kept, the same limits and workspaces), and the
+ * calling thread's current device is the one that holds the tensors.
+ *
+ * Numerics are those of fp8q_ffn.h but for one thing: a projection whose outputs
+ * are all 16-bit uses the fp8 instruction from 17 rows on (fp8q_linear from 65),
+ * which adds a step's products within about 16 bits of the largest.  A binary32
+ * y or z, a cast, and up to 16 rows have binary32 sums.  A row's result does not
+ * depend on what the other rows hold; its last bits may depend on how many there
+ * are, which choose the tiles and the splits of a contraction.
  */
 #ifndef FP8Q_MLP_H
 #define FP8Q_MLP_H
@@ -39,7 +45,8 @@ extern "C" {
  * The mean is taken twice, the second time of the differences from the first,
  * so that rows far from zero lose nothing but h's own rounding.  Sums are
  * binary32: a row whose sum passes 3.4e38 gets NaN, and one whose differences
- * pass 1.8e19 gets rstd = 0, as an infinite variance gives it.
+ * pass 1.8e19 gets rstd = 0, as an infinite variance gives it.  Short rows are
+ * summed in another order where there are more than 256 of them.
  * rows == 0 is a no-op; cols == 0 is a no-op except that the per-channel form
  * writes scale_inv[r] = 1 (mean and rstd are not written).
  */
@@ -80,7 +87,7 @@ fp8q_status_t fp8q_layernorm_backward(const void* dy, const void* h, fp8q_dtype_
  *   fp8q_linear_act:      y = act(z) (+ residual), rounded once to ydtype;
  *   fp8q_linear_act_cast: q, scale_inv = the per-128-group cast of act(z) (from
  *     binary32, fp8q_cast_per_group128's rule); N % 128 != 0 -> FP8Q_ESHAPE.
- * act: any fp8q_act_t.  bias: [N] of bdtype, any element type, or NULL.
+ * act: any fp8q_act_t; act(-infinity) is 0 but of FP8Q_IDENTITY.  bias: [N] of bdtype, any element type, or NULL.
  * residual: [M, N] of ydtype, or NULL; y may be the residual itself (in place).
  * z (or NULL): [M, N] of zdtype, each value rounded once: what the backward
  * pass reads.  K == 0 gives z = bias; M == 0 or N == 0 is a no-op.
@@ -102,7 +109,8 @@ fp8q_status_t fp8q_linear_act_cast(const uint8_t* x, fp8q_fmt_t xfmt, const floa
  * residual's gradient is dy itself) and the forward's z [M, N]:
  *   dz = dy * act'(z) in binary32;  dx [M, K] = dz W;  dw [N, K] = dz^T X;
  *   dbias[n] = sum_m dz, in binary32 from the unrounded dz.
- * act' of FP8Q_RELU is 0 from 0 down.  With FP8Q_IDENTITY dz = dy and z is not
+ * act' of FP8Q_RELU is 0 from 0 down; at -infinity and infinity a slope is 0 and
+ * 1.  With FP8Q_IDENTITY dz = dy and z is not
  * read (it may be NULL).  dy and z are bf16 or f16 (FP8Q_F32 -> FP8Q_EDTYPE); dx
  * has their type, dw and dbias dwdtype: that type or FP8Q_F32.  dx, dw and dbias
  * may each be NULL (not computed).  The operands of the two products, their
