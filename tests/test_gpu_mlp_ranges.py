@@ -285,3 +285,35 @@ def test_backward_offsets_past_32_bits():
     near(db, dz.sum(0), a.sum(0) * 40 * U + ez.sum(0) + TINY, "dbias")
     dx[at] = 0
     assert not dx.any()
+
+
+def test_h_without_a_residual_is_a_copy():
+    g = gen_of("copy")
+    for cols in (200, 1003, 33333):
+        x, w = up(rand(g, 5, cols).bfloat16()), up(rand(g, cols).bfloat16())
+        h = G.full((5, cols), 7.0, dtype=torch.bfloat16)
+        new = lambda: G.empty(5, dtype=torch.float32)
+        y, h2, _, _ = fq.layernorm(x, w, out=(torch.empty_like(x), h, new(), new()))
+        assert h2 is h and torch.equal(h, x) and torch.equal(y, fq.layernorm(x, w)[0])
+
+
+def test_batches_of_more_dimensions():
+    """[2, 3, K] is the six rows of [6, K]"""
+    g = gen_of("3d")
+    K, N = 256, 384
+    x, r = up(rand(g, 6, K).bfloat16()), up(rand(g, 6, N).bfloat16())
+    nw, b = up(rand(g, K).bfloat16()), up(rand(g, N).bfloat16())
+    w = [up(t) for t in operands(g, 1, K, N)[2:]]
+
+    def run(x, r):
+        q, s, h, mean, rstd = fq.layernorm_cast(x, nw, None, x)
+        y, _ = fq.linear_act_fp8(q, s, *w, b, None, r)
+        p, ps, z = fq.linear_act_fp8_cast(q, s, *w, b, "silu", keep=torch.bfloat16)
+        dn, dw, db = fq.linear_act_fp8_backward(r, z, q, s, *w, "silu")
+        return (q, s, h, y, p, ps, z, dn, dw, db, *fq.layernorm_backward(dn, h, nw, mean, rstd, x))
+
+    flat, deep = run(x, r), run(x.view(2, 3, K), r.view(2, 3, N))
+    for a, c in zip(flat, deep):
+        assert torch.equal(a.view(torch.uint8).flatten(), c.view(torch.uint8).flatten())
+    for i, last in ((0, K), (2, K), (3, N), (4, N), (6, N), (7, K), (10, K)):
+        assert deep[i].shape == (2, 3, last)
