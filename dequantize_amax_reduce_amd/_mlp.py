@@ -293,7 +293,8 @@ def layernorm(x, weight, bias=None, residual=None, eps=1e-5, out=None):
     else:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
         h, mean, rstd = _stats(x, _flat(x, "x")[0], residual)
-    _norm("fp8q_layernorm", x, weight, bias, y, None, residual, None if h is x and residual is None else h, mean, rstd, eps, None, None)
+    _norm("fp8q_layernorm", x, weight, bias, y, None, residual, None if h is x and residual is None else h, mean, rstd,
+          eps, None, None)
     return y, h, mean, rstd
 
 
@@ -310,7 +311,8 @@ def layernorm_cast(x, weight, bias=None, residual=None, eps=1e-5, fp8_format="e4
         s = torch.empty((rows,) if per_channel_scale else (rows, cols // 128), dtype=torch.float32, device=x.device)
         h, mean, rstd = _stats(x, rows, residual)
     name = "fp8q_layernorm_cast_per_channel" if per_channel_scale else "fp8q_layernorm_cast_group128"
-    _norm(name, x, weight, bias, q, s, residual, None if h is x and residual is None else h, mean, rstd, eps, fp8_format, None)
+    _norm(name, x, weight, bias, q, s, residual, None if h is x and residual is None else h, mean, rstd, eps, fp8_format,
+          None)
     return q, s, h, mean, rstd
 
 
