@@ -72,6 +72,14 @@ template <int WORDS> __device__ __forceinline__ void clear_sums(float* lds) {
     __syncthreads();
 }
 
+// s / n from rn = 1 / n: exact where the quotient is a binary32 number, so that a
+// constant row, whose d are equal and add up exactly, has y = b to the last bit (and
+// zeros in a cast, whose scale would show whatever is left)
+__device__ __forceinline__ float mean_of(float s, float n, float rn) {
+    const float q = s * rn;
+    return __builtin_fmaf(__builtin_fmaf(-q, n, s), rn, q);
+}
+
 // rstd from the sum of d^2 and the mean of d, rn = 1 / n (a NaN passes the clamp).
 // The instruction is within 2^-23 and takes subnormal values as 0.
 __device__ __forceinline__ float rstd_of(float s2, float m1, float rn, float eps) {
@@ -155,7 +163,7 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
     __shared__ float lds_s[3 * SW];
     __shared__ uint32_t lds_m[16];
     const int cols = (int)a.cols;
-    const float rn = 1.0f / (float)cols;
+    const float fc = (float)cols, rn = 1.0f / fc;
     const int lanes = WAVE ? 64 : (int)blockDim.x;
     const int t = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
     const int per = WAVE ? (int)blockDim.x >> 6 : 1;        // rows a workgroup takes at once
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
             d2[1] += WHOLE && dup[v] ? 0.0f : q;
         }
         row_sums<NW>(d2, lds_s + SW);
-        const float m1 = d2[0] * rn, rs = rstd_of(d2[1], m1, rn, a.eps);
+        const float m1 = mean_of(d2[0], fc, rn), rs = rstd_of(d2[1], m1, rn, a.eps);
         if (t == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;
@@ -284,7 +292,7 @@ template <int DT, bool WF32, int FMT, int TO> __global__ void __launch_bounds__(
     __shared__ uint32_t lds_m[16];
     clear_sums<48>(lds_s);
     const int cols = (int)a.cols, step = (int)blockDim.x * VE, c0 = (int)threadIdx.x * VE;
-    const float rn = 1.0f / (float)cols;
+    const float fc = (float)cols, rn = 1.0f / fc;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t off = row * a.cols * ES;
         const void* xr = (const char*)a.x + off;
@@ -315,7 +323,7 @@ template <int DT, bool WF32, int FMT, int TO> __global__ void __launch_bounds__(
             }
         }
         row_sums<16>(d2, lds_s + 16);
-        const float m1 = d2[0] * rn, rs = rstd_of(d2[1], m1, rn, a.eps);
+        const float m1 = mean_of(d2[0], fc, rn), rs = rstd_of(d2[1], m1, rn, a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;

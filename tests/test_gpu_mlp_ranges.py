@@ -317,3 +317,18 @@ def test_batches_of_more_dimensions():
         assert torch.equal(a.view(torch.uint8).flatten(), c.view(torch.uint8).flatten())
     for i, last in ((0, K), (2, K), (3, N), (4, N), (6, N), (7, K), (10, K)):
         assert deep[i].shape == (2, 3, last)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("cols", [1, 7, 128, 130, 384, 1000, 5001, 7168, 20001, 40001])
+def test_constant_rows_leave_nothing(cols, dt):
+    """every element is its row's mean: y is the bias itself, and without one a
+    cast per row is zeros with the scale of zeros, whose amax counts as 1"""
+    g = gen_of("constant", cols)
+    x = (0.5 * rand(g, 300, 1)).to(TORCH_HP[dt]).expand(300, cols).contiguous()
+    w, b = (1 + 0.2 * rand(g, cols)).to(x.dtype), (0.2 * rand(g, cols)).to(x.dtype)
+    y, _, _, _ = fq.layernorm(up(x), up(w), up(b))
+    assert torch.equal(y.cpu(), b.expand(300, cols))
+    q, s, _, _, _ = fq.layernorm_cast(up(x), up(w), per_channel_scale=True)
+    assert not q.float().any()
+    assert torch.equal(s.cpu(), torch.ones(300) / 448.0)
