@@ -16,6 +16,7 @@
 // row of values far from zero keeps the bits that its deviations have in h.
 // (With m0 alone a constant row of 1000s, whose y is b, would be off by what
 // m0's rounding leaves: 6e-5 / sqrt(eps), 2 % of the weight at eps = 1e-5.)
+// Rows too long for registers have m0 + m1 from a binary64 sum.
 #include "fp8q_ffn_plan.h"
 #include "fp8q_mlp_launch.h"
 #include "fp8q_rows.h"
@@ -30,8 +31,23 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 template <int CTRL, int ROWS = 0xF> __device__ __forceinline__ float dpp(float x) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, ROWS, 0xF, false));
 }
+template <int CTRL, int ROWS = 0xF> __device__ __forceinline__ double dpp(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ float last_lane(float x) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 63));
+}
+__device__ __forceinline__ double last_lane(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
 // the sum over each 4, 8 or 16 consecutive lanes, in all of them
-template <int LANES> __device__ __forceinline__ float part_sum(float v) {
+template <int LANES, typename T> __device__ __forceinline__ T part_sum(T v) {
     v += dpp<0xB1>(v);                                      // quad_perm [1,0,3,2]
     v += dpp<0x4E>(v);                                      // quad_perm [2,3,0,1]
     if constexpr (LANES >= 8) v += dpp<0x141>(v);           // row_half_mirror
@@ -39,11 +55,11 @@ template <int LANES> __device__ __forceinline__ float part_sum(float v) {
     return v;
 }
 // the sum over a wave's lanes, in every lane
-__device__ __forceinline__ float lane_sum(float v) {
+template <typename T> __device__ __forceinline__ T lane_sum(T v) {
     v = part_sum<16>(v);
     v += dpp<0x142, 0xA>(v);                                // row_bcast:15 into rows 1 and 3
     v += dpp<0x143, 0xC>(v);                                // row_bcast:31 into rows 2 and 3
-    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+    return last_lane(v);
 }
 
 // Sums of N values over the lanes of a row: one wave (NW = 0), or a workgroup of
@@ -53,7 +69,7 @@ __device__ __forceinline__ float lane_sum(float v) {
 // takes 4 additions, where all of them in every lane took 15, a tenth of the
 // instructions of a row of 7168.
 constexpr int sum_words(int nw) { return nw <= 4 ? 4 : nw <= 8 ? 8 : 16; }
-template <int NW, int N> __device__ __forceinline__ void row_sums(float (&v)[N], float* lds) {
+template <int NW, int N, typename T> __device__ __forceinline__ void row_sums(T (&v)[N], T* lds) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = lane_sum(v[i]);
     if constexpr (NW > 0) {
@@ -67,14 +83,16 @@ template <int NW, int N> __device__ __forceinline__ void row_sums(float (&v)[N],
     }
 }
 // before the first of them, by every thread
-template <int WORDS> __device__ __forceinline__ void clear_sums(float* lds) {
-    for (int i = (int)threadIdx.x; i < WORDS; i += (int)blockDim.x) lds[i] = 0.0f;
+template <int WORDS, typename T> __device__ __forceinline__ void clear_sums(T* lds) {
+    for (int i = (int)threadIdx.x; i < WORDS; i += (int)blockDim.x) lds[i] = T(0);
     __syncthreads();
 }
 
 // s / n from rn = 1 / n: exact where the quotient is a binary32 number, so that a
 // constant row, whose d are equal and add up exactly, has y = b to the last bit (and
-// zeros in a cast, whose scale would show whatever is left)
+// zeros in a cast, whose scale would show whatever is left).  They add up exactly in
+// rows held in registers: d is at most 2^6 units of h's last place there, of at most
+// 2^15 columns.
 __device__ __forceinline__ float mean_of(float s, float n, float rn) {
     const float q = s * rn;
     return __builtin_fmaf(__builtin_fmaf(-q, n, s), rn, q);
@@ -285,45 +303,54 @@ __device__ __forceinline__ void put_y(const LayerNorm& a, int64_t row, int c, co
 
 // Rows too long for registers, or shorter than a vector: passes over the row, the later ones mostly from
 // cache.  h and y are written in the last pass, after a lane's own reads of the
-// same columns, so that they may be x or the residual itself.
+// same columns, so that they may be x or the residual itself.  The mean is a
+// binary64 sum's, in the two halves m0 + m1: of a constant row of so many columns
+// the differences from a binary32 m0 need not add up exactly (they did not in a
+// quarter of such rows of 10^6, and a cast without a bias scales what is left to
+// full range).  It costs 2 to 7 % where the row's reductions are the time (20000 x 5
+// bf16 320 us against 312, 1 x 40960 9.8 / 9.2) and nothing where the bytes are
+// (512 x 40960 with residual 56.9 / 56.8).
 template <int DT, bool WF32, int FMT, int TO> __global__ void __launch_bounds__(1024) k_ln_long(LayerNorm a) {
     constexpr int VE = LaneVE<DT>::value, ES = ESize<DT>::value;
-    __shared__ float lds_s[48];
+    __shared__ double lds_s[16];
+    __shared__ float lds_q[16];
     __shared__ uint32_t lds_m[16];
-    clear_sums<48>(lds_s);
+    clear_sums<16>(lds_s);
+    clear_sums<16>(lds_q);
     const int cols = (int)a.cols, step = (int)blockDim.x * VE, c0 = (int)threadIdx.x * VE;
-    const float fc = (float)cols, rn = 1.0f / fc;
+    const double rn64 = 1.0 / (double)cols;
+    const float rn = (float)rn64;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t off = row * a.cols * ES;
         const void* xr = (const char*)a.x + off;
         const void* rr = a.res ? (const char*)a.res + off : nullptr;
-        float s[1] = {0.0f};
+        double s[1] = {0.0};
         for (int64_t c = c0; c < cols; c += step) {
             float h[VE];
             load_h<DT>(xr, rr, (int)c, cols, h);
+            double p = 0.0;
 #pragma unroll
-            for (int k = 0; k < VE; ++k) s[0] += h[k];
+            for (int k = 0; k < VE; k += 2) p += (double)h[k] + (double)h[k + 1];
+            s[0] += p;
         }
         row_sums<16>(s, lds_s);
-        const float m0 = s[0] * rn;
+        const double mean = s[0] * rn64;
+        const float m0 = (float)mean, m1 = (float)(mean - (double)m0);
         // d of the columns from c on, zero past the row's end
         auto diff = [&](int64_t c, float* d) {
             load_h<DT>(xr, rr, (int)c, cols, d);
 #pragma unroll
             for (int k = 0; k < VE; ++k) d[k] = c + k < cols ? d[k] - m0 : 0.0f;
         };
-        float d2[2] = {0.0f, 0.0f};
+        float d2[1] = {0.0f};
         for (int64_t c = c0; c < cols; c += step) {
             float d[VE];
             diff(c, d);
 #pragma unroll
-            for (int k = 0; k < VE; ++k) {
-                d2[0] += d[k];
-                d2[1] = __builtin_fmaf(d[k], d[k], d2[1]);
-            }
+            for (int k = 0; k < VE; ++k) d2[0] = __builtin_fmaf(d[k], d[k], d2[0]);
         }
-        row_sums<16>(d2, lds_s + 16);
-        const float m1 = mean_of(d2[0], fc, rn), rs = rstd_of(d2[1], m1, rn, a.eps);
+        row_sums<16>(d2, lds_q);
+        const float rs = rstd_of(d2[0], m1, rn, a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;

@@ -43,8 +43,10 @@ extern "C" {
  * weight, bias: [cols] of wdtype, which is xdtype or FP8Q_F32 (else
  * FP8Q_EDTYPE); bias may be NULL.  mean, rstd: [rows] floats, or NULL.
  * The mean is taken twice, the second time of the differences from the first,
- * so that rows far from zero lose nothing but h's own rounding.  Sums are
- * binary32: a row whose sum passes 3.4e38 gets NaN, and one whose differences
+ * so that rows far from zero lose nothing but h's own rounding, and a constant
+ * row has y = bias.  (Of rows too long for registers, past 32768 16-bit or 16384
+ * binary32 columns, and of rows under 16 bytes, it is a binary64 sum's.)  Sums are
+ * binary32: a row whose sum passes 3.4e38 may get NaN, and one whose differences
  * pass 1.8e19 gets rstd = 0, as an infinite variance gives it.  Short rows are
  * summed in another order where there are more than 256 of them.
  * rows == 0 is a no-op; cols == 0 is a no-op except that the per-channel form
