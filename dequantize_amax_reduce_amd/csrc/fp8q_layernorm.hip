@@ -13,7 +13,8 @@
 //
 // The mean is m0 + m1: m0 the rounded mean of h, m1 the mean of d = h - m0,
 // which is exact where h is near m0; the variance is mean(d^2) - m1^2.  So a
-// row of values far from zero keeps the bits that its deviations have in h.
+// row of values far from zero keeps the bits that its deviations have in h (and m1
+// is left out where it would add roundings instead: second_mean).
 // (With m0 alone a constant row of 1000s, whose y is b, would be off by what
 // m0's rounding leaves: 6e-5 / sqrt(eps), 2 % of the weight at eps = 1e-5.)
 // Rows too long for registers have m0 + m1 from a binary64 sum.
@@ -96,6 +97,16 @@ template <int WORDS, typename T> __device__ __forceinline__ void clear_sums(T* l
 __device__ __forceinline__ float mean_of(float s, float n, float rn) {
     const float q = s * rn;
     return __builtin_fmaf(__builtin_fmaf(-q, n, s), rn, q);
+}
+
+// m1 of a row held in registers, from the sum of d and q = mean(d^2): 0 where the
+// deviation is over 4 |m0|.  There m0 is within a few of its own roundings (16-bit
+// rows sum without any), while each d has one of the deviation's size, whose mean
+// beside a small m0 would be all that shows: 4e-6 of it for 1 in 100 rows of 7168
+// around zero, against 2e-7.  Squares under 2^-100 or past binary32 tell nothing.
+__device__ __forceinline__ float second_mean(float s, float m0, float q, float n, float rn) {
+    const float t = __builtin_fmaf(-16.0f * m0, m0, q);
+    return t >= 0x1p-100f && t <= 3.4028234663852886e38f ? 0.0f : mean_of(s, n, rn);
 }
 
 // rstd from the sum of d^2 and the mean of d, rn = 1 / n (a NaN passes the clamp).
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
             d2[1] += WHOLE && dup[v] ? 0.0f : q;
         }
         row_sums<NW>(d2, lds_s + SW);
-        const float m1 = mean_of(d2[0], fc, rn), rs = rstd_of(d2[1], m1, rn, a.eps);
+        const float m1 = second_mean(d2[0], m0, d2[1] * rn, fc, rn), rs = rstd_of(d2[1], m1, rn, a.eps);
         if (t == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;

@@ -1,13 +1,48 @@
 """GPU: bits that layer norm and projections with an epilogue have to keep
-(include/fp8q_mlp.h): constant rows of 10^6 columns."""
+(include/fp8q_mlp.h): the mean of rows around zero, constant rows of 10^6
+columns."""
 import pytest
 import torch
 
 import dequantize_amax_reduce_amd as fq
 from gpu_util import TORCH_HP
-from test_gpu_ffn import gen_of, rand
+from test_gpu_ffn import D, gen_of, rand, up
+from test_gpu_layernorm import U
 
 pytestmark = pytest.mark.gpu
+
+
+# rows of a wave (1 and 2 vectors), of a workgroup (1, 2 and 4), in passes, shorter than a vector
+WIDTHS = [(300, 256, "bf16"), (300, 1001, "f16"), (300, 500, "f32"), (70, 7168, "bf16"), (40, 5001, "f32"),
+          (20, 12001, "bf16"), (10, 32768, "f16"), (10, 40001, "bf16"), (10, 20000, "f32"), (50, 5, "bf16"), (50, 3, "f32")]
+
+
+@pytest.mark.parametrize("rows,cols,dt", WIDTHS)
+@pytest.mark.parametrize("res", [False, True])
+def test_mean_of_rows_around_zero(rows, cols, dt, res):
+    """x and residual are multiples of 2^-6 under 2, so that a row's sum has at most
+    24 bits in any order: the mean has the rounding of a quotient alone, two
+    where it is a product by the rounded 1 / n.  (Differences from it, each
+    rounded, would add 2^-24 of the deviation to a mean 100 times smaller.)"""
+    g = gen_of("mean", rows, cols, dt, res)
+    units = lambda: torch.randint(-127, 128, (rows, cols), generator=g).float()
+    a, r = units(), units()
+    for t in (a, r):                                        # the last row sums to zero: its mean is zero
+        n = cols // 2
+        t[-1, n:2 * n] = -t[-1, :n]
+        t[-1, 2 * n:] = 0.0
+    T = TORCH_HP[dt]
+    x, r = (a * 2.0 ** -6).to(T), (r * 2.0 ** -6).to(T)
+    h = x.to(D) + (r.to(D) if res else 0)
+    mean, var = h.mean(1), h.var(1, correction=0)
+    _, _, m, _ = fq.layernorm(up(x), up(torch.ones(cols, dtype=T)), None, up(r) if res else None)
+    err = (m.cpu().to(D) - mean).abs()
+    inside = 16 * mean.square() < 0.99 * var                # further out the mean is held to the row's bound
+    size = cols * a.new_empty(0, dtype=T).element_size()
+    inside |= not 16 <= size <= 65536                       # (rows in passes: a binary64 sum's)
+    assert inside.sum() > rows // 2
+    assert (err <= 2.01 * U * mean.abs())[inside].all(), float((err / mean.abs().clamp_min(1e-30))[inside].max() / U)
+    assert float(m[-1]) == 0.0
 
 
 @pytest.mark.parametrize("cols,dt", [(500001, "f32"), (1000003, "f32"), (1 << 20, "f32"), (1000003, "bf16")])
