@@ -109,10 +109,11 @@ __device__ __forceinline__ float second_mean(float s, float m0, float q, float n
     return t >= 0x1p-100f && t <= 3.4028234663852886e38f ? 0.0f : mean_of(s, n, rn);
 }
 
-// rstd from the sum of d^2 and the mean of d, rn = 1 / n (a NaN passes the clamp).
+// rstd from q = mean(d^2) and the mean of d (a NaN passes the clamp).  An infinite q
+// stays infinite beside any finite m1 (whose square may be, and would leave NaN).
 // The instruction is within 2^-23 and takes subnormal values as 0.
-__device__ __forceinline__ float rstd_of(float s2, float m1, float rn, float eps) {
-    float v = s2 * rn - m1 * m1;
+__device__ __forceinline__ float rstd_of(float q, float m1, float eps) {
+    float v = __builtin_fmaf(-m1, m1, q);
     v = (v < 0.0f ? 0.0f : v) + eps;
     const bool tiny = v < 0x1p-100f;
     const float r = __builtin_amdgcn_rsqf(tiny ? v * 0x1p100f : v);
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
             d2[1] += WHOLE && dup[v] ? 0.0f : q;
         }
         row_sums<NW>(d2, lds_s + SW);
-        const float m1 = second_mean(d2[0], m0, d2[1] * rn, fc, rn), rs = rstd_of(d2[1], m1, rn, a.eps);
+        const float ms = d2[1] * rn, m1 = second_mean(d2[0], m0, ms, fc, rn), rs = rstd_of(ms, m1, a.eps);
         if (t == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;
@@ -361,7 +362,7 @@ template <int DT, bool WF32, int FMT, int TO> __global__ void __launch_bounds__(
             for (int k = 0; k < VE; ++k) d2[0] = __builtin_fmaf(d[k], d[k], d2[0]);
         }
         row_sums<16>(d2, lds_q);
-        const float rs = rstd_of(d2[0], m1, rn, a.eps);
+        const float rs = rstd_of(d2[0] * rn, m1, a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = m0 + m1;
             if (a.rstd) a.rstd[row] = rs;

@@ -1,6 +1,6 @@
 """GPU: bits that layer norm and projections with an epilogue have to keep
-(include/fp8q_mlp.h): the mean of rows around zero, constant rows of 10^6
-columns."""
+(include/fp8q_mlp.h): the mean of rows around zero, rows whose squares pass
+binary32, constant rows of 10^6 columns."""
 import pytest
 import torch
 
@@ -43,6 +43,27 @@ def test_mean_of_rows_around_zero(rows, cols, dt, res):
     assert inside.sum() > rows // 2
     assert (err <= 2.01 * U * mean.abs())[inside].all(), float((err / mean.abs().clamp_min(1e-30))[inside].max() / U)
     assert float(m[-1]) == 0.0
+
+
+@pytest.mark.parametrize("cols", [3, 256, 701, 5001, 7168, 16384, 20000, 33333])
+@pytest.mark.parametrize("rows", [6, 300])
+def test_rows_whose_squares_pass_binary32(rows, cols):
+    """One element, or every one, of 1e27 to 1e35: the mean square of the
+    differences is infinite, so that rstd is 0 and y the bias.  A constant row of
+    1e30 has no differences, or infinite squares of its mean's roundings: y is
+    the bias too, and the mean is its value."""
+    g = gen_of("squares", rows, cols)
+    x = 256 * rand(g, rows, cols)
+    at = cols // 3
+    x[0, at], x[1, at], x[2, at] = 1e30, -1e35, 1e27
+    x[3], x[4] = 1e30 * rand(g, cols), 1e35 * rand(g, cols)
+    x[5] = 1e30
+    w, b = 1 + rand(g, cols), rand(g, cols)
+    y, _, mean, rstd = fq.layernorm(up(x), up(w), up(b))
+    assert (rstd[:5] == 0).all() and torch.isfinite(mean).all()
+    assert torch.equal(y[:6].cpu(), b.expand(6, cols))
+    assert abs(float(mean[5].cpu().to(D) / x[5, 0].to(D)) - 1) <= 2 * U
+    assert torch.isfinite(y).all()
 
 
 @pytest.mark.parametrize("cols,dt", [(500001, "f32"), (1000003, "f32"), (1 << 20, "f32"), (1000003, "bf16")])
