@@ -17,17 +17,19 @@ namespace {
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Sums are binary32 where an output shows them: a binary32 y or z, or a cast
-// with its scales.  Unlike a plain projection's, 16-bit outputs of 17 to 64 rows
-// take the fp8 instruction too (48 rows 18432 -> 7168: 25.4 us against 28.8).
-bool exact_sums(const MmFwd& f) { return f.q || (f.y && f.ydt == kF32) || (f.z && f.zdt == kF32); }
+// Sums are binary32 where an output shows them (a binary32 y or z, or a cast with
+// its scales), and of up to 64 rows, as fp8q_linear's are: the weights' bytes bound
+// those, and the fp8 instruction would take 3 us off 48 rows 18432 -> 7168 (28.8).
+bool exact_sums(const MmFwd& f) {
+    return f.M <= kExactMax || f.q || (f.y && f.ydt == kF32) || (f.z && f.zdt == kF32);
+}
 
 }  // namespace
 
 // enough for either kind of sum: the output types are not known here
 int64_t mm_act_workspace(int64_t M, int64_t N, int64_t K, bool cast) {
     int64_t most = 0;
-    for (int ex = cast ? 1 : 0; ex < 2; ++ex) {
+    for (int ex = cast || M <= kExactMax ? 1 : 0; ex < 2; ++ex) {
         const Plan p = plan_act(M, N, K, ex).p;
         most = std::max(most, p.rows ? (cast ? M * N * 4 : 0) : up256(part_bytes(p, M, N, false)));
     }

@@ -9,12 +9,12 @@
  * call, no allocation, no state kept, the same limits and workspaces), and the
  * calling thread's current device is the one that holds the tensors.
  *
- * Numerics are those of fp8q_ffn.h but for one thing: a projection whose outputs
- * are all 16-bit uses the fp8 instruction from 17 rows on (fp8q_linear from 65),
- * which adds a step's products within about 16 bits of the largest.  A binary32
- * y or z, a cast, and up to 16 rows have binary32 sums.  A row's result does not
- * depend on what the other rows hold; its last bits may depend on how many there
- * are, which choose the tiles and the splits of a contraction.
+ * Numerics are those of fp8q_ffn.h: a projection of more than 64 rows whose outputs
+ * are all 16-bit uses the fp8 instruction, which adds a step's products within
+ * about 16 bits of the largest; a binary32 y or z, a cast, and up to 64 rows have
+ * binary32 sums.  A row's result does not depend on what the other rows hold; its
+ * last bits may depend on how many there are, which choose the tiles and the splits
+ * of a contraction.
  */
 #ifndef FP8Q_MLP_H
 #define FP8Q_MLP_H

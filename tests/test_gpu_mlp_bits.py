@@ -1,12 +1,13 @@
 """GPU: bits that layer norm and projections with an epilogue have to keep
 (include/fp8q_mlp.h): the mean of rows around zero, rows whose squares pass
-binary32, constant rows of 10^6 columns."""
+binary32, constant rows of 10^6 columns; the sums of projections of 17
+to 64 rows and of more."""
 import pytest
 import torch
 
 import dequantize_amax_reduce_amd as fq
 from gpu_util import TORCH_HP
-from test_gpu_ffn import D, gen_of, rand, up
+from test_gpu_ffn import D, FP8, codes, gen_of, rand, up, w64, x64
 from test_gpu_layernorm import U
 
 pytestmark = pytest.mark.gpu
@@ -80,3 +81,58 @@ def test_constant_rows_of_a_million(cols, dt):
     assert torch.equal(mean.cpu(), v[:, 0].float())
     q, s, _, _, _ = fq.layernorm_cast(x, w, None, per_channel_scale=True)
     assert (q.float() == 0).all() and (s == torch.tensor(1.0) / 448).all()
+
+
+@pytest.mark.parametrize("M", [17, 33, 48, 64])
+@pytest.mark.parametrize("K,N", [(128, 72), (1152, 200), (7168, 61), (2048, 4104)])
+@pytest.mark.parametrize("dt,xf,wf,res", [("bf16", "e4m3fn", "e4m3fn", False), ("f16", "e5m2", "e4m3fn", True)])
+def test_sums_up_to_64_rows_are_binary32(M, K, N, dt, xf, wf, res):
+    """In every 128-block two products of 448^2 cancel beside 126 of 1/2, at
+    places that differ from block to block, and scales are powers of two: all
+    partial sums are multiples of a half, or of scales times it, of at most 24
+    bits, so binary32 sums have no rounding in any order.  (Sums that keep 16
+    bits below a block's largest product lose the halves.)"""
+    g = gen_of("binary32", M, K, N)
+    KB = K // 128
+    x, w = torch.ones(M, K), torch.full((N, K), 0.5)
+    for kb in range(KB):
+        i, j = (kb * 128 + torch.randperm(128, generator=g)[:2]).tolist()
+        x[:, i], x[:, j], w[:, i], w[:, j] = 448.0, 448.0, 448.0, -448.0
+    xq, wq = x.to(FP8[xf]), w.to(FP8[wf])
+    xs = 2.0 ** torch.randint(-2, 1, (M, KB), generator=g).float()
+    ws = 2.0 ** torch.randint(-2, 1, ((N + 127) // 128, KB), generator=g).float()
+    z = x64(xq, xs) @ w64(wq, ws).t()
+    assert torch.equal(z, 63 * xs.to(D) @ ws.to(D).repeat_interleave(128, dim=0)[:N].t())
+    T = TORCH_HP[dt]
+    r = torch.randint(-64, 65, (M, N), generator=g).to(T) if res else None
+    y, kept = fq.linear_act_fp8(up(xq), up(xs), up(wq), up(ws), None, None, None if r is None else up(r), T, keep=T)
+    assert torch.equal(kept.cpu(), z.to(T)) and torch.equal(y.cpu(), (z + (0 if r is None else r.to(D))).to(T))
+    if not res:                                             # and as a bare projection has them
+        assert torch.equal(y, fq.linear_fp8(up(xq), up(xs), up(wq), up(ws), out=torch.empty_like(y)))
+
+
+@pytest.mark.parametrize("M,K,N", [(65, 640, 72), (100, 4096, 264), (300, 7168, 300), (1003, 2048, 200), (1000, 512, 4101)])
+@pytest.mark.parametrize("keep", [False, True])
+def test_fp8_sums_keep_their_bits(M, K, N, keep):
+    """16-bit outputs of more than 64 rows: 16 bits are kept below the largest
+    product of 128, so a product is off by 2^-16 / sqrt 3 of it in root mean
+    square and a block's sum by sqrt(128) times that: 2^-13.1 of the root of the
+    sum of squared products, r, of which the largest is a part.  So f16 outputs
+    are within 2^-13 r, in root mean square, of their own rounding, and none is
+    further off than 2^-10 r and half a unit in its last place."""
+    g = gen_of("act bits", M, K, N)
+    xq, xs = codes(g, M, K, "e4m3fn", M)
+    wq, ws = codes(g, N, K, "e4m3fn", (N + 127) // 128)
+    X, W = x64(xq, xs) * 2.0 ** -4, w64(wq, ws)             # no f16 overflow
+    want = X @ W.t()
+    assert float(want.abs().max()) < 65504
+    H = torch.float16
+    y, z = fq.linear_act_fp8(up(xq), up(xs * 2.0 ** -4), up(wq), up(ws), ret_type=H, keep=H if keep else None)
+    r = torch.sqrt((X * X) @ (W * W).t())
+    live = r > 2.0 ** -8                                     # f16's subnormals are no matter here; zero rows
+    rms = lambda v: float(v.square().mean().sqrt())
+    for got in (y, z) if keep else (y,):
+        got = got.cpu().to(D)
+        e, rounding = ((got - want) / r)[live], ((want.half().to(D) - want) / r)[live]
+        assert rms(e) <= rms(rounding) + 2.0 ** -13
+        assert ((got - want).abs() <= r * 2.0 ** -10 + want.abs() * 2.0 ** -11 + 2.0 ** -25).all()
