@@ -369,7 +369,9 @@ def linear_act_fp8_backward(dy, z, x, x_scale_inv, w, w_scale_inv, activation=No
     """(dx, dw, dbias) of linear_act_fp8 and of linear_act_fp8_cast from dy and
     the forward's z (None without an activation), dx in dy's dtype (bf16 or
     f16), dw and dbias in grad_type (dy's dtype by default, or float32); dbias is
-    None with with_bias=False.  The residual's gradient is dy itself."""
+    None with with_bias=False.  The residual's gradient is dy itself.  `out`:
+    those three, caller-allocated, or None for one that is not computed (dw of
+    frozen weights)."""
     if out is not None:
         dx, dw, db = out
     else:

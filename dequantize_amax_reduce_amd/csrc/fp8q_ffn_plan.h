@@ -223,6 +223,18 @@ inline double time16(const Plan16& p, int64_t M, int64_t N) {
     return (double)((tiles + 255) / 256) * ((double)p.kper * each16(p.bm) + 4.0) +
            (p.splits > 1 ? 3.0 + (double)(p.splits * M * N * 8) / 5e6 : 0.0);
 }
+// One product of a joint launch, asked for without the other: the height of its own
+// least time for M x N outputs of `steps` steps.  Unsplit as in the joint launch, so
+// that a gradient has the same bits with and without the other.  (dx of 2048 x 4096 ->
+// 4096 114.9 us at the joint launch's height, 86.7 so; dw of 1000 x 5120 -> 640 41.9 / 34.2.)
+inline Plan16 alone16(int64_t M, int64_t N, int64_t steps) {
+    Plan16 p{256, 1, (int)steps, 0};
+    for (int h : {192, 128, 64}) {
+        const Plan16 alt{h, 1, (int)steps, 0};
+        if (time16(alt, M, N) < time16(p, M, N)) p = alt;
+    }
+    return p;
+}
 inline PlanBwd plan_bwd_act(int64_t M, int64_t N, int64_t K, bool rest) {
     const int64_t C = dz_columns(N, false, rest), R = rows_padded(M, rest);
     const int64_t s1 = (rest ? C + C / 2 : C) / 64, s2 = (rest ? R + R / 2 : R) / 64;   // steps

@@ -881,13 +881,18 @@ int64_t bias_rows(int64_t M) { return (M + 127) / 128 * 2; }  // sums of 64 rows
 // partial sums of dbias (bias: [bias_rows(M)][N] floats, or nullptr); sizes > 0
 void run_bwd(const MmBwd& f, int mode, bool act, float* bias, hipStream_t st) {
     const bool gated = mode == kOfGated, rest = has_rest(f.dt, mode);
-    const PlanBwd plan = plan_of(f.M, f.N, f.K, gated, rest, act);
+    PlanBwd plan = plan_of(f.M, f.N, f.K, gated, rest, act);
     const BwdLayout l = layout(f.M, f.N, f.K, gated, rest, plan);
     char* ws = (char*)f.ws;
     char *dz = ws + l.dz, *dzt = ws + l.dzt, *wt = ws + l.wt, *xt = ws + l.xt;
     float* part = (float*)(ws + l.part);
     const int KB = f.K / 128;
     const bool wdx = f.dx != nullptr, wdw = f.dw0 != nullptr;
+    if (plan.both && !(wdx && wdw)) {
+        plan.dx = alone16(f.M, f.K, plan.dx.kper);
+        plan.dw = alone16(f.N, f.K, plan.dw.kper);
+        plan.both = false;
+    }
     const int nb = (f.N + 127) / 128;
     float *sx = (float*)(ws + l.sx), *sw = (float*)(ws + l.sw);
     uint32_t *krow = (uint32_t*)(ws + l.krow), *kcol = (uint32_t*)(ws + l.kcol), *kx = (uint32_t*)(ws + l.kx),
@@ -929,7 +934,7 @@ void run_bwd(const MmBwd& f, int mode, bool act, float* bias, hipStream_t st) {
     const Mm16Args ax = mm16_args(dz, wt, f.M, f.K, l.C, rest, f.dx, nullptr, f.M, f.M, f.dt, plan.dx, krow, kw, qw, part);
     const Mm16Args aw = mm16_args(dzt, xt, gated ? l.Np + f.N : f.N, f.K, l.Mp, rest, f.dw0, gated ? f.dw1 : nullptr, f.N,
                                   gated ? l.Np : f.N, f.dwdt, plan.dw, kcol, kx, qx, part);
-    if (plan.both && wdx && wdw) return mm16_two(ax, aw, plan.dx.bm, rest, st);
+    if (plan.both) return mm16_two(ax, aw, plan.dx.bm, rest, st);
     if (wdx) mm16(ax, plan.dx.bm, rest, st);
     if (wdw) mm16(aw, plan.dw.bm, rest, st);
 }

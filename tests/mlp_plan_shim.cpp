@@ -32,3 +32,13 @@ extern "C" void shim_bwd_act(int64_t M, int64_t N, int64_t K, int rest, int64_t*
     }
     *o = p.both;
 }
+
+// rows a tile of dx and of dw where a joint launch's products are asked for alone
+extern "C" void shim_bwd_alone(int64_t M, int64_t N, int64_t K, int rest, int64_t* o) {
+    const fp8q::PlanBwd p = fp8q::plan_bwd_act(M, N, K, rest != 0);
+    o[0] = fp8q::alone16(M, K, p.dx.kper).bm;
+    o[1] = fp8q::alone16(N, K, p.dw.kper).bm;
+}
+extern "C" double shim_time16(int64_t M, int64_t N, int64_t steps, int bm) {
+    return fp8q::time16(fp8q::Plan16{bm, 1, (int)steps, 0}, M, N);
+}

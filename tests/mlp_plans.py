@@ -69,6 +69,18 @@ BACKWARD_REST = {
     (3000, 128, 4104): ((64, 4, 25), (128, 4, 18), False),
 }
 
+# (M, K, N) whose gradients one launch has: rows a tile of dx and of dw, each without the other
+ALONE = {
+    (130, 128, 130): (64, 64),
+    (65, 4736, 834): (64, 128),
+    (811, 4992, 65): (128, 64),
+    (257, 4992, 1580): (64, 192),
+    (1713, 4992, 339): (192, 64),
+    (1000, 5120, 640): (128, 64),
+    (2048, 4096, 4096): (128, 256),
+}
+ALONE_REST = {(64, 128, 65): (64, 64), (129, 4992, 787): (64, 128), (887, 4736, 138): (128, 64), (2048, 4096, 4096): (128, 256)}
+
 # (M, K, N, binary32 sums): (rows a tile, splits, blocks a split, column tiles of
 # 256, narrower ones, their width / 64) of a projection with an epilogue; a
 # pipeline has 3 stages (2 of 256 rows), and one block more is its steady step
@@ -96,7 +108,7 @@ class MlpPlans:
                         os.path.join(ROOT, "tests", "mlp_plan_shim.cpp"), "-o", lib], check=True)
         self.lib = ctypes.CDLL(lib)
 
-        self.lib.shim_mixed_rounds.restype = ctypes.c_double
+        self.lib.shim_mixed_rounds.restype = self.lib.shim_time16.restype = ctypes.c_double
 
     def layernorm(self, rows, cols, dt):
         out = (ctypes.c_int64 * 4)()
@@ -116,3 +128,11 @@ class MlpPlans:
         out = (ctypes.c_int64 * 7)()
         self.lib.shim_bwd_act(*(ctypes.c_int64(v) for v in (M, N, K)), ctypes.c_int(rest), out)
         return tuple(out)[:3], tuple(out)[3:6], bool(out[6])
+
+    def alone(self, M, K, N, rest):
+        out = (ctypes.c_int64 * 2)()
+        self.lib.shim_bwd_alone(*(ctypes.c_int64(v) for v in (M, N, K)), ctypes.c_int(rest), out)
+        return tuple(out)
+
+    def time16(self, M, N, steps, bm):
+        return self.lib.shim_time16(*(ctypes.c_int64(v) for v in (M, N, steps)), ctypes.c_int(bm))

@@ -1,12 +1,13 @@
 """GPU: bits that layer norm and projections with an epilogue have to keep
 (include/fp8q_mlp.h): the mean of rows around zero, rows whose squares pass
 binary32, constant rows of 10^6 columns; the sums of projections of 17
-to 64 rows and of more."""
+to 64 rows and of more; gradients asked for alone."""
 import pytest
 import torch
 
 import dequantize_amax_reduce_amd as fq
-from gpu_util import TORCH_HP
+from gpu_util import G, TORCH_HP
+from mlp_plans import ALONE, ALONE_REST
 from test_gpu_ffn import D, FP8, codes, gen_of, rand, up, w64, x64
 from test_gpu_layernorm import U
 
@@ -136,3 +137,20 @@ def test_fp8_sums_keep_their_bits(M, K, N, keep):
         e, rounding = ((got - want) / r)[live], ((want.half().to(D) - want) / r)[live]
         assert rms(e) <= rms(rounding) + 2.0 ** -13
         assert ((got - want).abs() <= r * 2.0 ** -10 + want.abs() * 2.0 ** -11 + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("M,K,N,dt,act", [(*s, *t) for s in ALONE for t in (("bf16", "gelu"), ("f16", None))] +
+                         [(*s, "f16", "silu") for s in ALONE_REST])
+def test_one_gradient_alone(M, K, N, dt, act):
+    """dx without dw and dw without dx run in tiles of their own: the same bits"""
+    g = gen_of("alone", M, K, N)
+    xq, xs = codes(g, M, K, "e4m3fn", M)
+    wq, ws = codes(g, N, K, "e4m3fn", (N + 127) // 128)
+    dy, z = (0.05 * rand(g, M, N)).to(TORCH_HP[dt]), (2 * rand(g, M, N)).to(TORCH_HP[dt])
+    args = (up(dy), None if act is None else up(z), up(xq), up(xs), up(wq), up(ws))
+    out = fq.linear_act_fp8_backward(*args, act)
+    scratch = G.empty(fq.fp8q_linear_act_backward_workspace_bytes(M, N, K), dtype=torch.uint8)
+    for i in range(3):
+        o = [torch.empty_like(t) if j == i else None for j, t in enumerate(out)]
+        fq.fp8q_linear_act_backward(*args, *o, act, scratch)
+        assert torch.equal(o[i], out[i]), i

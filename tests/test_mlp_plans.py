@@ -8,7 +8,7 @@ import shutil
 import pytest
 
 from ffn_plans import Plans
-from mlp_plans import ACT, BACKWARD, BACKWARD_REST, LAYERNORM, MlpPlans
+from mlp_plans import ACT, ALONE, ALONE_REST, BACKWARD, BACKWARD_REST, LAYERNORM, MlpPlans
 
 
 @pytest.fixture(scope="module")
@@ -110,3 +110,28 @@ def test_mixed_rounds(plans, tmp_path):
         for t in [1.0] * whole + [r] * part:
             heapq.heappush(ends, heapq.heappop(ends) + t)
         assert abs(P.mixed_rounds(whole, part, r) - max(ends)) < 1e-4 * (1 + max(ends)), (whole, part, r)
+
+
+def test_one_gradient_without_the_other(plans, tmp_path):
+    """Of a joint launch's products one alone takes the height of its own least
+    time, which the joint one need not be, unsplit as there."""
+    P = MlpPlans(tmp_path)
+    for rest, table in ((False, ALONE), (True, ALONE_REST)):
+        for key, want in table.items():
+            assert P.backward(*key, rest)[2] and P.alone(*key, rest) == want, key
+    assert {h for v in ALONE.values() for h in v} == {64, 128, 192, 256}
+    rng = random.Random(8)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))
+    both = slower = 0
+    for _ in range(4000):
+        M, K, N, rest = log(32, 5000), 128 * log(1, 60), log(32, 6000), rng.random() < 0.5
+        dx, dw, joint = P.backward(M, K, N, rest)
+        if not joint:
+            continue
+        both += 1
+        for (bm, splits, steps), h, rows in zip((dx, dw), P.alone(M, K, N, rest), (M, N)):
+            assert splits == 1
+            best = min(P.time16(rows, K, steps, b) for b in (64, 128, 192, 256))
+            assert P.time16(rows, K, steps, h) == best
+            slower += P.time16(rows, K, steps, bm) > 1.2 * best
+    assert both > 100 and slower > 50                       # what the joint height would cost
