@@ -9,6 +9,14 @@ extern "C" void shim_layernorm(int64_t rows, int64_t nv, int tiny, int64_t* o) {
     o[3] = p.at_once;
 }
 
+// vectors a thread (0: in passes), threads, workgroups
+extern "C" void shim_layernorm_bwd(int64_t rows, int64_t nv, int64_t* o) {
+    const fp8q::NormPlan p = fp8q::norm_bwd_plan(rows, nv);
+    o[0] = p.V;
+    o[1] = p.threads;
+    o[2] = p.groups;
+}
+
 // rows a tile (0: few rows), splits, blocks of 128 a split, row tiles, column tiles of 256, of 64 nt2, nt2
 extern "C" void shim_act(int64_t M, int64_t N, int64_t K, int ex, int64_t* o) {
     const fp8q::PlanAct a = fp8q::plan_act(M, N, K, ex != 0);

@@ -100,6 +100,24 @@ ACT = {
     (70, 7168, 128, True): (64, 14, 4, 1, 0, 4),
 }
 
+# (rows, columns, dtype) of the norm's backward pass: (vectors a thread, threads, workgroups)
+LAYERNORM_BACKWARD = {
+    (600, 1501, "bf16"): (1, 192, 512),
+    (520, 2048, "f16"): (1, 256, 512),
+    (600, 1001, "f32"): (1, 256, 512),
+    (530, 7168, "f16"): (2, 448, 512),
+    (515, 4101, "bf16"): (2, 320, 512),
+    (600, 4001, "f32"): (2, 512, 512),
+    (600, 8200, "bf16"): (2, 576, 512),
+    (515, 12001, "bf16"): (2, 768, 512),
+    (520, 16384, "f16"): (2, 1024, 512),
+    (600, 5001, "f32"): (2, 640, 512),
+    (515, 8192, "f32"): (2, 1024, 512),
+    (514, 16400, "bf16"): (0, 1024, 512),
+    (514, 16401, "f16"): (0, 1024, 512),
+    (600, 8193, "f32"): (0, 1024, 512),
+}
+
 
 class MlpPlans:
     def __init__(self, folder):
@@ -115,6 +133,11 @@ class MlpPlans:
         self.lib.shim_layernorm(ctypes.c_int64(rows), ctypes.c_int64(vectors(cols, dt)),
                                 ctypes.c_int(cols < (4 if dt == "f32" else 8)), out)
         return (bool(out[0]), *tuple(out)[1:])
+
+    def layernorm_backward(self, rows, cols, dt):
+        out = (ctypes.c_int64 * 3)()
+        self.lib.shim_layernorm_bwd(ctypes.c_int64(rows), ctypes.c_int64(vectors(cols, dt)), out)
+        return tuple(out)
 
     def act(self, M, K, N, exact):
         out = (ctypes.c_int64 * 7)()

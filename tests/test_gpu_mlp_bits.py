@@ -1,13 +1,15 @@
 """GPU: bits that layer norm and projections with an epilogue have to keep
 (include/fp8q_mlp.h): the mean of rows around zero, rows whose squares pass
-binary32, constant rows of 10^6 columns; the sums of projections of 17
-to 64 rows and of more; gradients asked for alone."""
+binary32, constant rows of 10^6 columns; the sums of projections of 17 to 64
+rows and of more; gradients asked for alone; and every instance of the layer
+norm's backward pass over more rows than it has workgroups."""
 import pytest
 import torch
 
 import dequantize_amax_reduce_amd as fq
+import test_gpu_layernorm as L
 from gpu_util import G, TORCH_HP
-from mlp_plans import ALONE, ALONE_REST
+from mlp_plans import ALONE, ALONE_REST, LAYERNORM_BACKWARD
 from test_gpu_ffn import D, FP8, codes, gen_of, rand, up, w64, x64
 from test_gpu_layernorm import U
 
@@ -154,3 +156,11 @@ def test_one_gradient_alone(M, K, N, dt, act):
         o = [torch.empty_like(t) if j == i else None for j, t in enumerate(out)]
         fq.fp8q_linear_act_backward(*args, *o, act, scratch)
         assert torch.equal(o[i], out[i]), i
+
+
+@pytest.mark.parametrize("rows,cols,dt", list(LAYERNORM_BACKWARD))
+@pytest.mark.parametrize("dh,wf32", [(False, False), (True, True)])
+def test_every_instance_of_the_norms_backward(rows, cols, dt, dh, wf32):
+    """more rows than workgroups: the next row's loads, the sums over rows, and
+    dx over dy and over dh"""
+    L.test_backward(rows, cols, dt, dh, wf32)

@@ -8,7 +8,7 @@ import shutil
 import pytest
 
 from ffn_plans import Plans
-from mlp_plans import ACT, ALONE, ALONE_REST, BACKWARD, BACKWARD_REST, LAYERNORM, MlpPlans
+from mlp_plans import ACT, ALONE, ALONE_REST, BACKWARD, BACKWARD_REST, LAYERNORM, LAYERNORM_BACKWARD, MlpPlans
 
 
 @pytest.fixture(scope="module")
@@ -135,3 +135,15 @@ def test_one_gradient_without_the_other(plans, tmp_path):
             assert P.time16(rows, K, steps, h) == best
             slower += P.time16(rows, K, steps, bm) > 1.2 * best
     assert both > 100 and slower > 50                       # what the joint height would cost
+
+
+def test_layernorm_backward_variants(plans, tmp_path):
+    """the sizes that run on the GPU reach every instance, with more rows than workgroups"""
+    plan = MlpPlans(tmp_path).layernorm_backward
+    for key, want in LAYERNORM_BACKWARD.items():
+        assert plan(*key) == want and key[0] > want[2], key
+    # type, vectors a thread, and the size of the workgroup that its launch bounds name
+    got = {(k[2] == "f32", v, t > 512) for k, (v, t, _) in LAYERNORM_BACKWARD.items()}
+    assert got == {(f, v, big) for f in (False, True) for v, big in ((1, False), (2, False), (2, True), (0, True))}
+    # 16-bit rows of the most threads ask for 128 KB of LDS
+    assert max(2 * v * 8 * t * 4 for (_, _, dt), (v, t, _) in LAYERNORM_BACKWARD.items() if dt != "f32") == 128 << 10
