@@ -304,6 +304,7 @@ template <int ACT> __device__ __forceinline__ float unary_value(float z) {
 
 // dy act'(z); the slope is 0 at -infinity and 1 at infinity
 template <int ACT> __device__ __forceinline__ float unary_grad(float dy, float z) {
+    static_assert(ACT != kIdentity, "its slope is 1");
     if constexpr (ACT == kGelu) {
         const Gelu g(z);
         const float q = (0.39894228040143268f * g.x - g.r) * g.e;   // x phi(x) - Phi(-x), over e
@@ -340,17 +341,21 @@ template <int ACT> __device__ __forceinline__ int slope_exponent(float z) {
 }
 
 // f(integral_constant) over a runtime activation; with_unary: those of a
-// projection without a gate
+// projection without a gate; with_slope: those of them whose slope is not 1
 template <typename F> __device__ __forceinline__ void with_act(int act, F&& f) {
     if (act == kSilu) f(std::integral_constant<int, kSilu>{});
     else if (act == kGelu) f(std::integral_constant<int, kGelu>{});
     else f(std::integral_constant<int, kGeluTanh>{});
 }
 
+template <typename F> __device__ __forceinline__ void with_slope(int act, F&& f) {
+    if (act == kRelu) f(std::integral_constant<int, kRelu>{});
+    else with_act(act, f);
+}
+
 template <typename F> __device__ __forceinline__ void with_unary(int act, F&& f) {
     if (act == kIdentity) f(std::integral_constant<int, kIdentity>{});
-    else if (act == kRelu) f(std::integral_constant<int, kRelu>{});
-    else with_act(act, f);
+    else with_slope(act, f);
 }
 
 // ---------------------------------------------------------------------------

@@ -378,11 +378,12 @@ __global__ void __launch_bounds__(256) k_scales(ScaleArgs a) {
 template <int DT, int MODE, bool FULL, bool QUICK>
 __device__ __forceinline__ void dz_values(const uint16_t* dy, const uint16_t* z, int64_t m, int c, int N, int act,
                                           float* g, float* u) {
+    static_assert(MODE != kOfUnary || !QUICK, "the keys of one activation's dz come from bounds on its slope");
     ld8<DT, FULL>(dy + m * N, c, N, g);
     if constexpr (MODE == kOfUnary) {
         float zv[8];
         ld8<DT, FULL>(z + m * N, c, N, zv);
-        with_unary(act, [&](auto A) {
+        with_slope(act, [&](auto A) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const float d = unary_grad<decltype(A)::value>(g[k], zv[k]);
@@ -522,31 +523,31 @@ template <int DT, int MODE> __global__ void __launch_bounds__(256) k_keys(KeyArg
                     const uint32_t kr = max_lanes<16>(top > 0 ? (uint32_t)max(top + ew[0], 0) : 0u);
                     if (v == 0 && a.krow && kr && m0 + (i + r) * 16 + rl < a.M) atomicMax(a.krow + m[r], kr);
                 }
-                continue;
-            }
+            } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                m[r] = m0 + (i + r) * 16 + rl;
-                if (m[r] > a.M - 1) m[r] = a.M - 1;
-                ex[r] = exponent_of(a.sx[m[r]]);
-                dz_values<DT, MODE, decltype(FULL)::value, true>(a.dy, a.z, m[r], c, a.N, a.act, d[r][0], d[r][H - 1]);
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                uint32_t kr = 0;
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t b = finite_bits(d[r][h][k]);
-                        top = umax(top, b);
-                        kc[h][k] = umax(kc[h][k], key_of(b, ex[r]));
-                    }
-                    kr = umax(kr, key_of(top, ew[h]));
+                for (int r = 0; r < R; ++r) {
+                    m[r] = m0 + (i + r) * 16 + rl;
+                    if (m[r] > a.M - 1) m[r] = a.M - 1;
+                    ex[r] = exponent_of(a.sx[m[r]]);
+                    dz_values<DT, MODE, decltype(FULL)::value, true>(a.dy, a.z, m[r], c, a.N, a.act, d[r][0], d[r][H - 1]);
                 }
-                kr = max_lanes<16>(kr);
-                if (v == 0 && a.krow && kr && m0 + (i + r) * 16 + rl < a.M) atomicMax(a.krow + m[r], kr);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    uint32_t kr = 0;
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t b = finite_bits(d[r][h][k]);
+                            top = umax(top, b);
+                            kc[h][k] = umax(kc[h][k], key_of(b, ex[r]));
+                        }
+                        kr = umax(kr, key_of(top, ew[h]));
+                    }
+                    kr = max_lanes<16>(kr);
+                    if (v == 0 && a.krow && kr && m0 + (i + r) * 16 + rl < a.M) atomicMax(a.krow + m[r], kr);
+                }
             }
         }
     };
