@@ -9,7 +9,7 @@
 // written once.  A row stays in registers between its reductions, as binary32.
 // The instructions are close behind: 41 an element (a quarter of them the three sums
 // over the workgroup and their divisions) took 160 to 180 us for 16384 x 7168 as the
-// clock fell under load, 31 take 149.
+// clock fell under load, 32 take 149 to 157.
 //
 // The mean is m0 + m1: m0 the rounded mean of h, m1 the mean of d = h - m0,
 // which is exact where h is near m0; the variance is mean(d^2) - m1^2.  So a
@@ -212,7 +212,9 @@ __global__ void __launch_bounds__(TB, V == 1 ? 8 : 4) k_ln_rows(LayerNorm a) {
     };
     load(first);
     if (NW) clear_sums<3 * SW>(lds_s);
-    constexpr bool HOLD = V <= 1;                           // four vectors leave no registers for them
+    // one vector's weights stay in registers; two and four vectors leave none for theirs
+    // beside the next row's loads (or spill already), and load them again for every row
+    constexpr bool HOLD = V <= 1;
     Affine<DT, WF32> w[V], b[V];
     auto load_wb = [&](int v) {
         w[v].load(a.w, place(v).c);

@@ -444,7 +444,7 @@ __device__ __forceinline__ void mm_tile(const FwdArgs& a, char* smem, int64_t m0
             }
         }
         // A loop for each activation: one body of all three is past what is unrolled.
-        // The 256-row tile spills 33 registers around it, to the GELU's constants,
+        // The 256-row tile spills 34 registers around it, to the GELU's constants,
         // and none inside the loop above.
         with_act(a.act, [&](auto A) {
 #pragma unroll
