@@ -1,8 +1,8 @@
 """GPU: bits that layer norm and projections with an epilogue have to keep
 (include/fp8q_mlp.h): the mean of rows around zero, rows whose squares pass
 binary32, constant rows of 10^6 columns; the sums of projections of 17 to 64
-rows and of more; gradients asked for alone; and every instance of the layer
-norm's backward pass over more rows than it has workgroups."""
+rows and of more; gradients asked for alone, and f16 ones; and every instance of
+the layer norm's backward pass over more rows than it has workgroups."""
 import pytest
 import torch
 
@@ -156,6 +156,23 @@ def test_one_gradient_alone(M, K, N, dt, act):
         o = [torch.empty_like(t) if j == i else None for j, t in enumerate(out)]
         fq.fp8q_linear_act_backward(*args, *o, act, scratch)
         assert torch.equal(o[i], out[i]), i
+
+
+@pytest.mark.parametrize("M,K,N", [(500, 640, 700), (300, 1024, 1000), (1500, 256, 90)])
+def test_f16_gradients_of_a_bare_product(M, K, N):
+    """Without an activation dy is exact in f16 and one operand of a product has one
+    f16 rounding: of independent signs, in the sum the share of its norm that the
+    outputs' own rounding is of theirs.  So sqrt 2 times that in all; a tenth more for
+    the sample."""
+    g = gen_of("bare", M, K, N)
+    xq, xs = codes(g, M, K, "e4m3fn", M)
+    wq, ws = codes(g, N, K, "e4m3fn", (N + 127) // 128)
+    dy = (0.01 * rand(g, M, N)).half()
+    dx, dw, _ = fq.linear_act_fp8_backward(up(dy), None, up(xq), up(xs), up(wq), up(ws))
+    for got, want in ((dx, dy.to(D) @ w64(wq, ws)), (dw, dy.to(D).t() @ x64(xq, xs))):
+        assert float(want.abs().max()) < 65504
+        own = (want.half().to(D) - want).norm()
+        assert (got.cpu().to(D) - want).norm() <= 1.1 * 2 ** 0.5 * own
 
 
 @pytest.mark.parametrize("rows,cols,dt", list(LAYERNORM_BACKWARD))
